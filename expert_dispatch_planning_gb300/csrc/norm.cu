@@ -1,0 +1,400 @@
+// norm.cu -- root-mean-square norm with the residual's addition and its
+// gradient (sm_103a).
+//
+// Forward, one pass over the row: s = x + r stays in registers (fp32), the
+// row's sum of squares gives rstd, v = s * rstd * w is stored as bf16, and
+// its largest magnitude gives the scale of the 8-bit output.  Backward: the
+// row's mean of dy*w*xhat gives dx; dy*xhat is summed over the rows of a
+// block in registers (a thread keeps its columns for all of them), one
+// partial row a block, and a second launch adds the partials in block order,
+// so that the result does not depend on scheduling.
+//
+// Memory bound: every element is read once and written once.  A row belongs
+// to one warp when 32 lanes hold it (H <= 512), else to a whole block with 8,
+// 16 or 32 elements a thread.
+#include <cuda_fp8.h>
+
+#include <cmath>
+
+#include "vec8.cuh"
+
+namespace moe {
+
+constexpr float kE4m3Max = 448.f;
+
+struct NormArgs {
+    const uint16_t* x;
+    const void* residual;
+    const void* weight;
+    int weight_f32;
+    int N, H;
+    float eps;
+    float down, mean;  // a power of two near 1/sqrt(H), and 1/(H down^2): the squares are summed scaled down, so
+                       // that a row overflows only where a mean square does
+    uint16_t* y;
+    void* residual_out;
+    float* rstd;
+    uint8_t* q;
+    float* q_scale;
+};
+
+// Sums (or maxima) over the threads that share a row: a warp, or the block
+// through shared memory.  `buf` holds 32 floats; the leading barrier lets it
+// be used again.
+template <bool WARP, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float t = __shfl_xor_sync(FULL_MASK, v, o);
+        v = MAX ? fmaxf(v, t) : v + t;
+    }
+    if constexpr (!WARP) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+        __syncthreads();
+        const int warps = blockDim.x >> 5;
+        v = (threadIdx.x & 31) < warps ? buf[threadIdx.x & 31] : 0.f;  // maxima are of magnitudes: 0 is neutral
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float t = __shfl_xor_sync(FULL_MASK, v, o);
+            v = MAX ? fmaxf(v, t) : v + t;
+        }
+    }
+    return v;
+}
+
+__device__ __forceinline__ void load_weight8(const void* w, int f32, int c, float (&f)[8]) {
+    if (f32) {
+        const float4* p = reinterpret_cast<const float4*>(w) + 2 * static_cast<int64_t>(c);
+        const float4 a = __ldg(p), b = __ldg(p + 1);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else {
+        unpack8(__ldg(reinterpret_cast<const uint4*>(w) + c), f);
+    }
+}
+
+// RES: 0 no residual, else its element type.
+template <int VPT, bool WARP, int RES>
+__global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_kernel(const NormArgs a) {
+    __shared__ float buf[32];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int lanes = WARP ? 32 : blockDim.x;
+    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= a.N) return;
+    const int nvec = a.H / 8;
+    const int64_t at = row * a.H;
+
+    float s[VPT][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * lanes;
+        if (c < nvec) {
+            load8(a.x + at, c, s[i]);
+            if constexpr (RES != 0) {
+                float r[8];
+                if constexpr (RES == 2) load8(static_cast<const float*>(a.residual) + at, c, r);
+                else load8(static_cast<const uint16_t*>(a.residual) + at, c, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[i][j] += r[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float t = s[i][j] * a.down;
+                ss = fmaf(t, t, ss);
+            }
+        }
+    }
+    ss = row_reduce<WARP, false>(ss, buf);
+    const float rstd = 1.f / sqrtf(fmaf(ss, a.mean, a.eps));
+    if (a.rstd != nullptr && lane == 0) a.rstd[row] = rstd;
+
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * lanes;
+        if (c < nvec) {
+            if constexpr (RES == 2) {
+                if (a.residual_out != nullptr) store8(static_cast<float*>(a.residual_out) + at, c, s[i]);
+            } else if constexpr (RES == 1) {
+                if (a.residual_out != nullptr) store8(static_cast<uint16_t*>(a.residual_out) + at, c, s[i]);
+            }
+            float w[8];
+            load_weight8(a.weight, a.weight_f32, c, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s[i][j] = s[i][j] * rstd * w[j];
+                amax = fmaxf(amax, fabsf(s[i][j]));
+            }
+            if (a.y != nullptr) store8(a.y + at, c, s[i]);
+        }
+    }
+    if (a.q == nullptr) return;
+    amax = row_reduce<WARP, true>(amax, buf);
+    const float scale = amax > 0.f ? amax / kE4m3Max : 1.f / kE4m3Max;
+    if (lane == 0) a.q_scale[row] = scale;
+    // one reciprocal a row; rows so small that it would overflow divide instead
+    const bool tiny = scale < 1e-37f;
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * lanes;
+        if (c < nvec) {
+            uint32_t out[2] = {0u, 0u};
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float2 v = tiny ? make_float2(s[i][j] / scale, s[i][j + 1] / scale)
+                                      : make_float2(s[i][j] * inv, s[i][j + 1] * inv);
+                out[j / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3))
+                              << (16 * ((j / 2) & 1));
+            }
+            *reinterpret_cast<uint2*>(a.q + at + 8 * static_cast<int64_t>(c)) = make_uint2(out[0], out[1]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- backward
+struct NormBackwardArgs {
+    const uint16_t* dy;
+    const void* s;
+    const void* weight;
+    int weight_f32;
+    const float* rstd;
+    const void* ds;
+    int N, H;
+    uint16_t* dx;
+    float* dres;
+    float* partial;  // [gridDim.x][H], or null without dweight
+};
+
+template <int VPT, bool WARP, typename S>
+__global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_backward_kernel(const NormBackwardArgs a) {
+    extern __shared__ float sh[];  // WARP: [warps][H] for the block's sum
+    __shared__ float buf[32];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int lanes = WARP ? 32 : blockDim.x;
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+    const int per_step = WARP ? warps : 1;
+    const int nvec = a.H / 8;
+
+    float w[VPT][8], acc[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * lanes;
+        if (c < nvec) load_weight8(a.weight, a.weight_f32, c, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+    }
+    // rows of a block are consecutive: its partial sum has a fixed order
+    const int64_t steps = (static_cast<int64_t>(a.N) + per_step - 1) / per_step;
+    const int64_t begin = blockIdx.x * steps / gridDim.x, end = (blockIdx.x + 1) * steps / gridDim.x;
+    for (int64_t step = begin; step < end; ++step) {
+        const int64_t row = WARP ? step * per_step + warp : step;
+        if (row >= a.N) break;
+        const int64_t at = row * a.H;
+        const float rstd = __ldg(a.rstd + row);
+        float xhat[VPT][8], t[VPT][8];
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * lanes;
+            if (c < nvec) {
+                load8(a.dy + at, c, t[i]);
+                load8(static_cast<const S*>(a.s) + at, c, xhat[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    xhat[i][j] *= rstd;
+                    acc[i][j] = fmaf(t[i][j], xhat[i][j], acc[i][j]);
+                    t[i][j] *= w[i][j];
+                    dot = fmaf(t[i][j], xhat[i][j], dot);
+                }
+            }
+        }
+        const float mean = row_reduce<WARP, false>(dot, buf) / static_cast<float>(a.H);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * lanes;
+            if (c < nvec) {
+                float d[8];
+                if (a.ds != nullptr) load8(static_cast<const S*>(a.ds) + at, c, d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float v = rstd * (t[i][j] - xhat[i][j] * mean);
+                    d[j] = a.ds != nullptr ? d[j] + v : v;
+                }
+                store8(a.dx + at, c, d);
+                if (a.dres != nullptr) store8(a.dres + at, c, d);
+            }
+        }
+    }
+    if (a.partial == nullptr) return;
+    float* out = a.partial + static_cast<int64_t>(blockIdx.x) * a.H;
+    if constexpr (WARP) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * lanes;
+            if (c < nvec) store8(sh + warp * a.H, c, acc[i]);
+        }
+        __syncthreads();
+        for (int h = threadIdx.x; h < a.H; h += blockDim.x) {
+            float v = 0.f;
+            for (int k = 0; k < warps; ++k) v += sh[k * a.H + h];
+            out[h] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * lanes;
+            if (c < nvec) store8(out, c, acc[i]);
+        }
+    }
+}
+
+// dweight[h] = sum of the blocks' partials: 32 columns a block, 8 rows of
+// threads that each add every 8th partial, joined in shared memory.
+__global__ void __launch_bounds__(256) norm_dweight_kernel(const float* partial, int blocks, int H, float* dweight) {
+    __shared__ float sh[8][33];
+    pdl_wait();
+    pdl_trigger();
+    const int h = blockIdx.x * 32 + threadIdx.x, g = threadIdx.y;
+    float v = 0.f;
+    if (h < H)
+        for (int b = g; b < blocks; b += 8) v += partial[static_cast<int64_t>(b) * H + h];
+    sh[g][threadIdx.x] = v;
+    __syncthreads();
+    if (g == 0 && h < H) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += sh[k][threadIdx.x];
+        dweight[h] = t;
+    }
+}
+
+}  // namespace moe
+
+// ---------------------------------------------------------------- host
+namespace {
+
+constexpr int kMaxH = 32768;  // a row in the registers of 1024 threads
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool float_type(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; }
+
+// chunks of 8 elements a thread, with at most 256 threads a chunk
+int norm_vpt(int H) { return H <= 2048 ? 1 : H <= 8192 ? 2 : 4; }
+int norm_threads(int H) { return (H / 8 + 32 * norm_vpt(H) - 1) / (32 * norm_vpt(H)) * 32; }
+
+template <int VPT, bool WARP>
+int launch_norm(const moe::NormArgs& a, int res, dim3 grid, dim3 block, cudaStream_t stream) {
+    if (res == 0) return moe_host::launch(moe::norm_kernel<VPT, WARP, 0>, grid, block, 0, stream, a);
+    if (res == 1) return moe_host::launch(moe::norm_kernel<VPT, WARP, 1>, grid, block, 0, stream, a);
+    return moe_host::launch(moe::norm_kernel<VPT, WARP, 2>, grid, block, 0, stream, a);
+}
+
+template <int VPT, bool WARP>
+int launch_backward(const moe::NormBackwardArgs& a, bool f32, dim3 grid, dim3 block, size_t smem,
+                    cudaStream_t stream) {
+    if (f32) return moe_host::launch(moe::norm_backward_kernel<VPT, WARP, float>, grid, block, smem, stream, a);
+    return moe_host::launch(moe::norm_backward_kernel<VPT, WARP, uint16_t>, grid, block, smem, stream, a);
+}
+
+// Blocks of the backward kernel: four an SM, no more than there are rows.
+int backward_blocks(int N, int H) {
+    const int64_t units = H <= 512 ? (static_cast<int64_t>(N) + 3) / 4 : N;
+    const int64_t cap = static_cast<int64_t>(moe_host::num_sms()) * 4;
+    return static_cast<int>(units < cap ? units : cap);
+}
+
+}  // namespace
+
+extern "C" MOE_API int moe_residual_norm(const uint16_t* x, const void* residual, int residual_dtype,
+                                         const void* weight, int weight_dtype, int N, int H, float eps, uint16_t* y,
+                                         void* residual_out, float* rstd, uint8_t* q, float* q_scale,
+                                         cudaStream_t stream) {
+    if (N < 0 || H < 8 || H % 8 != 0 || !(eps >= 0.f) || std::isinf(eps)) return MOE_ERR_INVALID_ARG;
+    if (!float_type(weight_dtype) || (residual != nullptr && !float_type(residual_dtype))) return MOE_ERR_INVALID_ARG;
+    if ((q == nullptr) != (q_scale == nullptr) && N > 0) return MOE_ERR_INVALID_ARG;
+    if (N > 0 && (x == nullptr || weight == nullptr || (y == nullptr && q == nullptr))) return MOE_ERR_INVALID_ARG;
+    if (residual == nullptr && residual_out != nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(y) || !aligned16(residual_out) ||
+        (reinterpret_cast<uintptr_t>(rstd) & 3u) != 0 || (reinterpret_cast<uintptr_t>(q) & 7u) != 0 ||
+        (reinterpret_cast<uintptr_t>(q_scale) & 3u) != 0)
+        return MOE_ERR_INVALID_ARG;
+    if (H > kMaxH) return MOE_ERR_UNSUPPORTED;
+    if (N == 0) return MOE_OK;
+    int k = 0;
+    while ((int64_t(1) << (2 * k)) < H) ++k;
+    const float mean = static_cast<float>(static_cast<double>(int64_t(1) << (2 * k)) / H);
+    const moe::NormArgs a = {x, residual, weight,       weight_dtype == MOE_DTYPE_F32, N, H, eps, std::ldexp(1.f, -k),
+                             mean, y,     residual_out, rstd,                          q, q_scale};
+    const int res = residual == nullptr ? 0 : residual_dtype == MOE_DTYPE_F32 ? 2 : 1;
+    if (H <= 512) {
+        const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(N) + 3) / 4)), block(128);
+        return H <= 256 ? launch_norm<1, true>(a, res, grid, block, stream)
+                        : launch_norm<2, true>(a, res, grid, block, stream);
+    }
+    const dim3 grid(static_cast<unsigned>(N)), block(static_cast<unsigned>(norm_threads(H)));
+    switch (norm_vpt(H)) {
+        case 1: return launch_norm<1, false>(a, res, grid, block, stream);
+        case 2: return launch_norm<2, false>(a, res, grid, block, stream);
+        default: return launch_norm<4, false>(a, res, grid, block, stream);
+    }
+}
+
+extern "C" MOE_API size_t moe_residual_norm_backward_workspace_size(int N, int H) {
+    if (N < 0 || H < 8 || H % 8 != 0 || H > kMaxH) return 0;
+    const int blocks = backward_blocks(N, H);
+    return static_cast<size_t>(blocks > 0 ? blocks : 1) * H * sizeof(float);
+}
+
+extern "C" MOE_API int moe_residual_norm_backward(const uint16_t* dy, const void* s, int s_dtype, const void* weight,
+                                                  int weight_dtype, const float* rstd, const void* ds, int N, int H,
+                                                  uint16_t* dx, float* dres, float* dweight, void* workspace,
+                                                  size_t workspace_bytes, cudaStream_t stream) {
+    if (N < 0 || H < 8 || H % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if (!float_type(weight_dtype) || !float_type(s_dtype)) return MOE_ERR_INVALID_ARG;
+    if (N > 0 && (dy == nullptr || s == nullptr || weight == nullptr || rstd == nullptr || dx == nullptr))
+        return MOE_ERR_INVALID_ARG;
+    if (dres != nullptr && s_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(s) || !aligned16(weight) || !aligned16(ds) || !aligned16(dx) ||
+        !aligned16(dres) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(rstd) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(dweight) & 3u) != 0)
+        return MOE_ERR_INVALID_ARG;
+    if (H > kMaxH) return MOE_ERR_UNSUPPORTED;
+    if (dweight != nullptr && N > 0) {
+        if (workspace == nullptr) return MOE_ERR_INVALID_ARG;
+        if (workspace_bytes < moe_residual_norm_backward_workspace_size(N, H)) return MOE_ERR_CAPACITY;
+    }
+    if (N == 0) {
+        if (dweight != nullptr && cudaMemsetAsync(dweight, 0, sizeof(float) * H, stream) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    const int blocks = backward_blocks(N, H);
+    const moe::NormBackwardArgs a = {dy, s, weight, weight_dtype == MOE_DTYPE_F32, rstd, ds, N, H, dx, dres,
+                                     dweight != nullptr ? static_cast<float*>(workspace) : nullptr};
+    const bool f32 = s_dtype == MOE_DTYPE_F32;
+    const dim3 grid(static_cast<unsigned>(blocks));
+    int rc;
+    if (H <= 512) {
+        const dim3 block(128);
+        const size_t smem = 4 * sizeof(float) * H;
+        rc = H <= 256 ? launch_backward<1, true>(a, f32, grid, block, smem, stream)
+                      : launch_backward<2, true>(a, f32, grid, block, smem, stream);
+    } else {
+        const dim3 block(static_cast<unsigned>(norm_threads(H)));
+        switch (norm_vpt(H)) {
+            case 1: rc = launch_backward<1, false>(a, f32, grid, block, 0, stream); break;
+            case 2: rc = launch_backward<2, false>(a, f32, grid, block, 0, stream); break;
+            default: rc = launch_backward<4, false>(a, f32, grid, block, 0, stream); break;
+        }
+    }
+    if (rc != MOE_OK || dweight == nullptr) return rc;
+    return moe_host::launch(moe::norm_dweight_kernel, dim3(static_cast<unsigned>((H + 31) / 32)), dim3(32, 8), 0,
+                            stream, static_cast<const float*>(a.partial), blocks, H, dweight);
+}

@@ -400,6 +400,133 @@ MOE_API int moe_combine(const uint16_t* y, const float* topk_w, int N, int K, in
                         int alignment, const MoePlanOut* plan, uint16_t* out,
                         cudaStream_t stream);
 
+/* ---------------------------------------------------------------- around the experts */
+/* Element types of arguments that take more than one. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F32 1
+#define MOE_DTYPE_E4M3 2 /* 8-bit floating point, 4 exponent and 3 mantissa bits, largest value 448 */
+
+/*
+ * Root-mean-square norm with the residual's addition.  Row by row, in fp32:
+ *   s = x + residual (x alone without a residual),
+ *   rstd = 1 / sqrt(mean(s^2) + eps),  v = s * rstd * weight,
+ *   residual_out = s,  y = bf16(v),
+ *   q_scale = max|v| / 448 (1/448 for a row of zeros),  q = e4m3(v / q_scale).
+ * v is taken from the unrounded s, and q from the unrounded v.
+ *   x            (device) bf16[N][H]; H % 8 == 0; every row array 16-byte aligned.
+ *   residual     (device) [N][H] of residual_dtype (MOE_DTYPE_BF16 or _F32), or NULL.
+ *   weight       (device) [H] of weight_dtype (MOE_DTYPE_BF16 or _F32), 16-byte aligned.
+ *   y            (device) bf16[N][H] out, or NULL when q is given.
+ *   residual_out (device) [N][H] of residual_dtype out, or NULL; may be
+ *                residual itself; needs a residual.
+ *   rstd         (device) float32[N] out, or NULL.
+ *   q, q_scale   (device) e4m3[N][H] (8-byte aligned) and float32[N] out, both or neither.
+ * eps >= 0 and finite.  N = 0 launches nothing.  One launch.
+ */
+MOE_API int moe_residual_norm(const uint16_t* x, const void* residual, int residual_dtype,
+                              const void* weight, int weight_dtype, int N, int H, float eps,
+                              uint16_t* y, void* residual_out, float* rstd, uint8_t* q, float* q_scale,
+                              cudaStream_t stream);
+
+/*
+ * Gradient of the norm.  With xhat = s * rstd and t = dy * weight:
+ *   d = rstd * (t - xhat * mean(t * xhat)) + ds,
+ *   dx = bf16(d), dres = d,  dweight = sum over the rows of dy * xhat.
+ *   dy           (device) bf16[N][H], gradient of y.
+ *   s            (device) [N][H] of s_dtype (MOE_DTYPE_BF16 or _F32): the
+ *                norm's residual_out, or its x where there was no residual.
+ *   rstd         (device) float32[N] from the forward call.
+ *   ds           (device) [N][H] of s_dtype, the gradient that reaches s
+ *                from elsewhere (the residual stream), or NULL.
+ *   dx           (device) bf16[N][H] out: the gradient of x (and of a bf16 residual).
+ *   dres         (device) float32[N][H] out or NULL, the gradient of an fp32
+ *                residual; only with s_dtype MOE_DTYPE_F32.
+ *   dweight      (device) float32[H] out, or NULL.  Summed in a fixed order.
+ *   workspace    (device) moe_residual_norm_backward_workspace_size(N, H)
+ *                bytes, 16-byte aligned, no initialisation; needed for dweight.
+ * Two launches (one without dweight).  N = 0 zeroes dweight.
+ */
+MOE_API size_t moe_residual_norm_backward_workspace_size(int N, int H);
+MOE_API int moe_residual_norm_backward(const uint16_t* dy, const void* s, int s_dtype, const void* weight,
+                                       int weight_dtype, const float* rstd, const void* ds, int N, int H,
+                                       uint16_t* dx, float* dres, float* dweight, void* workspace,
+                                       size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The experts' gated feed-forward over a plan's permuted rows.  For a row m
+ * of expert e's group, [cu_seqlens[e], cu_seqlens[e] + tokens_per_expert[e]):
+ *   g = x[m] . w_gate[e]^T,  u = x[m] . w_up[e]^T,
+ *   h[m] = bf16(silu(g) * u),  y[m] = bf16(h[m] . w_down[e]^T),
+ * products accumulated in fp32, silu(g) = g / (1 + e^-g).  Rows of no group
+ * are not read (they may hold anything); of them, a group's padding (up to
+ * cu_seqlens[e+1]) is written as zeros in y and the rest is left untouched.
+ *   x          (device) [rows][H]: bf16, or e4m3 with x_scale; x_dtype says which.
+ *   x_scale    (device) float32[rows] with e4m3: x[m] stands for x[m] * x_scale[m]; else NULL.
+ *   w_gate_up  (device) [E][2][I][H] of x_dtype: gate rows, then up rows.
+ *   w_scale    (device) float32[E][2][I] with e4m3, one scale a channel; else NULL.
+ *   w_down     (device) bf16[E][H][I].
+ *   rows       rows of x, h, preact and y (the plan's capacity, or at least
+ *              cu_seqlens[E]); rows < 2^31.
+ *   plan       uses cu_seqlens, tokens_per_expert and status.  A group that
+ *              leaves [0, rows) sets MOE_ERR_DEVICE_INDEX and is not touched
+ *              (the other outputs are then unspecified); with an error in
+ *              the status before the call nothing is written.
+ *   h          (device) bf16[rows][I] out (the groups' rows), also the
+ *              call's workspace.
+ *   preact     (device) float32[rows][2][I] out, or NULL: g and u for the
+ *              backward call (32 bits, so that the gradients' operands are
+ *              rounded once).  bf16 only.
+ *   y          (device) bf16[rows][H] out; must not alias x.
+ * H % 8 == 0 (H % 16 == 0 with e4m3), I % 8 == 0, H and I < 2^20, 1 <= E <= 1024;
+ * 16-byte aligned arrays.  rows = 0 launches nothing.
+ */
+MOE_API int moe_expert_ffn(const void* x, const float* x_scale, const void* w_gate_up, const float* w_scale,
+                           const uint16_t* w_down, int64_t rows, int E, int H, int I, int x_dtype,
+                           const MoePlanOut* plan, uint16_t* h, float* preact, uint16_t* y,
+                           cudaStream_t stream);
+
+/*
+ * Gradients of moe_expert_ffn (bf16).  For the rows of each group:
+ *   dh = dy . w_down,  dg = dh * u * sig(g) * (1 + g * (1 - sig(g))),
+ *   du = dh * silu(g),  dgate_up = bf16(dg, du),
+ *   dx = bf16(dg . w_gate + du . w_up),
+ *   dw_gate_up[e] = bf16((dg, du)^T . x),  dw_down[e] = bf16(dy^T . h),
+ * the last two summed over the group's rows (zeros for an empty group).
+ * Rows of no group are not read; a group's padding is written as zeros in dx.
+ *   dy, x, h, preact, w_gate_up, w_down: as in the forward call, and from it.
+ *   dgate_up    (device) bf16[rows][2][I]: the call's workspace (it holds
+ *               dg and du of the groups' rows afterwards).
+ *   dx          (device) bf16[rows][H] out, or NULL if not wanted.
+ *   dw_gate_up  (device) bf16[E][2][I][H] out, or NULL.
+ *   dw_down     (device) bf16[E][H][I] out, or NULL.
+ * Sizes, plan and errors as in the forward call.  rows = 0 zeroes the
+ * weights' gradients.
+ */
+MOE_API int moe_expert_ffn_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* h,
+                                    const float* preact, const uint16_t* w_gate_up, const uint16_t* w_down,
+                                    int64_t rows, int E, int H, int I, const MoePlanOut* plan,
+                                    uint16_t* dgate_up, uint16_t* dx, uint16_t* dw_gate_up,
+                                    uint16_t* dw_down, cudaStream_t stream);
+
+/*
+ * Gradient of moe_combine.  For every pair (s, k) with slot = raw slot(s, k):
+ *   dy[slot] = bf16(topk_w[s][k] * dout[s]),
+ *   dw[s][k] = sum over h of dout[s][h] * y[slot][h]  (fp32, fixed order);
+ * rows inside the plan's zero-fill ranges are written as zeros in dy and the
+ * rows past them are left untouched.  (The permute's gradient is moe_combine
+ * with weights of one.)
+ *   dout    (device) bf16[N][H];  y, dy (device) bf16[rows][H];  topk_w, dw
+ *           (device) float32[N][K].  rows: the plan's capacity, or at least
+ *           cu_seqlens[E].  dy must not alias y.
+ *   plan    uses dst, zero_fill_ranges and status; a slot outside [0, rows)
+ *           sets MOE_ERR_DEVICE_INDEX and its token is skipped.
+ * H % 8 == 0, 1 <= K <= 32, K <= E <= 1024; 16-byte aligned rows.  N = 0
+ * launches nothing.
+ */
+MOE_API int moe_combine_backward(const uint16_t* dout, const uint16_t* y, const float* topk_w, int N, int K,
+                                 int H, int E, int64_t rows, const MoePlanOut* plan, uint16_t* dy,
+                                 float* dw, cudaStream_t stream);
+
 /* ---------------------------------------------------------------- status */
 /*
  * Synchronise `stream`, copy the plan's device status to *device_status
