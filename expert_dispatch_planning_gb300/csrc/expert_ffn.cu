@@ -8,24 +8,34 @@
 //   dx      dx   [row, j] = dgate_up[row, k] * w_gate_up[e][k][j]
 //   dw      dW[e][i][j]   = sum over the group's rows of left[row, i] * right[row, j]
 //
-// One persistent kernel, one block an SM.  A tile is 128 rows of the output by
-// up to 256 columns; its fp32 accumulators lie in tensor memory, twice, so
-// that one tile's epilogue runs under the next one's products.  Warp 0 brings
-// 128-byte wide slices of both operands into a ring of shared-memory stages
-// (tensor copies, 128-byte swizzle), warp 1 issues the matrix instructions,
-// warps 2-5 read the accumulators (32 rows each) and write the output.  The
-// gated product has the gate's and the up projection's columns of the same
-// channels side by side in one tile, so that silu(g) * u needs no exchange;
-// dgate applies the activation's gradient to dh in its epilogue, so that dh
-// is never written.
+// One persistent kernel; two blocks on neighbouring SMs work as a pair on one
+// tile (tcgen05 with cta_group::2, M = 256).  The instruction's M side is the
+// weights' output index and its N side the group's rows: the weights' extents
+// fill tiles of 256, while a group of any length is cut into tiles of equal
+// length, a multiple of 16 rows up to 256, so that ragged groups cost little.
+// (In dw both sides are weights' indexes and the groups are the k side.)
+// Each block holds the fp32 accumulators of its 128 output channels by all the
+// tile's rows in tensor memory, twice, so that one tile's epilogue runs under
+// the next one's products.
 //
-// Operands: where k is the contiguous index (x, h, dy, dgate_up; weights of
-// gated and down) a stage holds rows of 64 k's (128 in 8 bits); where it is
-// not (weights of dgate and dx, both of dw) a stage holds 64 rows of k, each
-// with 64 of the tile's rows or columns, and the instruction reads it
-// transposed.  Slices that leave an array are filled with zeros by the copy.
-// In dw the last slice of a group runs on into other rows, which may hold
-// anything: the issuing warp zeroes them in both operands first.
+// Warp 0 of each block brings its operands' slices of 128 bytes of k into a
+// ring of shared-memory stages (tensor copies, 128-byte swizzle): 128 rows of
+// the M side and half of the tile's N side, of which the hardware shows both
+// halves to both SMs.  Warp 1 of the pair's first block issues the matrix
+// instructions.  Warps 2-9 read the accumulators (a warp sees 32 channels),
+// turn them through shared memory so that a row's channels lie side by side,
+// and write the output.  In the gated product every 32 rows of the M side are
+// 16 channels of the gate and the same 16 of the up projection, so that a
+// warp has both for silu(g) * u; dgate applies the activation's gradient to
+// dh there, so that dh is never written.
+//
+// Where k is the contiguous index (x, h, dy, dgate_up; weights of gated and
+// down) a stage holds rows of 64 k's (128 in 8 bits); where it is not (weights
+// of dgate and dx, both sides of dw) it holds rows of 64 of the M or N index,
+// one for each k, and the instruction reads it transposed.  Slices that leave
+// an array are filled with zeros by the copy.  In dw a group's last slice runs
+// on into other rows, which may hold anything: warp 1 of each block zeroes
+// them in both operands before the instruction reads the stage.
 #include <cuda_fp8.h>
 
 #include "tensor_core.cuh"
@@ -35,100 +45,110 @@ namespace moe {
 
 enum Product { kGated, kDown, kDgate, kDx, kDw };
 
-constexpr int kTileM = 128;
-constexpr int kRing = 196 * 1024;  // bytes of shared memory for the stages
-constexpr int kMaxStages = 16;
-constexpr int kThreads = 192;
-constexpr int kSlice = 128;        // bytes of k (or of a 64-element run) in a stage's row
+constexpr int kTile = 256;         // both sides of a tile at most
+constexpr int kHalf = 128;         // a block's part of it
+constexpr int kSlice = 128;        // bytes of a stage's row
+constexpr int kMaxStages = 12;
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kChunk = 16;         // accumulator columns that a warp turns at a time
+constexpr int kTurnStride = 48;    // floats between a chunk's rows: 16 banks apart for the gated reads
 
 struct FfnArgs {
-    const float* a_scale;
+    const float* a_scale;   // gated in 8 bits: scales of x's rows and of the channels
     const float* b_scale;
     const float* preact_in;
     const int32_t* cu;
     const int32_t* count;
     int32_t* status;
     int64_t rows;
-    int E, M, N, K;       // output width N, contraction length K (dw: output M x N)
+    int E, M, N, K;         // M: output channels; K: contraction length; dw: output M x N
+    int ring_bytes;
     uint16_t* out;
     float* preact_out;
     int64_t timeout_ns;
 };
 
 struct Shared {
-    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    float turn[kEpilogueWarps][kChunk * kTurnStride];
+    uint64_t full[kMaxStages], empty[kMaxStages], tail_full[kMaxStages], tail_ready[kMaxStages], acc_full[2],
+        acc_empty[2];
     uint32_t tmem;
-    int failed;
-    int stop;             // the plan's status held an error
-    int scan[kThreads / 32];
-    int most[kThreads / 32];
+    int stop;               // the plan's status held an error
+    int scan[kThreads / 32], most[kThreads / 32];
 };
 
 struct Tile {
     int e;
-    int64_t first;   // the group's first row
-    int count;       // its rows
-    int padded;      // and with its padding
-    int m0, n0;      // the tile's first output row (within the group; dw: of M) and column
-    int slices;      // of k
+    int first, count, padded;  // the group's first row, its rows, and with its padding
+    int m0;                    // the pair's first output channel
+    int n0, n;                 // first row within the group (dw: first column) and how many
+    int slices;                // of k
+    bool last;                 // the group's last rows
 };
 
 // What every warp of a block knows about the work.
 struct Work {
-    const int* first;
-    const int* count;
-    const int* padded;
+    const int *first, *count, *padded;
     const int* prefix;  // row tiles before each expert (not dw)
     int E, M, N, k_slices;
-    int cols;           // output columns of a tile
-    int n_tiles;
+    int m_step, m_tiles;
     int64_t tiles;
 };
 
 template <int P>
 __device__ __forceinline__ Tile locate(const Work& w, int64_t t) {
     Tile r;
-    int mt;
+    int nt;
     int64_t at;
     if constexpr (P == kDw) {
-        mt = (w.M + kTileM - 1) / kTileM;
-        const int64_t per = static_cast<int64_t>(mt) * w.n_tiles;
+        nt = (w.N + kTile - 1) / kTile;
+        const int64_t per = static_cast<int64_t>(w.m_tiles) * nt;
         r.e = static_cast<int>(t / per);
         at = t - r.e * per;
     } else {
-        int lo = 0, hi = w.E;  // the expert with prefix[e] * n_tiles <= t < prefix[e + 1] * n_tiles
+        int lo = 0, hi = w.E;  // the expert with prefix[e] * m_tiles <= t < prefix[e + 1] * m_tiles
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (static_cast<int64_t>(w.prefix[mid]) * w.n_tiles <= t) lo = mid;
+            if (static_cast<int64_t>(w.prefix[mid]) * w.m_tiles <= t) lo = mid;
             else hi = mid;
         }
         r.e = lo;
-        mt = w.prefix[lo + 1] - w.prefix[lo];
-        at = t - static_cast<int64_t>(w.prefix[lo]) * w.n_tiles;
+        nt = w.prefix[lo + 1] - w.prefix[lo];
+        at = t - static_cast<int64_t>(w.prefix[lo]) * w.m_tiles;
     }
-    // bands of 16 row tiles, column by column: what the blocks work on at one time stays in L2
-    constexpr int kBand = 16;
-    const int band = static_cast<int>(at / (kBand * static_cast<int64_t>(w.n_tiles)));
-    const int in_band = static_cast<int>(at - band * (kBand * static_cast<int64_t>(w.n_tiles)));
-    const int height = min(kBand, mt - band * kBand);
-    r.m0 = (band * kBand + in_band % height) * kTileM;
-    r.n0 = in_band / height * w.cols;
+    // bands of 8 tiles of the N side, the M side outermost within a band: what
+    // the pairs work on at one time is about square and stays in L2
+    constexpr int kBand = 8;
+    const int64_t per_band = static_cast<int64_t>(kBand) * w.m_tiles;
+    const int band = static_cast<int>(at / per_band);
+    const int in_band = static_cast<int>(at - band * per_band);
+    const int width = min(kBand, nt - band * kBand);
+    r.m0 = in_band / width * w.m_step;
+    const int j = band * kBand + in_band % width;
     r.first = w.first[r.e];
     r.count = w.count[r.e];
     r.padded = w.padded[r.e];
-    r.slices = P == kDw ? (r.count + 63) / 64 : w.k_slices;
+    r.last = j == nt - 1;
+    if constexpr (P == kDw) {
+        r.n0 = j * kTile;
+        r.n = min(kTile, w.N - r.n0);
+        r.slices = (r.count + 63) / 64;
+    } else {
+        const int each = ((r.count + nt - 1) / nt + 15) & ~15;
+        r.n0 = j * each;
+        r.n = min(each, r.count - r.n0);
+        r.slices = w.k_slices;
+    }
     return r;
 }
 
-// Bounded wait; on a timeout the block gives up (`failed`) and the plan's status says so.
-__device__ __forceinline__ bool wait(const FfnArgs& a, Shared* sh, uint64_t* bar, uint32_t parity) {
-    if (mbar_wait_bounded(bar, parity, static_cast<uint64_t>(a.timeout_ns))) return true;
-    *reinterpret_cast<volatile int*>(&sh->failed) = 1;
+// Bounded wait; on a timeout the caller gives up and the plan's status says so.
+__device__ __forceinline__ bool wait(const FfnArgs& a, uint64_t* bar, uint32_t parity) {
+    if (mbar_wait_pair(bar, parity, static_cast<uint64_t>(a.timeout_ns))) return true;
     record_error(a.status, MOE_ERR_DEVICE_TIMEOUT, blockIdx.x);
     return false;
 }
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) { return pack2(lo, hi); }
 
 // silu(g) = g * sigmoid(g) and sigmoid(g).  The hardware exponential and
 // division are within 2^-20 of the exact value for |g| < 16; beyond, where
@@ -137,141 +157,144 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) { return pack2(lo
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
-// Eight columns of a row, as bf16.
-__device__ __forceinline__ void store8_bf16(uint16_t* p, const float* v) {
-    st_v4(p, make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])));
+__device__ __forceinline__ void store4_bf16(uint16_t* p, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(a, b), pack2(c, d));
 }
 
+// One chunk of a row product: 16 rows of the group by the warp's 32 channels,
+// turned through `turn` so that neighbouring lanes hold neighbouring channels.
 template <int P>
-__device__ void epilogue(const FfnArgs& a, const Tile& t, int bn, uint32_t acc, int quarter, int lane, int thread) {
-    const int cols = P == kGated ? bn / 2 : bn;
-    const int m = t.m0 + quarter * 32 + lane;
-    const bool live = P == kDw ? m < a.M : m < t.count;
-    const bool any = P == kDw ? t.m0 + quarter * 32 < a.M : t.m0 + quarter * 32 < t.count;
-    const int64_t N = a.N;
-    const int64_t row = P == kDw ? static_cast<int64_t>(t.e) * a.M + m : t.first + m;
-    const uint32_t lane_addr = acc + (static_cast<uint32_t>(quarter * 32) << 16);
-    float row_scale = 1.f;
-    if (P == kGated && a.a_scale != nullptr && live) row_scale = __ldg(a.a_scale + row);
-    for (int c = 0; c < cols && any; c += 16) {
-        const int n = t.n0 + c;
-        if (n >= a.N) break;
-        const int width = min(16, a.N - n);  // 8 or 16
-        uint32_t v0[16], v1[16];
-        float f[16];
-        __syncwarp();  // the loads below are the whole warp's
-        if (P == kDw && t.slices == 0) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v0[j] = 0u;
-        } else {
-            tmem_load16(lane_addr + c, v0);
-            if constexpr (P == kGated) tmem_load16(lane_addr + cols + c, v1);
-        }
-        if constexpr (P == kDgate) {
-            float g[16], u[16];
-            if (live) {
-                const float* pre = a.preact_in + row * 2 * N + n;
-                for (int j = 0; j < width; j += 4) {
-                    *reinterpret_cast<float4*>(g + j) = __ldg(reinterpret_cast<const float4*>(pre + j));
-                    *reinterpret_cast<float4*>(u + j) = __ldg(reinterpret_cast<const float4*>(pre + N + j));
-                }
-            }
-            tmem_wait_load();
-            if (live) {
-                float d[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float dh = __uint_as_float(v0[j]), s = sigmoid(g[j]);
-                    f[j] = dh * u[j] * s * fmaf(g[j], 1.f - s, 1.f);
-                    d[j] = dh * g[j] * s;
-                }
-                uint16_t* out = a.out + row * 2 * N + n;
-                store8_bf16(out, f);
-                store8_bf16(out + N, d);
-                if (width == 16) {
-                    store8_bf16(out + 8, f + 8);
-                    store8_bf16(out + N + 8, d + 8);
-                }
-            }
-            continue;
-        }
+__device__ __forceinline__ void epilogue_chunk(const FfnArgs& a, const Tile& t, int rank, uint32_t acc, int c0,
+                                               int quarter, int lane, float* turn) {
+    const int64_t M = a.M;
+    uint32_t v[kChunk];
+    if constexpr (P == kGated) {
+        const int c = t.m0 + rank * 64 + quarter * 16 + (lane & 3) * 4;  // this lane's 4 channels
+        __syncwarp();
+        tmem_load16(acc + c0, v);
         tmem_wait_load();
-        if (!live) continue;
-        if constexpr (P == kGated) {
-            float g[16], u[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                g[j] = __uint_as_float(v0[j]);
-                u[j] = __uint_as_float(v1[j]);
-            }
+        for (int j = 0; j < kChunk; ++j) turn[j * kTurnStride + lane] = __uint_as_float(v[j]);
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < kChunk / 8; ++it) {
+            const int j = it * 8 + (lane >> 2), n = c0 + j;
+            if (n >= t.n || c >= M) continue;
+            const int64_t row = t.first + static_cast<int64_t>(t.n0 + n);
+            float4 g = *reinterpret_cast<const float4*>(turn + j * kTurnStride + (lane & 3) * 4);
+            float4 u = *reinterpret_cast<const float4*>(turn + j * kTurnStride + 16 + (lane & 3) * 4);
             if (a.a_scale != nullptr) {
-                const float* ws = a.b_scale + static_cast<int64_t>(t.e) * 2 * N + n;
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (j < width) {
-                        g[j] *= row_scale * __ldg(ws + j);
-                        u[j] *= row_scale * __ldg(ws + N + j);
-                    }
+                const float s = __ldg(a.a_scale + row);
+                const float4 sg = __ldg(reinterpret_cast<const float4*>(a.b_scale + 2 * M * t.e + c));
+                const float4 su = __ldg(reinterpret_cast<const float4*>(a.b_scale + 2 * M * t.e + M + c));
+                g = make_float4(g.x * (s * sg.x), g.y * (s * sg.y), g.z * (s * sg.z), g.w * (s * sg.w));
+                u = make_float4(u.x * (s * su.x), u.y * (s * su.y), u.z * (s * su.z), u.w * (s * su.w));
             }
             if (a.preact_out != nullptr) {
-                float* pre = a.preact_out + row * 2 * N + n;
-#pragma unroll
-                for (int j = 0; j < 16; j += 4)
-                    if (j < width) {
-                        *reinterpret_cast<float4*>(pre + j) = make_float4(g[j], g[j + 1], g[j + 2], g[j + 3]);
-                        *reinterpret_cast<float4*>(pre + N + j) = make_float4(u[j], u[j + 1], u[j + 2], u[j + 3]);
-                    }
+                *reinterpret_cast<float4*>(a.preact_out + row * 2 * M + c) = g;
+                *reinterpret_cast<float4*>(a.preact_out + row * 2 * M + M + c) = u;
             }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = silu(g[j]) * u[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v0[j]);
+            store4_bf16(a.out + row * M + c, silu(g.x) * u.x, silu(g.y) * u.y, silu(g.z) * u.z, silu(g.w) * u.w);
         }
-        store8_bf16(a.out + row * N + n, f);
-        if (width == 16) store8_bf16(a.out + row * N + n + 8, f + 8);
-    }
-    if constexpr (P == kDown || P == kDx) {
-        // the group's last row tile zeroes its padding, which may go on past the tile
-        if (t.m0 + kTileM >= t.count && t.padded > t.count) {
-            const int chunks = (min(cols, a.N - t.n0) + 7) / 8;
-            const int64_t todo = static_cast<int64_t>(t.padded - t.count) * chunks;
-            for (int64_t i = thread; i < todo; i += 128) {
-                const int64_t r = t.first + t.count + i / chunks;
-                st_v4(a.out + r * N + t.n0 + 8 * (i % chunks), make_uint4(0u, 0u, 0u, 0u));
+    } else {
+        const int c = t.m0 + rank * kHalf + quarter * 32 + (lane & 7) * 4;
+        constexpr int kIts = kChunk / 4;
+        float4 g[P == kDgate ? kIts : 1], u[P == kDgate ? kIts : 1];
+        if constexpr (P == kDgate) {  // asked for before the accumulators are read
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int n = c0 + it * 4 + (lane >> 3);
+                if (n < t.n && c < M) {
+                    const float* pre = a.preact_in + (t.first + static_cast<int64_t>(t.n0 + n)) * 2 * M + c;
+                    g[it] = ld_stream_f4(pre);
+                    u[it] = ld_stream_f4(pre + M);
+                }
             }
         }
+        __syncwarp();
+        tmem_load16(acc + c0, v);
+        tmem_wait_load();
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) turn[j * kTurnStride + lane] = __uint_as_float(v[j]);
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+            const int j = it * 4 + (lane >> 3), n = c0 + j;
+            if (n >= t.n || c >= M) continue;
+            const int64_t row = t.first + static_cast<int64_t>(t.n0 + n);
+            const float4 d = *reinterpret_cast<const float4*>(turn + j * kTurnStride + (lane & 7) * 4);
+            if constexpr (P == kDgate) {
+                const float dh[4] = {d.x, d.y, d.z, d.w}, gs[4] = {g[it].x, g[it].y, g[it].z, g[it].w},
+                            us[4] = {u[it].x, u[it].y, u[it].z, u[it].w};
+                float dg[4], du[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float s = sigmoid(gs[i]);
+                    dg[i] = dh[i] * us[i] * s * fmaf(gs[i], 1.f - s, 1.f);
+                    du[i] = dh[i] * gs[i] * s;
+                }
+                store4_bf16(a.out + row * 2 * M + c, dg[0], dg[1], dg[2], dg[3]);
+                store4_bf16(a.out + row * 2 * M + M + c, du[0], du[1], du[2], du[3]);
+            } else {
+                store4_bf16(a.out + row * M + c, d.x, d.y, d.z, d.w);
+            }
+        }
     }
+}
+
+// dw: a lane holds an output row; it writes 16 columns of it.
+__device__ __forceinline__ void epilogue_dw(const FfnArgs& a, const Tile& t, int rank, uint32_t acc, int c0, int quarter,
+                                            int lane) {
+    const int m = t.m0 + rank * kHalf + quarter * 32 + lane;
+    uint32_t v[kChunk];
+    if (t.slices > 0) {
+        __syncwarp();
+        tmem_load16(acc + c0, v);
+        tmem_wait_load();
+    } else {
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) v[j] = 0u;
+    }
+    if (m >= a.M) return;
+    uint16_t* out = a.out + (static_cast<int64_t>(t.e) * a.M + m) * a.N + t.n0 + c0;
+    uint32_t p[kChunk / 2];
+#pragma unroll
+    for (int j = 0; j < kChunk; j += 2) p[j / 2] = pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+    st_v4(out, make_uint4(p[0], p[1], p[2], p[3]));
+    if (c0 + 8 < t.n) st_v4(out + 8, make_uint4(p[4], p[5], p[6], p[7]));
 }
 
 template <int P, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
-    ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a16,
-               const __grid_constant__ CUtensorMap map_b, const FfnArgs a) {
+    ffn_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_n,
+               const __grid_constant__ CUtensorMap map_n16, const FfnArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    constexpr bool kAmn = P == kDw, kBmn = P == kDgate || P == kDx || P == kDw;  // k is not the contiguous index
+    constexpr bool kMmn = P == kDgate || P == kDx || P == kDw, kNmn = P == kDw;  // k is not the contiguous index
     constexpr int kElems = FP8 ? 128 : 64;                                       // k's of a slice
 
     uint8_t* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    Shared* sh = reinterpret_cast<Shared*>(ring + kRing);
+    Shared* sh = reinterpret_cast<Shared*>(ring + a.ring_bytes);
     int* first = reinterpret_cast<int*>(sh + 1);
     int *count = first + a.E, *padded = count + a.E, *prefix = padded + a.E;  // prefix: E + 1
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(pair_rank());
     if (tid == 0) {
-        tensor_prefetch(&map_a);
-        tensor_prefetch(&map_b);
+        tensor_prefetch(&map_m);
+        tensor_prefetch(&map_n);
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sh->full[i], 1);
             mbar_init(&sh->empty[i], 1);
+            mbar_init(&sh->tail_full[i], 1);
+            mbar_init(&sh->tail_ready[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->acc_full[i], 1);
-            mbar_init(&sh->acc_empty[i], 4);
+            mbar_init(&sh->acc_empty[i], 2 * kEpilogueWarps);
         }
         fence_mbar_init();
-        sh->failed = 0;
     }
+    __syncwarp();
     if (warp == 1) tmem_alloc(&sh->tmem, 512);
     pdl_wait();
     pdl_trigger();
@@ -287,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         first[e] = fits ? static_cast<int>(f) : 0;
         count[e] = fits ? static_cast<int>(c) : 0;
         padded[e] = fits ? static_cast<int>(p) : 0;
-        mine += (count[e] + kTileM - 1) / kTileM;
+        mine += (count[e] + kTile - 1) / kTile;
         longest = max(longest, count[e]);
     }
     int before = mine;  // inclusive over the warp, then exclusive over the block
@@ -299,43 +322,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     longest = __reduce_max_sync(FULL_MASK, longest);
     if (lane == 31) sh->scan[warp] = before;
     if (lane == 0) sh->most[warp] = longest;
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
     int row_tiles = 0;
     before -= mine;
     longest = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += sh->scan[w];
-        row_tiles += sh->scan[w];
-        longest = max(longest, sh->most[w]);
+    for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < warp) before += sh->scan[i];
+        row_tiles += sh->scan[i];
+        longest = max(longest, sh->most[i]);
     }
     for (int e = tid * per; e < min(a.E, (tid + 1) * per); ++e) {
         prefix[e] = before;
-        before += (count[e] + kTileM - 1) / kTileM;
+        before += (count[e] + kTile - 1) / kTile;
     }
     if (tid == 0) prefix[a.E] = row_tiles;
 
-    // ---- the tile's width: the fewest rounds of the grid, each weighed by its
-    // columns and what a tile costs beside them (its rows' copies, its start)
-    const int64_t m_tiles = P == kDw ? static_cast<int64_t>(a.E) * ((a.M + kTileM - 1) / kTileM) : row_tiles;
-    const int a_rows = P == kDw || longest > 64 ? kTileM : max(16, (longest + 15) / 16 * 16);
-    int bn = 256;
-    int64_t best = -1;
-    for (int b = 256; b >= 64; b >>= 1) {
-        const int c = P == kGated ? b / 2 : b;
-        const int64_t rounds = (m_tiles * ((a.N + c - 1) / c) + gridDim.x - 1) / gridDim.x;
-        const int64_t cost = rounds * (b + a_rows / 4 + 16);
-        if (best < 0 || cost < best) {
-            best = cost;
-            bn = b;
-        }
-    }
-    const uint32_t a_bytes = static_cast<uint32_t>(a_rows) * kSlice;
-    const uint32_t stage_bytes = a_bytes + static_cast<uint32_t>(bn) * kSlice;
-    // the instruction reads 128 rows of A, past the end of a smaller stage: the last one keeps clear of the ring's end
-    const uint32_t past = stage_bytes < kTileM * kSlice ? kTileM * kSlice - stage_bytes : 0;
-    const int stages = min(kMaxStages, static_cast<int>((kRing - past) / stage_bytes));
     Work w;
     w.first = first;
     w.count = count;
@@ -345,107 +346,140 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.M = a.M;
     w.N = a.N;
     w.k_slices = (a.K + kElems - 1) / kElems;
-    w.cols = P == kGated ? bn / 2 : bn;
-    w.n_tiles = (a.N + w.cols - 1) / w.cols;
-    w.tiles = m_tiles * w.n_tiles;
+    w.m_step = P == kGated ? kHalf : kTile;  // a gated tile holds each channel twice
+    w.m_tiles = (a.M + w.m_step - 1) / w.m_step;
+    w.tiles = P == kDw ? static_cast<int64_t>(a.E) * w.m_tiles * ((a.N + kTile - 1) / kTile)
+                       : static_cast<int64_t>(row_tiles) * w.m_tiles;
+    // short groups leave room for more stages: the N side's part is as long as the longest tile's half
+    const int half = (min(P == kDw ? kTile : longest, kTile) + 15) / 16 * 8;
+    const int n_rows = P == kDw || half > 64 ? kHalf : max(16, (half + 15) / 16 * 16);
+    const uint32_t stage_bytes = static_cast<uint32_t>(kHalf + n_rows) * kSlice;
+    const int stages = min(kMaxStages, static_cast<int>(a.ring_bytes / stage_bytes));
+    tc_fence_before();
     __syncthreads();
+    pair_sync();  // both blocks' barriers and tensor memory are ready
+    tc_fence_after();
     const uint32_t tmem = sh->tmem;
     const bool run = sh->stop == 0;
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (run && warp == 0) {
         if (lane == 0) {
             int s = 0;
             uint32_t phase = 0;
-            int64_t issued = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; i < w.tiles && ok; i += gridDim.x) {
+            for (int64_t i = pair; i < w.tiles && ok; i += pairs) {
                 const Tile t = locate<P>(w, i);
-                const int live = P == kDw ? kTileM : min(kTileM, t.count - t.m0);
-                const int pieces = live > 64 ? 0 : (live + 15) / 16;  // 0: one copy of 128 rows
-                const uint32_t bytes = (pieces ? pieces * 16 : kTileM) * kSlice + bn * kSlice;
+                const int mine = ((t.n + 15) & ~15) / 2;              // N-side rows (dw: columns) of a block
+                const int pieces = P == kDw ? (mine + 63) / 64 : mine > 64 ? 0 : (mine + 15) / 16;
+                const uint32_t bytes =
+                    kHalf * kSlice + (P == kDw ? pieces * 8192 : pieces ? pieces * 16 * kSlice : kHalf * kSlice);
+                const int m = t.m0 + rank * (P == kGated ? 64 : kHalf);
                 for (int k = 0; k < t.slices; ++k) {
-                    if (!(ok = wait(a, sh, &sh->empty[s], phase ^ 1u))) break;
-                    uint8_t* sa = ring + s * stage_bytes;
-                    uint8_t* sb = sa + a_bytes;
-                    uint64_t* bar = &sh->full[s];
-                    mbar_arrive_expect_tx(bar, bytes);
-                    const int at = k * kElems;
-                    if constexpr (P == kDw) {
-                        const int row = static_cast<int>(t.first) + k * 64;
-                        for (int j = 0; j < 2; ++j) tensor_load_2d(sa + j * 8192, &map_a, t.m0 + 64 * j, row, bar);
-                        for (int j = 0; j < bn / 64; ++j)
-                            tensor_load_2d(sb + j * 8192, &map_b, t.n0 + 64 * j, row, bar);
+                    if (!(ok = wait(a, &sh->empty[s], phase ^ 1u))) break;
+                    uint8_t* sm = ring + s * stage_bytes;
+                    uint8_t* sn = sm + kHalf * kSlice;
+                    // the second block's copies are counted by the first one's barrier,
+                    // but for a last slice that it has to mend first
+                    const bool tail = P == kDw && k + 1 == t.slices && (t.count & 15) != 0;
+                    uint32_t bar;
+                    if (rank == 0) {
+                        mbar_arrive_expect_tx(&sh->full[s], tail ? bytes : 2 * bytes);
+                        bar = smem_addr(&sh->full[s]);
+                    } else if (tail) {
+                        mbar_arrive_expect_tx(&sh->tail_full[s], bytes);
+                        bar = smem_addr(&sh->tail_full[s]);
                     } else {
-                        const int row = static_cast<int>(t.first) + t.m0;
-                        if (pieces == 0) tensor_load_2d(sa, &map_a, at, row, bar);
-                        for (int j = 0; j < pieces; ++j)
-                            tensor_load_2d(sa + j * 16 * kSlice, &map_a16, at, row + 16 * j, bar);
-                        if constexpr (P == kGated) {
-                            for (int j = 0; j < bn / 64; ++j) {
-                                tensor_load_3d(sb + j * 4096, &map_b, at, t.n0 + 32 * j, 2 * t.e, bar);
-                                tensor_load_3d(sb + bn * (kSlice / 2) + j * 4096, &map_b, at, t.n0 + 32 * j,
-                                               2 * t.e + 1, bar);
-                            }
-                        } else if constexpr (P == kDown) {
-                            for (int j = 0; j < bn / 64; ++j)
-                                tensor_load_3d(sb + j * 8192, &map_b, at, t.n0 + 64 * j, t.e, bar);
-                        } else {
-                            for (int j = 0; j < bn / 64; ++j)
-                                tensor_load_3d(sb + j * 8192, &map_b, t.n0 + 64 * j, at, t.e, bar);
-                        }
+                        bar = leader_addr(&sh->full[s]);
                     }
-                    ++issued;
+                    const int at = k * kElems;
+                    if constexpr (P == kGated) {
+                        for (int j = 0; j < 4; ++j) tensor_load_4d(sm + j * 4096, &map_m, at, m + 16 * j, 0, t.e, bar);
+                    } else if constexpr (P == kDown) {
+                        tensor_load_3d(sm, &map_m, at, m, t.e, bar);
+                    } else if constexpr (P == kDw) {
+                        for (int j = 0; j < 2; ++j)
+                            tensor_load_2d(sm + j * 8192, &map_m, m + 64 * j, t.first + k * 64, bar);
+                    } else {
+                        for (int j = 0; j < 2; ++j) tensor_load_3d(sm + j * 8192, &map_m, m + 64 * j, at, t.e, bar);
+                    }
+                    if constexpr (P == kDw) {
+                        for (int j = 0; j < pieces; ++j)
+                            tensor_load_2d(sn + j * 8192, &map_n, t.n0 + rank * mine + 64 * j, t.first + k * 64, bar);
+                    } else {
+                        const int row = t.first + t.n0 + rank * mine;
+                        if (pieces == 0) tensor_load_2d(sn, &map_n, at, row, bar);
+                        for (int j = 0; j < pieces; ++j)
+                            tensor_load_2d(sn + j * 16 * kSlice, &map_n16, at, row + 16 * j, bar);
+                    }
                     if (++s == stages) {
                         s = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            if (!ok)  // let the copies in flight land before the block's shared memory goes
-                for (int64_t j = max(int64_t(0), issued - stages); j < issued; ++j)
-                    mbar_wait_bounded(&sh->full[j % stages], static_cast<uint32_t>((j / stages) & 1),
-                                      static_cast<uint64_t>(a.timeout_ns));
+            if (!ok) {  // time for the copies in flight to land before the block's shared memory goes
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 20000000u) __nanosleep(1000);
+            }
         }
-    } else if (run && warp == 1) {
-        const uint32_t desc = mma_desc(FP8 ? 0u : 1u, kAmn, kBmn, kTileM, bn);
+        __syncwarp();
+    } else if (run && warp == 1 && (rank == 0 || P == kDw)) {
         int s = 0, buf = 0;
-        uint32_t phase = 0, acc_phase = 0;
+        uint32_t phase = 0, acc_phase = 0, tails = 0;  // tails: a bit a stage, how often it held a last slice
         bool ok = true;
-        for (int64_t i = blockIdx.x; i < w.tiles && ok; i += gridDim.x) {
+        for (int64_t i = pair; i < w.tiles && ok; i += pairs) {
             const Tile t = locate<P>(w, i);
             if (t.slices == 0) continue;
-            if (!(ok = wait(a, sh, &sh->acc_empty[buf], acc_phase ^ 1u))) break;
-            tc_fence_after();
-            for (int k = 0; k < t.slices; ++k) {
-                if (!(ok = wait(a, sh, &sh->full[s], phase))) break;
+            const int nb = (t.n + 15) & ~15;
+            const uint32_t desc = mma_desc(FP8 ? 0u : 1u, kMmn, kNmn, kTile, nb);
+            if (rank == 0) {
+                if (!(ok = wait(a, &sh->acc_empty[buf], acc_phase ^ 1u))) break;
                 tc_fence_after();
-                uint8_t* sa = ring + s * stage_bytes;
-                uint8_t* sb = sa + a_bytes;
+            }
+            for (int k = 0; k < t.slices; ++k) {
+                uint8_t* sm = ring + s * stage_bytes;
+                uint8_t* sn = sm + kHalf * kSlice;
                 int steps = 4;
+                bool tail = false;
                 if constexpr (P == kDw) {
                     const int valid = min(64, t.count - 64 * k);
                     steps = (valid + 15) / 16;
-                    if (valid < steps * 16) {  // rows past the group: zero in both operands
-                        const int boxes = 2 + bn / 64, chunks = (steps * 16 - valid) * 8;
-                        for (int j = lane; j < boxes * chunks; j += 32) {
-                            uint8_t* box = j / chunks < 2 ? sa + j / chunks * 8192 : sb + (j / chunks - 2) * 8192;
-                            *reinterpret_cast<uint4*>(box + valid * kSlice + j % chunks * 16) =
+                    tail = k + 1 == t.slices && (t.count & 15) != 0;
+                    if (rank == 0 || tail)
+                        if (!(ok = wait(a, rank == 0 ? &sh->full[s] : &sh->tail_full[s],
+                                        rank == 0 ? phase : (tails >> s) & 1u)))
+                            break;
+                    if (tail) {  // rows past the group: zero in both operands
+                        const int boxes = 2 + (nb / 2 + 63) / 64, chunks = (steps * 16 - valid) * 8;
+                        for (int j = lane; j < boxes * chunks; j += 32)  // the N side's boxes follow the M side's two
+                            *reinterpret_cast<uint4*>(sm + j / chunks * 8192 + valid * kSlice + j % chunks * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
-                        }
                         fence_proxy_async_smem();
                         __syncwarp();
+                        if (rank != 0) {
+                            if (lane == 0) mbar_arrive_leader(&sh->tail_ready[s]);
+                        } else if (!(ok = wait(a, &sh->tail_ready[s], (tails >> s) & 1u))) {
+                            break;
+                        }
+                        tails ^= 1u << s;
                     }
+                } else {
+                    if (!(ok = wait(a, &sh->full[s], phase))) break;
                 }
-                if (lane == 0) {
-                    const uint64_t da = operand_desc(smem_addr(sa), kAmn ? 8192 : 16, 1024);
-                    const uint64_t db = operand_desc(smem_addr(sb), kBmn ? 8192 : 16, 1024);
-                    for (int j = 0; j < steps; ++j)  // 32 bytes of k, or 16 rows of it
-                        mma<FP8>(tmem + buf * 256, da + j * ((kAmn ? 2048 : 32) >> 4),
-                                 db + j * ((kBmn ? 2048 : 32) >> 4), desc, k > 0 || j > 0);
-                    mma_commit(&sh->empty[s]);
-                    if (k + 1 == t.slices) mma_commit(&sh->acc_full[buf]);
+                if (rank == 0) {
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t dm = operand_desc(smem_addr(sm), kMmn ? 8192 : 16, 1024);
+                        const uint64_t dn = operand_desc(smem_addr(sn), kNmn ? 8192 : 16, 1024);
+                        for (int j = 0; j < steps; ++j)  // 32 bytes of k, or 16 rows of it
+                            mma<FP8>(tmem + buf * kTile, dm + j * ((kMmn ? 2048 : 32) >> 4),
+                                     dn + j * ((kNmn ? 2048 : 32) >> 4), desc, k > 0 || j > 0);
+                        mma_commit(&sh->empty[s]);
+                        if (k + 1 == t.slices) mma_commit(&sh->acc_full[buf]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 if (++s == stages) {
                     s = 0;
                     phase ^= 1u;
@@ -453,29 +487,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if ((buf ^= 1) == 0) acc_phase ^= 1u;
         }
-    } else if (run) {
-        const int quarter = warp & 3;  // the rows of tensor memory a warp may read
+    } else if (run && warp >= 2) {
+        const int quarter = warp & 3;           // the lanes of tensor memory that a warp may read
+        const int turn = (warp - 2) >> 2;       // two warps a quarter take every other chunk
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         int buf = 0;
         uint32_t acc_phase = 0;
-        for (int64_t i = blockIdx.x; i < w.tiles; i += gridDim.x) {
+        for (int64_t i = pair; i < w.tiles; i += pairs) {
             const Tile t = locate<P>(w, i);
             if (t.slices > 0) {
-                if (!wait(a, sh, &sh->acc_full[buf], acc_phase)) break;
+                if (!wait(a, &sh->acc_full[buf], acc_phase)) break;
                 tc_fence_after();
             }
-            epilogue<P>(a, t, bn, tmem + buf * 256, quarter, lane, tid - 64);
+            for (int c = turn * kChunk; c < t.n; c += 2 * kChunk) {
+                if constexpr (P == kDw) epilogue_dw(a, t, rank, tmem + buf * kTile + lanes, c, quarter, lane);
+                else epilogue_chunk<P>(a, t, rank, tmem + buf * kTile + lanes, c, quarter, lane, sh->turn[warp - 2]);
+            }
             if (t.slices > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->acc_empty[buf]);
+                if (lane == 0) mbar_arrive_leader(&sh->acc_empty[buf]);
                 if ((buf ^= 1) == 0) acc_phase ^= 1u;
+            }
+            if constexpr (P == kDown || P == kDx) {  // the group's padding: zeros
+                if (t.last && t.padded > t.count) {
+                    const int c0 = t.m0 + rank * kHalf, chunks = (min(kHalf, a.M - c0) + 7) / 8;
+                    const int64_t todo = chunks > 0 ? static_cast<int64_t>(t.padded - t.count) * chunks : 0;
+                    for (int64_t j = tid - 64; j < todo; j += 32 * kEpilogueWarps)
+                        st_v4(a.out + (t.first + t.count + j / chunks) * static_cast<int64_t>(a.M) + c0 + 8 * (j % chunks),
+                              make_uint4(0u, 0u, 0u, 0u));
+                }
             }
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    pair_sync();  // neither block leaves while the other may still use its barriers or tensor memory
     if (warp == 1) {
-        __syncwarp();
         tc_fence_after();
         tmem_free(tmem, 512);
     }
@@ -497,36 +546,45 @@ int check_sizes(int64_t rows, int E, int H, int I, const MoePlanOut* plan) {
     return MOE_OK;
 }
 
-// One product: left operand's rows (and dw's right ones) or weights, as the kernel's maps want them.
+// One product: the weights (dw: the left rows) and the rows (dw: the right ones).
 template <int P, bool FP8 = false>
-int launch_product(const void* left, const void* right, const moe::FfnArgs& a, cudaStream_t stream) {
+int launch_product(const void* weights, const void* row_data, moe::FfnArgs a, cudaStream_t stream) {
     constexpr int bytes = FP8 ? 1 : 2;
-    CUtensorMap map_a, map_a16, map_b;
+    CUtensorMap map_m, map_n, map_n16;
     int rc;
-    if constexpr (P == moe::kDw) {
-        rc = moe_host::make_tensor_map(&map_a, left, 2, 2, a.M, a.rows, 1, 64);
-        map_a16 = map_a;
-        if (rc == MOE_OK) rc = moe_host::make_tensor_map(&map_b, right, 2, 2, a.N, a.rows, 1, 64);
-    } else {
-        rc = moe_host::make_tensor_map(&map_a, left, bytes, 2, a.K, a.rows, 1, moe::kTileM);
-        if (rc == MOE_OK) rc = moe_host::make_tensor_map(&map_a16, left, bytes, 2, a.K, a.rows, 1, 16);
-        if (rc == MOE_OK) {
-            if constexpr (P == moe::kGated)
-                rc = moe_host::make_tensor_map(&map_b, right, bytes, 3, a.K, a.N, 2 * a.E, 32);
-            else if constexpr (P == moe::kDown)
-                rc = moe_host::make_tensor_map(&map_b, right, 2, 3, a.K, a.N, a.E, 64);
-            else
-                rc = moe_host::make_tensor_map(&map_b, right, 2, 3, a.N, a.K, a.E, 64);
-        }
-    }
+    if constexpr (P == moe::kGated) rc = moe_host::make_tensor_map(&map_m, weights, bytes, {a.K, a.M, 2, a.E}, 16, 2);
+    else if constexpr (P == moe::kDown) rc = moe_host::make_tensor_map(&map_m, weights, 2, {a.K, a.M, a.E}, moe::kHalf);
+    else if constexpr (P == moe::kDw) rc = moe_host::make_tensor_map(&map_m, weights, 2, {a.M, a.rows}, 64);
+    else rc = moe_host::make_tensor_map(&map_m, weights, 2, {a.M, a.K, a.E}, 64);
+    if (rc == MOE_OK)
+        rc = P == moe::kDw ? moe_host::make_tensor_map(&map_n, row_data, 2, {a.N, a.rows}, 64)
+                           : moe_host::make_tensor_map(&map_n, row_data, bytes, {a.K, a.rows}, moe::kHalf);
+    if (rc == MOE_OK && P != moe::kDw) rc = moe_host::make_tensor_map(&map_n16, row_data, bytes, {a.K, a.rows}, 16);
     if (rc != MOE_OK) return rc;
-    const size_t smem = 1024 + moe::kRing + sizeof(moe::Shared) + sizeof(int) * (4 * static_cast<size_t>(a.E) + 1);
-    static_assert(1024 + moe::kRing + sizeof(moe::Shared) + sizeof(int) * 4097 <= 227 * 1024, "shared memory");
-    if (cudaFuncSetAttribute(moe::ffn_kernel<P, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-        cudaSuccess)
+    if (P == moe::kDw) map_n16 = map_n;
+    // six stages of 32 KB with up to 256 experts, five beyond (their table takes the room)
+    constexpr size_t kSmem = 227 * 1024, kStage = 2 * moe::kHalf * moe::kSlice;
+    const size_t fixed = 1024 + sizeof(moe::Shared) + sizeof(int) * (4 * static_cast<size_t>(a.E) + 1);
+    a.ring_bytes = static_cast<int>((kSmem - fixed) / kStage * kStage);
+    static_assert(1024 + sizeof(moe::Shared) + sizeof(int) * 4097 + 5 * kStage <= kSmem, "shared memory");
+    if (cudaFuncSetAttribute(moe::ffn_kernel<P, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmem)) != cudaSuccess)
         return MOE_ERR_CUDA;
-    return moe_host::launch(moe::ffn_kernel<P, FP8>, dim3(static_cast<unsigned>(moe_host::num_sms())),
-                            dim3(moe::kThreads), smem, stream, map_a, map_a16, map_b, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(moe_host::num_sms() & ~1));
+    cfg.blockDim = dim3(moe::kThreads);
+    cfg.dynamicSmemBytes = fixed + a.ring_bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = moe_host::pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, moe::ffn_kernel<P, FP8>, map_m, map_n, map_n16, a) == cudaSuccess ? MOE_OK
+                                                                                                    : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -557,18 +615,18 @@ extern "C" MOE_API int moe_expert_ffn(const void* x, const float* x_scale, const
     a.timeout_ns = moe_host::timeout_ns();
     a.a_scale = x_scale;
     a.b_scale = w_scale;
-    a.N = I;
+    a.M = I;
     a.K = H;
     a.out = h;
     a.preact_out = preact;
-    const int rg = fp8 ? launch_product<moe::kGated, true>(x, w_gate_up, a, stream)
-                       : launch_product<moe::kGated>(x, w_gate_up, a, stream);
+    const int rg = fp8 ? launch_product<moe::kGated, true>(w_gate_up, x, a, stream)
+                       : launch_product<moe::kGated>(w_gate_up, x, a, stream);
     if (rg != MOE_OK) return rg;
     a.a_scale = a.b_scale = nullptr;
-    a.N = H;
+    a.M = H;
     a.K = I;
     a.out = y;
-    return launch_product<moe::kDown>(h, w_down, a, stream);
+    return launch_product<moe::kDown>(w_down, h, a, stream);
 }
 
 extern "C" MOE_API int moe_expert_ffn_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* h,
@@ -603,17 +661,17 @@ extern "C" MOE_API int moe_expert_ffn_backward(const uint16_t* dy, const uint16_
     a.timeout_ns = moe_host::timeout_ns();
     if (dx != nullptr || dw_gate_up != nullptr) {
         a.preact_in = preact;
-        a.N = I;
+        a.M = I;
         a.K = H;
         a.out = dgate_up;
-        rc = launch_product<moe::kDgate>(dy, w_down, a, stream);
+        rc = launch_product<moe::kDgate>(w_down, dy, a, stream);
         if (rc != MOE_OK) return rc;
     }
     if (dx != nullptr) {
-        a.N = H;
+        a.M = H;
         a.K = 2 * I;
         a.out = dx;
-        rc = launch_product<moe::kDx>(dgate_up, w_gate_up, a, stream);
+        rc = launch_product<moe::kDx>(w_gate_up, dgate_up, a, stream);
         if (rc != MOE_OK) return rc;
     }
     if (dw_gate_up != nullptr) {
