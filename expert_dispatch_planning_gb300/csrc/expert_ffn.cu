@@ -34,8 +34,9 @@
 // of dgate and dx, both sides of dw) it holds rows of 64 of the M or N index,
 // one for each k, and the instruction reads it transposed.  Slices that leave
 // an array are filled with zeros by the copy.  In dw a group's last slice runs
-// on into other rows, which may hold anything: warp 1 of each block zeroes
-// them in both operands before the instruction reads the stage.
+// on into other rows, which may hold anything: a further warp of each block
+// zeroes them in both operands.  It does so as soon as the slice is there,
+// while the instructions of the slices before it run.
 #include <cuda_fp8.h>
 
 #include "tensor_core.cuh"
@@ -51,6 +52,7 @@ constexpr int kSlice = 128;        // bytes of a stage's row
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kMendWarp = 2 + kEpilogueWarps;  // dw has one warp more
 constexpr int kChunk = 16;         // accumulator columns that a warp turns at a time
 constexpr int kTurnStride = 48;    // floats between a chunk's rows: 16 banks apart for the gated reads
 
@@ -64,6 +66,7 @@ struct FfnArgs {
     int64_t rows;
     int E, M, N, K;         // M: output channels; K: contraction length; dw: output M x N
     int ring_bytes;
+    int wide;               // dw: rows of whole 32-byte sectors
     uint16_t* out;
     float* preact_out;
     int64_t timeout_ns;
@@ -75,7 +78,7 @@ struct Shared {
         acc_empty[2];
     uint32_t tmem;
     int stop;               // the plan's status held an error
-    int scan[kThreads / 32], most[kThreads / 32];
+    int scan[kMendWarp + 1], most[kMendWarp + 1];
 };
 
 struct Tile {
@@ -260,12 +263,18 @@ __device__ __forceinline__ void epilogue_dw(const FfnArgs& a, const Tile& t, int
     uint32_t p[kChunk / 2];
 #pragma unroll
     for (int j = 0; j < kChunk; j += 2) p[j / 2] = pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+    if (a.wide) {  // whole 32-byte sectors
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out), "r"(p[0]), "r"(p[1]), "r"(p[2]),
+                     "r"(p[3]), "r"(p[4]), "r"(p[5]), "r"(p[6]), "r"(p[7])
+                     : "memory");
+        return;
+    }
     st_v4(out, make_uint4(p[0], p[1], p[2], p[3]));
     if (c0 + 8 < t.n) st_v4(out + 8, make_uint4(p[4], p[5], p[6], p[7]));
 }
 
 template <int P, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(P == kDw ? kThreads + 32 : kThreads, 1)
     ffn_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_n,
                const __grid_constant__ CUtensorMap map_n16, const FfnArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -286,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh->full[i], 1);
             mbar_init(&sh->empty[i], 1);
             mbar_init(&sh->tail_full[i], 1);
-            mbar_init(&sh->tail_ready[i], 1);
+            mbar_init(&sh->tail_ready[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->acc_full[i], 1);
@@ -301,7 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) sh->stop = ld_volatile_s32(a.status) != 0;
 
     // ---- the groups: row tiles before each expert, and the longest group
-    const int per = (a.E + kThreads - 1) / kThreads;
+    const int threads = P == kDw ? kThreads + 32 : kThreads, warps = threads / 32;
+    const int per = (a.E + threads - 1) / threads;
     int mine = 0, longest = 0;
     for (int e = tid * per; e < min(a.E, (tid + 1) * per); ++e) {
         const int64_t f = __ldg(a.cu + e), c = __ldg(a.count + e), p = c == 0 ? 0 : __ldg(a.cu + e + 1) - f;
@@ -326,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int row_tiles = 0;
     before -= mine;
     longest = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < warps; ++i) {
         if (i < warp) before += sh->scan[i];
         row_tiles += sh->scan[i];
         longest = max(longest, sh->most[i]);
@@ -379,16 +389,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = wait(a, &sh->empty[s], phase ^ 1u))) break;
                     uint8_t* sm = ring + s * stage_bytes;
                     uint8_t* sn = sm + kHalf * kSlice;
-                    // the second block's copies are counted by the first one's barrier,
-                    // but for a last slice that it has to mend first
-                    const bool tail = P == kDw && k + 1 == t.slices && (t.count & 15) != 0;
+                    // both blocks' copies are counted by the first one's barrier, but those
+                    // of a slice that has to be mended by each block's own
                     uint32_t bar;
-                    if (rank == 0) {
-                        mbar_arrive_expect_tx(&sh->full[s], tail ? bytes : 2 * bytes);
-                        bar = smem_addr(&sh->full[s]);
-                    } else if (tail) {
+                    if (P == kDw && k + 1 == t.slices && (t.count & 15) != 0) {
                         mbar_arrive_expect_tx(&sh->tail_full[s], bytes);
                         bar = smem_addr(&sh->tail_full[s]);
+                    } else if (rank == 0) {
+                        mbar_arrive_expect_tx(&sh->full[s], 2 * bytes);
+                        bar = smem_addr(&sh->full[s]);
                     } else {
                         bar = leader_addr(&sh->full[s]);
                     }
@@ -424,70 +433,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (run && warp == 1 && (rank == 0 || P == kDw)) {
-        int s = 0, buf = 0;
-        uint32_t phase = 0, acc_phase = 0, tails = 0;  // tails: a bit a stage, how often it held a last slice
-        bool ok = true;
-        for (int64_t i = pair; i < w.tiles && ok; i += pairs) {
+    } else if (run && warp == 1 && rank == 0) {
+        // One thread from end to end, the four instructions of a slice unrolled:
+        // gaps between them cost (a loop over a slice's steps: dw 1650 us, this 1430
+        // at 32768 rows, H = I = 4096, 8 experts).
+        if (lane == 0) {
+            int s = 0, buf = 0;
+            uint32_t acc_phase = 0, full_phase = 0, tail_phase = 0;  // the latter two: a bit a stage
+            bool ok = true;
+            for (int64_t i = pair; i < w.tiles && ok; i += pairs) {
+                const Tile t = locate<P>(w, i);
+                if (t.slices == 0) continue;
+                const uint32_t desc = mma_desc(FP8 ? 0u : 1u, kMmn, kNmn, kTile, (t.n + 15) & ~15);
+                const uint32_t acc = tmem + buf * kTile;
+                if (!(ok = wait(a, &sh->acc_empty[buf], acc_phase ^ 1u))) break;
+                for (int k = 0; k < t.slices; ++k) {
+                    const bool last = k + 1 == t.slices;
+                    if (P == kDw && last && (t.count & 15) != 0) {
+                        if (!(ok = wait(a, &sh->tail_ready[s], (tail_phase >> s) & 1u))) break;
+                        tail_phase ^= 1u << s;
+                    } else {
+                        if (!(ok = wait(a, &sh->full[s], (full_phase >> s) & 1u))) break;
+                        full_phase ^= 1u << s;
+                    }
+                    tc_fence_after();
+                    const uint32_t sm = smem_addr(ring + s * stage_bytes);
+                    const uint64_t dm = operand_desc(sm, kMmn ? 8192 : 16, 1024);
+                    const uint64_t dn = operand_desc(sm + kHalf * kSlice, kNmn ? 8192 : 16, 1024);
+                    constexpr int kStepM = (kMmn ? 2048 : 32) >> 4, kStepN = (kNmn ? 2048 : 32) >> 4;
+                    // 32 bytes of k, or 16 rows of it, an instruction; dw's last slice may have fewer
+                    const int steps = P == kDw && last ? ((t.count - 1) % 64) / 16 + 1 : 4;
+                    if (P != kDw || steps == 4) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma<FP8>(acc, dm + j * kStepM, dn + j * kStepN, desc, k > 0 || j > 0);
+                    } else {
+                        for (int j = 0; j < steps; ++j)
+                            mma<FP8>(acc, dm + j * kStepM, dn + j * kStepN, desc, k > 0 || j > 0);
+                    }
+                    mma_commit(&sh->empty[s]);
+                    if (last) mma_commit(&sh->acc_full[buf]);
+                    if (++s == stages) s = 0;
+                }
+                if ((buf ^= 1) == 0) acc_phase ^= 1u;
+            }
+        }
+        __syncwarp();
+    } else if (P == kDw && run && warp == kMendWarp) {
+        int s = 0;
+        uint32_t tail_phase = 0;
+        for (int64_t i = pair; i < w.tiles; i += pairs) {
             const Tile t = locate<P>(w, i);
             if (t.slices == 0) continue;
-            const int nb = (t.n + 15) & ~15;
-            const uint32_t desc = mma_desc(FP8 ? 0u : 1u, kMmn, kNmn, kTile, nb);
-            if (rank == 0) {
-                if (!(ok = wait(a, &sh->acc_empty[buf], acc_phase ^ 1u))) break;
-                tc_fence_after();
+            s = (s + t.slices - 1) % stages;
+            if ((t.count & 15) != 0) {
+                if (!wait(a, &sh->tail_full[s], (tail_phase >> s) & 1u)) break;
+                tail_phase ^= 1u << s;
+                // rows from the group's end to a multiple of 16; the N side's boxes of
+                // 64 columns follow the M side's two in the stage
+                const int valid = t.count & 63, chunks = (((valid + 15) & ~15) - valid) * 8;
+                const int boxes = 2 + (((t.n + 15) & ~15) / 2 + 63) / 64;
+                uint8_t* at = ring + s * stage_bytes + valid * kSlice;
+                for (int j = lane; j < boxes * chunks; j += 32)
+                    *reinterpret_cast<uint4*>(at + j / chunks * 8192 + j % chunks * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_leader(&sh->tail_ready[s]);
             }
-            for (int k = 0; k < t.slices; ++k) {
-                uint8_t* sm = ring + s * stage_bytes;
-                uint8_t* sn = sm + kHalf * kSlice;
-                int steps = 4;
-                bool tail = false;
-                if constexpr (P == kDw) {
-                    const int valid = min(64, t.count - 64 * k);
-                    steps = (valid + 15) / 16;
-                    tail = k + 1 == t.slices && (t.count & 15) != 0;
-                    if (rank == 0 || tail)
-                        if (!(ok = wait(a, rank == 0 ? &sh->full[s] : &sh->tail_full[s],
-                                        rank == 0 ? phase : (tails >> s) & 1u)))
-                            break;
-                    if (tail) {  // rows past the group: zero in both operands
-                        const int boxes = 2 + (nb / 2 + 63) / 64, chunks = (steps * 16 - valid) * 8;
-                        for (int j = lane; j < boxes * chunks; j += 32)  // the N side's boxes follow the M side's two
-                            *reinterpret_cast<uint4*>(sm + j / chunks * 8192 + valid * kSlice + j % chunks * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (rank != 0) {
-                            if (lane == 0) mbar_arrive_leader(&sh->tail_ready[s]);
-                        } else if (!(ok = wait(a, &sh->tail_ready[s], (tails >> s) & 1u))) {
-                            break;
-                        }
-                        tails ^= 1u << s;
-                    }
-                } else {
-                    if (!(ok = wait(a, &sh->full[s], phase))) break;
-                }
-                if (rank == 0) {
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t dm = operand_desc(smem_addr(sm), kMmn ? 8192 : 16, 1024);
-                        const uint64_t dn = operand_desc(smem_addr(sn), kNmn ? 8192 : 16, 1024);
-                        for (int j = 0; j < steps; ++j)  // 32 bytes of k, or 16 rows of it
-                            mma<FP8>(tmem + buf * kTile, dm + j * ((kMmn ? 2048 : 32) >> 4),
-                                     dn + j * ((kNmn ? 2048 : 32) >> 4), desc, k > 0 || j > 0);
-                        mma_commit(&sh->empty[s]);
-                        if (k + 1 == t.slices) mma_commit(&sh->acc_full[buf]);
-                    }
-                    __syncwarp();
-                }
-                if (++s == stages) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-            }
-            if ((buf ^= 1) == 0) acc_phase ^= 1u;
+            if (++s == stages) s = 0;
         }
-    } else if (run && warp >= 2) {
+    } else if (run && warp >= 2 && warp < kMendWarp) {
         const int quarter = warp & 3;           // the lanes of tensor memory that a warp may read
         const int turn = (warp - 2) >> 2;       // two warps a quarter take every other chunk
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -566,13 +581,14 @@ int launch_product(const void* weights, const void* row_data, moe::FfnArgs a, cu
     constexpr size_t kSmem = 227 * 1024, kStage = 2 * moe::kHalf * moe::kSlice;
     const size_t fixed = 1024 + sizeof(moe::Shared) + sizeof(int) * (4 * static_cast<size_t>(a.E) + 1);
     a.ring_bytes = static_cast<int>((kSmem - fixed) / kStage * kStage);
+    a.wide = a.N % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     static_assert(1024 + sizeof(moe::Shared) + sizeof(int) * 4097 + 5 * kStage <= kSmem, "shared memory");
     if (cudaFuncSetAttribute(moe::ffn_kernel<P, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmem)) != cudaSuccess)
         return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(moe_host::num_sms() & ~1));
-    cfg.blockDim = dim3(moe::kThreads);
+    cfg.blockDim = dim3(P == moe::kDw ? moe::kThreads + 32 : moe::kThreads);
     cfg.dynamicSmemBytes = fixed + a.ring_bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

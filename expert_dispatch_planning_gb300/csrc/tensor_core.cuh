@@ -30,17 +30,19 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
 }
-// mbar_wait_bounded for arrivals from the other block.
+// mbar_wait_bounded for arrivals from the other block.  The thread sleeps in
+// the barrier unit for up to 20 us at a time: ten waiting warps that poll take
+// issue slots and shared-memory cycles from the copies and the instructions.
 __device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
     while (true) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
             : "memory");
         if (ok) return true;
         const uint64_t now = globaltimer_ns();
