@@ -96,6 +96,8 @@ class MoeError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load the in-tree library; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

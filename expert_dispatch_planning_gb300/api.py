@@ -17,17 +17,26 @@ SCORING = {"softmax": _lib.MOE_SCORING_SOFTMAX, "sigmoid": _lib.MOE_SCORING_SIGM
            0: 0, 1: 1}
 
 
-def _stream(stream=None) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+# Handles and addresses go to the library as plain integers: small calls are
+# bound by this file (a call with a handful of outputs spent 24 of 28 us here;
+# torch.cuda.current_stream() alone 11 of them).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _ptr(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+def _stream(stream=None) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _need(t, dtype, shape, name):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError("%s must be a contiguous CUDA %s tensor of shape %s (got %s %s)" % (
             name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
 
@@ -329,11 +338,13 @@ def _plan_struct(p, names):
     c = getattr(p, "c_struct", None)
     if c is not None:
         return ctypes.byref(c)
+    c = MoePlanOut()
     for k in names:
         t = getattr(p, k)
-        if t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda:
+        if t.dtype is not torch.int32 or not t.is_contiguous() or not t.is_cuda:
             raise ValueError("%s must be a contiguous CUDA int32 tensor" % k)
-    return ctypes.byref(MoePlanOut(**{k: getattr(p, k).data_ptr() for k in names}))
+        setattr(c, k, t.data_ptr())
+    return ctypes.byref(c)
 
 
 @dataclass
@@ -368,20 +379,24 @@ def residual_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
         _need(residual, residual.dtype, (N, H), "residual")
         if residual_out is None:
             residual_out = torch.empty_like(residual)
-        _need(residual_out, residual.dtype, (N, H), "residual_out")
+        else:
+            _need(residual_out, residual.dtype, (N, H), "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if out is None:
-        out = torch.empty((N, H), dtype=torch.bfloat16, device=dev)
-    _need(out, torch.bfloat16, (N, H), "out")
+        out = torch.empty_like(x)
+    else:
+        _need(out, torch.bfloat16, (N, H), "out")
     rstd = torch.empty(N, dtype=torch.float32, device=dev)
     if quantize:
         if q is None:
             q = torch.empty((N, H), dtype=torch.float8_e4m3fn, device=dev)
+        else:
+            _need(q, torch.float8_e4m3fn, (N, H), "q")
         if q_scale is None:
             q_scale = torch.empty(N, dtype=torch.float32, device=dev)
-        _need(q, torch.float8_e4m3fn, (N, H), "q")
-        _need(q_scale, torch.float32, (N,), "q_scale")
+        else:
+            _need(q_scale, torch.float32, (N,), "q_scale")
     elif q is not None or q_scale is not None:
         raise ValueError("q and q_scale need quantize=True")
     rc = load().moe_residual_norm(_ptr(x), _ptr(residual), _DTYPE[torch.bfloat16 if residual is None else residual.dtype],
@@ -455,12 +470,14 @@ def expert_ffn(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, p
         raise ValueError("the plan has %d experts, w_gate_up %d" % (p.tokens_per_expert.numel(), E))
     if h is None:
         h = torch.empty((rows, I), dtype=torch.bfloat16, device=x.device)
-    _need(h, torch.bfloat16, (rows, I), "h")
+    else:
+        _need(h, torch.bfloat16, (rows, I), "h")
     if preact is not None:
         _need(preact, torch.float32, (rows, 2, I), "preact")
     if out is None:
         out = torch.empty((rows, H), dtype=torch.bfloat16, device=x.device)
-    _need(out, torch.bfloat16, (rows, H), "out")
+    else:
+        _need(out, torch.bfloat16, (rows, H), "out")
     rc = load().moe_expert_ffn(_ptr(x), _ptr(x_scale), _ptr(w_gate_up), _ptr(w_scale), _ptr(w_down), rows, E, H, I,
                                _DTYPE[x.dtype], _plan_struct(p, ("cu_seqlens", "tokens_per_expert", "status")), _ptr(h),
                                _ptr(preact), _ptr(out), _stream(stream))
@@ -491,11 +508,13 @@ def expert_ffn_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, prea
         raise ValueError("the plan has %d experts, w_gate_up %d" % (p.tokens_per_expert.numel(), E))
     if dgate_up is None:
         dgate_up = torch.empty((rows, 2, I), dtype=bf16, device=x.device)
-    _need(dgate_up, bf16, (rows, 2, I), "dgate_up")
+    else:
+        _need(dgate_up, bf16, (rows, 2, I), "dgate_up")
     if need_dx:
         if dx is None:
-            dx = torch.empty((rows, H), dtype=bf16, device=x.device)
-        _need(dx, bf16, (rows, H), "dx")
+            dx = torch.empty_like(x)
+        else:
+            _need(dx, bf16, (rows, H), "dx")
     elif dx is not None:
         raise ValueError("dx is given but need_dx is False")
     dwgu = torch.empty_like(w_gate_up) if need_dw else None
@@ -523,11 +542,13 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor, 
     _need(topk_w, torch.float32, (N, K), "topk_w")
     _need(p.dst, torch.int32, (N, K), "dst")
     if dy is None:
-        dy = torch.empty((rows, H), dtype=torch.bfloat16, device=y.device)
+        dy = torch.empty_like(y)
+    else:
+        _need(dy, torch.bfloat16, (rows, H), "dy")
     if dw is None:
-        dw = torch.empty((N, K), dtype=torch.float32, device=y.device)
-    _need(dy, torch.bfloat16, (rows, H), "dy")
-    _need(dw, torch.float32, (N, K), "dw")
+        dw = torch.empty_like(topk_w)
+    else:
+        _need(dw, torch.float32, (N, K), "dw")
     rc = load().moe_combine_backward(_ptr(dout), _ptr(y), _ptr(topk_w), N, K, H, E, rows,
                                      _plan_struct(p, ("dst", "zero_fill_ranges", "status")), _ptr(dy), _ptr(dw),
                                      _stream(stream))

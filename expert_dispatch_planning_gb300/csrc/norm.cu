@@ -198,8 +198,18 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_backward_kernel(c
         if (row >= a.N) break;
         const int64_t at = row * a.H;
         const float rstd = __ldg(a.rstd + row);
-        float xhat[VPT][8], t[VPT][8];
+        float xhat[VPT][8], t[VPT][8], d[VPT][8];  // ds is asked for with the rest, before the row's sum is waited for
         float dot = 0.f;
+        if (a.ds != nullptr) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (lane + i * lanes < nvec) load8(static_cast<const S*>(a.ds) + at, lane + i * lanes, d[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[i][j] = 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = lane + i * lanes;
@@ -220,15 +230,10 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_backward_kernel(c
         for (int i = 0; i < VPT; ++i) {
             const int c = lane + i * lanes;
             if (c < nvec) {
-                float d[8];
-                if (a.ds != nullptr) load8(static_cast<const S*>(a.ds) + at, c, d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float v = rstd * (t[i][j] - xhat[i][j] * mean);
-                    d[j] = a.ds != nullptr ? d[j] + v : v;
-                }
-                store8(a.dx + at, c, d);
-                if (a.dres != nullptr) store8(a.dres + at, c, d);
+                for (int j = 0; j < 8; ++j) d[i][j] += rstd * (t[i][j] - xhat[i][j] * mean);
+                store8(a.dx + at, c, d[i]);
+                if (a.dres != nullptr) store8(a.dres + at, c, d[i]);
             }
         }
     }
@@ -255,24 +260,22 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_backward_kernel(c
     }
 }
 
-// dweight[h] = sum of the blocks' partials: 32 columns a block, 8 rows of
-// threads that each add every 8th partial, joined in shared memory.
-__global__ void __launch_bounds__(256) norm_dweight_kernel(const float* partial, int blocks, int H, float* dweight) {
-    __shared__ float sh[8][33];
+// dweight[h] = sum of the blocks' partials: 32 columns a block; each of its 32
+// warps adds every 32nd partial, and the warps' sums are joined in order.
+__global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* partial, int blocks, int H, float* dweight) {
+    __shared__ float sh[32][33];
     pdl_wait();
     pdl_trigger();
     const int h = blockIdx.x * 32 + threadIdx.x, g = threadIdx.y;
     float v = 0.f;
-    if (h < H)
-        for (int b = g; b < blocks; b += 8) v += partial[static_cast<int64_t>(b) * H + h];
+    if (h < H) {
+#pragma unroll 4
+        for (int b = g; b < blocks; b += 32) v += partial[static_cast<int64_t>(b) * H + h];
+    }
     sh[g][threadIdx.x] = v;
     __syncthreads();
-    if (g == 0 && h < H) {
-        float t = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) t += sh[k][threadIdx.x];
-        dweight[h] = t;
-    }
+    v = warp_sum(sh[threadIdx.x][g]);  // warp g joins column g
+    if (threadIdx.x == 0 && blockIdx.x * 32 + g < H) dweight[blockIdx.x * 32 + g] = v;
 }
 
 }  // namespace moe
@@ -395,6 +398,6 @@ extern "C" MOE_API int moe_residual_norm_backward(const uint16_t* dy, const void
         }
     }
     if (rc != MOE_OK || dweight == nullptr) return rc;
-    return moe_host::launch(moe::norm_dweight_kernel, dim3(static_cast<unsigned>((H + 31) / 32)), dim3(32, 8), 0,
+    return moe_host::launch(moe::norm_dweight_kernel, dim3(static_cast<unsigned>((H + 31) / 32)), dim3(32, 32), 0,
                             stream, static_cast<const float*>(a.partial), blocks, H, dweight);
 }
