@@ -9,9 +9,14 @@
 // partial row a block, and a second launch adds the partials in block order,
 // so that the result does not depend on scheduling.
 //
-// Memory bound: every element is read once and written once.  A row belongs
-// to one warp when 32 lanes hold it (H <= 512), else to a whole block with 8,
-// 16 or 32 elements a thread.
+// Memory bound: every element is read once and written once.  Three forms:
+//   - H <= 512: a warp a row, four rows a block;
+//   - few rows, or very wide ones: a block a row, 8, 16 or 32 elements a thread;
+//   - else a ring: blocks that stay, each thread copying its own columns of the
+//     next rows into its own places in shared memory (cp.async) while the block
+//     works on a row, so that the row's reductions never empty the memory
+//     pipeline.  A thread reads only what it copied, so the ring needs no
+//     barrier; the row's sums take one each.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -74,7 +79,20 @@ __device__ __forceinline__ void load_weight8(const void* w, int f32, int c, floa
     }
 }
 
-// RES: 0 no residual, else its element type.
+// The 8-bit output's scale of a row and the values' rounding: one reciprocal a
+// row; rows so small that it would overflow divide instead.
+struct Quantum {
+    float scale, inv;
+    bool tiny;
+    __device__ __forceinline__ explicit Quantum(float amax)
+        : scale(amax > 0.f ? amax / kE4m3Max : 1.f / kE4m3Max), inv(1.f / scale), tiny(scale < 1e-37f) {}
+    __device__ __forceinline__ uint32_t two(float lo, float hi) const {
+        const float2 v = tiny ? make_float2(lo / scale, hi / scale) : make_float2(lo * inv, hi * inv);
+        return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    }
+};
+
+// RES: 0 no residual, 1 bf16, 2 fp32.
 template <int VPT, bool WARP, int RES>
 __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_kernel(const NormArgs a) {
     __shared__ float buf[32];
@@ -134,25 +152,15 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_kernel(const Norm
     }
     if (a.q == nullptr) return;
     amax = row_reduce<WARP, true>(amax, buf);
-    const float scale = amax > 0.f ? amax / kE4m3Max : 1.f / kE4m3Max;
-    if (lane == 0) a.q_scale[row] = scale;
-    // one reciprocal a row; rows so small that it would overflow divide instead
-    const bool tiny = scale < 1e-37f;
-    const float inv = 1.f / scale;
+    const Quantum q(amax);
+    if (lane == 0) a.q_scale[row] = q.scale;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = lane + i * lanes;
-        if (c < nvec) {
-            uint32_t out[2] = {0u, 0u};
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const float2 v = tiny ? make_float2(s[i][j] / scale, s[i][j + 1] / scale)
-                                      : make_float2(s[i][j] * inv, s[i][j + 1] * inv);
-                out[j / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3))
-                              << (16 * ((j / 2) & 1));
-            }
-            *reinterpret_cast<uint2*>(a.q + at + 8 * static_cast<int64_t>(c)) = make_uint2(out[0], out[1]);
-        }
+        if (c < nvec)
+            *reinterpret_cast<uint2*>(a.q + at + 8 * static_cast<int64_t>(c)) =
+                make_uint2(q.two(s[i][0], s[i][1]) | q.two(s[i][2], s[i][3]) << 16,
+                           q.two(s[i][4], s[i][5]) | q.two(s[i][6], s[i][7]) << 16);
     }
 }
 
@@ -260,6 +268,233 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_backward_kernel(c
     }
 }
 
+// ---------------------------------------------------------------- ring
+// A thread owns groups of four columns, t, t + T, ...: 8 bytes of a bf16 row,
+// 16 of an fp32 one, neighbouring threads side by side.
+__device__ __forceinline__ void cp_async_group(uint16_t* dst, const uint16_t* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_group(float* dst, const float* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float (&f)[4]) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+}
+__device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void load_weight4(const void* w, int f32, int h, float (&f)[4]) {
+    if (f32) load4(static_cast<const float*>(w) + h, f);
+    else load4(static_cast<const uint16_t*>(w) + h, f);
+}
+
+// The block's sum or maximum with one barrier: `buf` holds two sets of 32
+// floats that a caller uses in turn.
+template <bool MAX>
+__device__ __forceinline__ float block_reduce(float v, float* buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float t = __shfl_xor_sync(FULL_MASK, v, o);
+        v = MAX ? fmaxf(v, t) : v + t;
+    }
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = (threadIdx.x & 31) < (blockDim.x >> 5) ? buf[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float t = __shfl_xor_sync(FULL_MASK, v, o);
+        v = MAX ? fmaxf(v, t) : v + t;
+    }
+    return v;
+}
+
+constexpr int kRingThreads = 1024;
+constexpr int kRingGroups = 2;  // groups of four columns a thread at most: H <= 8192
+
+// R: the residual's element type (uint16_t also stands for none).
+template <int SLOTS, typename R, bool RES>
+__global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];  // [SLOTS][x row, residual row]
+    __shared__ float buf[2][2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int T = blockDim.x, H = a.H;
+    const uint32_t slot_bytes = static_cast<uint32_t>(H) * (RES ? 2 + sizeof(R) : 2);
+    const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.N / gridDim.x;
+    const int64_t end = (static_cast<int64_t>(blockIdx.x) + 1) * a.N / gridDim.x;
+    auto fetch = [&](int64_t row) {
+        if (row < end) {
+            uint16_t* x = reinterpret_cast<uint16_t*>(smem + (row - begin) % SLOTS * slot_bytes);
+            R* r = reinterpret_cast<R*>(x + H);
+#pragma unroll
+            for (int i = 0; i < kRingGroups; ++i) {
+                const int h = 4 * (threadIdx.x + i * T);
+                if (h < H) {
+                    cp_async_group(x + h, a.x + row * H + h);
+                    if constexpr (RES) cp_async_group(r + h, static_cast<const R*>(a.residual) + row * H + h);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float w[kRingGroups][4];
+#pragma unroll
+    for (int i = 0; i < kRingGroups; ++i) {
+        const int h = 4 * (threadIdx.x + i * T);
+        if (h < H) load_weight4(a.weight, a.weight_f32, h, w[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < SLOTS - 1; ++j) fetch(begin + j);
+    for (int64_t row = begin; row < end; ++row) {
+        fetch(row + SLOTS - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+        const uint16_t* x = reinterpret_cast<const uint16_t*>(smem + (row - begin) % SLOTS * slot_bytes);
+        const R* r = reinterpret_cast<const R*>(x + H);
+        const int64_t at = row * H;
+        float(*sums)[32] = buf[row & 1];
+        float s[kRingGroups][4];
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) {
+                load4(x + h, s[i]);
+                if constexpr (RES) {
+                    float q[4];
+                    load4(r + h, q);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[i][j] += q[j];
+                    if (a.residual_out != nullptr) store4(static_cast<R*>(a.residual_out) + at + h, s[i]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float t = s[i][j] * a.down;
+                    ss = fmaf(t, t, ss);
+                }
+            }
+        }
+        ss = block_reduce<false>(ss, sums[0]);
+        const float rstd = 1.f / sqrtf(fmaf(ss, a.mean, a.eps));
+        if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = s[i][j] * rstd * w[i][j];
+                    amax = fmaxf(amax, fabsf(s[i][j]));
+                }
+                if (a.y != nullptr) store4(a.y + at + h, s[i]);
+            }
+        }
+        if (a.q == nullptr) continue;
+        amax = block_reduce<true>(amax, sums[1]);
+        const Quantum q(amax);
+        if (threadIdx.x == 0) a.q_scale[row] = q.scale;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H)
+                *reinterpret_cast<uint32_t*>(a.q + at + h) = q.two(s[i][0], s[i][1]) | q.two(s[i][2], s[i][3]) << 16;
+        }
+    }
+}
+
+template <int SLOTS, typename S, bool DS>
+__global__ void __launch_bounds__(kRingThreads) norm_backward_ring_kernel(const NormBackwardArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];  // [SLOTS][dy row, s row, ds row]
+    __shared__ float buf[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int T = blockDim.x, H = a.H;
+    const uint32_t slot_bytes = static_cast<uint32_t>(H) * (2 + (DS ? 2 : 1) * sizeof(S));
+    const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.N / gridDim.x;
+    const int64_t end = (static_cast<int64_t>(blockIdx.x) + 1) * a.N / gridDim.x;
+    auto fetch = [&](int64_t row) {
+        if (row < end) {
+            uint16_t* dy = reinterpret_cast<uint16_t*>(smem + (row - begin) % SLOTS * slot_bytes);
+            S* s = reinterpret_cast<S*>(dy + H);
+#pragma unroll
+            for (int i = 0; i < kRingGroups; ++i) {
+                const int h = 4 * (threadIdx.x + i * T);
+                if (h < H) {
+                    cp_async_group(dy + h, a.dy + row * H + h);
+                    cp_async_group(s + h, static_cast<const S*>(a.s) + row * H + h);
+                    if constexpr (DS) cp_async_group(s + H + h, static_cast<const S*>(a.ds) + row * H + h);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float w[kRingGroups][4], acc[kRingGroups][4];
+#pragma unroll
+    for (int i = 0; i < kRingGroups; ++i) {
+        const int h = 4 * (threadIdx.x + i * T);
+        if (h < H) load_weight4(a.weight, a.weight_f32, h, w[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < SLOTS - 1; ++j) fetch(begin + j);
+    float next_rstd = begin < end ? __ldg(a.rstd + begin) : 0.f;
+    for (int64_t row = begin; row < end; ++row) {
+        fetch(row + SLOTS - 1);
+        const float rstd = next_rstd;
+        if (row + 1 < end) next_rstd = __ldg(a.rstd + row + 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+        const uint16_t* dy = reinterpret_cast<const uint16_t*>(smem + (row - begin) % SLOTS * slot_bytes);
+        const S* s = reinterpret_cast<const S*>(dy + H);
+        const int64_t at = row * H;
+        float xhat[kRingGroups][4], t[kRingGroups][4];
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) {
+                load4(dy + h, t[i]);
+                load4(s + h, xhat[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    xhat[i][j] *= rstd;
+                    acc[i][j] = fmaf(t[i][j], xhat[i][j], acc[i][j]);
+                    t[i][j] *= w[i][j];
+                    dot = fmaf(t[i][j], xhat[i][j], dot);
+                }
+            }
+        }
+        const float mean = block_reduce<false>(dot, buf[row & 1]) / static_cast<float>(H);
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (DS) load4(s + H + h, d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[j] += rstd * (t[i][j] - xhat[i][j] * mean);
+                store4(a.dx + at + h, d);
+                if (a.dres != nullptr) store4(a.dres + at + h, d);
+            }
+        }
+    }
+    if (a.partial == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < kRingGroups; ++i) {
+        const int h = 4 * (threadIdx.x + i * T);
+        if (h < H) store4(a.partial + static_cast<int64_t>(blockIdx.x) * H + h, acc[i]);
+    }
+}
+
 // dweight[h] = sum of the blocks' partials: 32 columns a block; each of its 32
 // warps adds every 32nd partial, and the warps' sums are joined in order.
 __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* partial, int blocks, int H, float* dweight) {
@@ -306,7 +541,57 @@ int launch_backward(const moe::NormBackwardArgs& a, bool f32, dim3 grid, dim3 bl
     return moe_host::launch(moe::norm_backward_kernel<VPT, WARP, uint16_t>, grid, block, smem, stream, a);
 }
 
-// Blocks of the backward kernel: four an SM, no more than there are rows.
+// The ring form: `slot` bytes a row, two to eight slots, blocks as many as
+// their rings and threads fit an SM.  Taken when every block gets a few rows
+// (fewer would only wait for their own) and a row has enough columns to keep
+// its barrier cheap.
+struct Ring {
+    int slots = 0, threads = 0, blocks = 0;  // slots = 0: not taken
+    size_t smem = 0;
+};
+Ring ring_for(int N, int H, size_t slot) {
+    constexpr size_t kSmem = 220 * 1024;
+    Ring r;
+    if (H <= 512 || H > 4 * moe::kRingGroups * moe::kRingThreads || 2 * slot > kSmem) return r;
+    const int slots = 8 * slot <= kSmem / 2 ? 8 : 4 * slot <= kSmem ? 4 : 2;
+    const int per_thread = 4 * moe::kRingGroups;
+    const int threads = (H + 32 * per_thread - 1) / (32 * per_thread) * 32;
+    const int by_smem = static_cast<int>(kSmem / (slots * slot)), by_threads = 1536 / threads;
+    const int per_sm = by_smem < by_threads ? by_smem : by_threads;
+    const int blocks = moe_host::num_sms() * (per_sm < 1 ? 1 : per_sm > 6 ? 6 : per_sm);
+    if (N < 4 * blocks) return r;
+    r.slots = slots;
+    r.threads = threads;
+    r.blocks = blocks;
+    r.smem = slots * slot;
+    return r;
+}
+
+template <typename Kernel, typename Args>
+int launch_ring(Kernel kernel, const Ring& r, const Args& a, cudaStream_t stream) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return moe_host::launch(kernel, dim3(static_cast<unsigned>(r.blocks)), dim3(static_cast<unsigned>(r.threads)), r.smem,
+                            stream, a);
+}
+
+template <int SLOTS>
+int launch_norm_ring(const Ring& r, const moe::NormArgs& a, int res, cudaStream_t stream) {
+    if (res == 0) return launch_ring(moe::norm_ring_kernel<SLOTS, uint16_t, false>, r, a, stream);
+    if (res == 1) return launch_ring(moe::norm_ring_kernel<SLOTS, uint16_t, true>, r, a, stream);
+    return launch_ring(moe::norm_ring_kernel<SLOTS, float, true>, r, a, stream);
+}
+
+template <int SLOTS>
+int launch_backward_ring(const Ring& r, const moe::NormBackwardArgs& a, bool f32, cudaStream_t stream) {
+    if (f32)
+        return a.ds != nullptr ? launch_ring(moe::norm_backward_ring_kernel<SLOTS, float, true>, r, a, stream)
+                               : launch_ring(moe::norm_backward_ring_kernel<SLOTS, float, false>, r, a, stream);
+    return a.ds != nullptr ? launch_ring(moe::norm_backward_ring_kernel<SLOTS, uint16_t, true>, r, a, stream)
+                           : launch_ring(moe::norm_backward_ring_kernel<SLOTS, uint16_t, false>, r, a, stream);
+}
+
+// Blocks of the backward kernel's other forms: four an SM, no more than there are rows.
 int backward_blocks(int N, int H) {
     const int64_t units = H <= 512 ? (static_cast<int64_t>(N) + 3) / 4 : N;
     const int64_t cap = static_cast<int64_t>(moe_host::num_sms()) * 4;
@@ -336,6 +621,10 @@ extern "C" MOE_API int moe_residual_norm(const uint16_t* x, const void* residual
     const moe::NormArgs a = {x, residual, weight,       weight_dtype == MOE_DTYPE_F32, N, H, eps, std::ldexp(1.f, -k),
                              mean, y,     residual_out, rstd,                          q, q_scale};
     const int res = residual == nullptr ? 0 : residual_dtype == MOE_DTYPE_F32 ? 2 : 1;
+    const Ring ring = ring_for(N, H, static_cast<size_t>(H) * (2 + 2 * res));
+    if (ring.slots == 8) return launch_norm_ring<8>(ring, a, res, stream);
+    if (ring.slots == 4) return launch_norm_ring<4>(ring, a, res, stream);
+    if (ring.slots == 2) return launch_norm_ring<2>(ring, a, res, stream);
     if (H <= 512) {
         const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(N) + 3) / 4)), block(128);
         return H <= 256 ? launch_norm<1, true>(a, res, grid, block, stream)
@@ -351,7 +640,8 @@ extern "C" MOE_API int moe_residual_norm(const uint16_t* x, const void* residual
 
 extern "C" MOE_API size_t moe_residual_norm_backward_workspace_size(int N, int H) {
     if (N < 0 || H < 8 || H % 8 != 0 || H > kMaxH) return 0;
-    const int blocks = backward_blocks(N, H);
+    int blocks = backward_blocks(N, H);  // the ring form may have more, of the narrowest type
+    if (N > blocks) blocks = N < 6 * moe_host::num_sms() ? N : 6 * moe_host::num_sms();
     return static_cast<size_t>(blocks > 0 ? blocks : 1) * H * sizeof(float);
 }
 
@@ -378,13 +668,19 @@ extern "C" MOE_API int moe_residual_norm_backward(const uint16_t* dy, const void
             return MOE_ERR_CUDA;
         return MOE_OK;
     }
-    const int blocks = backward_blocks(N, H);
+    const bool f32 = s_dtype == MOE_DTYPE_F32;
+    const size_t esize = f32 ? 4 : 2;
+    const Ring ring = ring_for(N, H, H * (2 + (ds != nullptr ? 2 : 1) * esize));
+    const int blocks = ring.slots > 0 ? ring.blocks : backward_blocks(N, H);
     const moe::NormBackwardArgs a = {dy, s, weight, weight_dtype == MOE_DTYPE_F32, rstd, ds, N, H, dx, dres,
                                      dweight != nullptr ? static_cast<float*>(workspace) : nullptr};
-    const bool f32 = s_dtype == MOE_DTYPE_F32;
     const dim3 grid(static_cast<unsigned>(blocks));
     int rc;
-    if (H <= 512) {
+    if (ring.slots > 0) {
+        rc = ring.slots == 8   ? launch_backward_ring<8>(ring, a, f32, stream)
+             : ring.slots == 4 ? launch_backward_ring<4>(ring, a, f32, stream)
+                               : launch_backward_ring<2>(ring, a, f32, stream);
+    } else if (H <= 512) {
         const dim3 block(128);
         const size_t smem = 4 * sizeof(float) * H;
         rc = H <= 256 ? launch_backward<1, true>(a, f32, grid, block, smem, stream)
