@@ -79,18 +79,24 @@ __device__ __forceinline__ void load_weight8(const void* w, int f32, int c, floa
     }
 }
 
-// The 8-bit output's scale of a row and the values' rounding: one reciprocal a
-// row; rows so small that it would overflow divide instead.
+// The 8-bit output's scale of a row and its values' rounding: a product with
+// the scale's reciprocal, both moved up by a power of two where the reciprocal
+// would overflow.
 struct Quantum {
-    float scale, inv;
-    bool tiny;
-    __device__ __forceinline__ explicit Quantum(float amax)
-        : scale(amax > 0.f ? amax / kE4m3Max : 1.f / kE4m3Max), inv(1.f / scale), tiny(scale < 1e-37f) {}
-    __device__ __forceinline__ uint32_t two(float lo, float hi) const {
-        const float2 v = tiny ? make_float2(lo / scale, hi / scale) : make_float2(lo * inv, hi * inv);
-        return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    float scale, up, inv;
+    __device__ __forceinline__ uint32_t round4(const float* v) const {
+        const float2 a = make_float2(v[0] * up * inv, v[1] * up * inv), b = make_float2(v[2] * up * inv, v[3] * up * inv);
+        return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3)) |
+               static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16;
     }
 };
+__device__ __forceinline__ Quantum quantum_of(float amax) {
+    Quantum q;
+    q.scale = (amax > 0.f ? amax : 1.f) * (1.f / kE4m3Max);
+    q.up = q.scale < 1e-30f ? 0x1p64f : 1.f;
+    q.inv = __fdividef(1.f, q.scale * q.up);
+    return q;
+}
 
 // RES: 0 no residual, 1 bf16, 2 fp32.
 template <int VPT, bool WARP, int RES>
@@ -127,7 +133,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_kernel(const Norm
         }
     }
     ss = row_reduce<WARP, false>(ss, buf);
-    const float rstd = 1.f / sqrtf(fmaf(ss, a.mean, a.eps));
+    const float rstd = rsqrtf(fmaf(ss, a.mean, a.eps));  // within 2^-22
     if (a.rstd != nullptr && lane == 0) a.rstd[row] = rstd;
 
     float amax = 0.f;
@@ -152,15 +158,14 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_kernel(const Norm
     }
     if (a.q == nullptr) return;
     amax = row_reduce<WARP, true>(amax, buf);
-    const Quantum q(amax);
+    const Quantum q = quantum_of(amax);
     if (lane == 0) a.q_scale[row] = q.scale;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = lane + i * lanes;
         if (c < nvec)
             *reinterpret_cast<uint2*>(a.q + at + 8 * static_cast<int64_t>(c)) =
-                make_uint2(q.two(s[i][0], s[i][1]) | q.two(s[i][2], s[i][3]) << 16,
-                           q.two(s[i][4], s[i][5]) | q.two(s[i][6], s[i][7]) << 16);
+                make_uint2(q.round4(s[i]), q.round4(s[i] + 4));
     }
 }
 
@@ -331,9 +336,9 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
     const uint32_t slot_bytes = static_cast<uint32_t>(H) * (RES ? 2 + sizeof(R) : 2);
     const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.N / gridDim.x;
     const int64_t end = (static_cast<int64_t>(blockIdx.x) + 1) * a.N / gridDim.x;
-    auto fetch = [&](int64_t row) {
+    auto fetch = [&](int64_t row, uint32_t slot) {
         if (row < end) {
-            uint16_t* x = reinterpret_cast<uint16_t*>(smem + (row - begin) % SLOTS * slot_bytes);
+            uint16_t* x = reinterpret_cast<uint16_t*>(smem + slot * slot_bytes);
             R* r = reinterpret_cast<R*>(x + H);
 #pragma unroll
             for (int i = 0; i < kRingGroups; ++i) {
@@ -353,11 +358,12 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
         if (h < H) load_weight4(a.weight, a.weight_f32, h, w[i]);
     }
 #pragma unroll
-    for (int j = 0; j < SLOTS - 1; ++j) fetch(begin + j);
-    for (int64_t row = begin; row < end; ++row) {
-        fetch(row + SLOTS - 1);
+    for (int j = 0; j < SLOTS - 1; ++j) fetch(begin + j, j);
+    uint32_t slot = 0;  // the row's
+    for (int64_t row = begin; row < end; ++row, slot = (slot + 1) % SLOTS) {
+        fetch(row + SLOTS - 1, (slot + SLOTS - 1) % SLOTS);
         asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
-        const uint16_t* x = reinterpret_cast<const uint16_t*>(smem + (row - begin) % SLOTS * slot_bytes);
+        const uint16_t* x = reinterpret_cast<const uint16_t*>(smem + slot * slot_bytes);
         const R* r = reinterpret_cast<const R*>(x + H);
         const int64_t at = row * H;
         float(*sums)[32] = buf[row & 1];
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
             }
         }
         ss = block_reduce<false>(ss, sums[0]);
-        const float rstd = 1.f / sqrtf(fmaf(ss, a.mean, a.eps));
+        const float rstd = rsqrtf(fmaf(ss, a.mean, a.eps));  // within 2^-22
         if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
         float amax = 0.f;
 #pragma unroll
@@ -400,13 +406,13 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
         }
         if (a.q == nullptr) continue;
         amax = block_reduce<true>(amax, sums[1]);
-        const Quantum q(amax);
+        const Quantum q = quantum_of(amax);
         if (threadIdx.x == 0) a.q_scale[row] = q.scale;
 #pragma unroll
         for (int i = 0; i < kRingGroups; ++i) {
             const int h = 4 * (threadIdx.x + i * T);
             if (h < H)
-                *reinterpret_cast<uint32_t*>(a.q + at + h) = q.two(s[i][0], s[i][1]) | q.two(s[i][2], s[i][3]) << 16;
+                *reinterpret_cast<uint32_t*>(a.q + at + h) = q.round4(s[i]);
         }
     }
 }
@@ -421,9 +427,9 @@ __global__ void __launch_bounds__(kRingThreads) norm_backward_ring_kernel(const 
     const uint32_t slot_bytes = static_cast<uint32_t>(H) * (2 + (DS ? 2 : 1) * sizeof(S));
     const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.N / gridDim.x;
     const int64_t end = (static_cast<int64_t>(blockIdx.x) + 1) * a.N / gridDim.x;
-    auto fetch = [&](int64_t row) {
+    auto fetch = [&](int64_t row, uint32_t slot) {
         if (row < end) {
-            uint16_t* dy = reinterpret_cast<uint16_t*>(smem + (row - begin) % SLOTS * slot_bytes);
+            uint16_t* dy = reinterpret_cast<uint16_t*>(smem + slot * slot_bytes);
             S* s = reinterpret_cast<S*>(dy + H);
 #pragma unroll
             for (int i = 0; i < kRingGroups; ++i) {
@@ -446,14 +452,15 @@ __global__ void __launch_bounds__(kRingThreads) norm_backward_ring_kernel(const 
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < SLOTS - 1; ++j) fetch(begin + j);
+    for (int j = 0; j < SLOTS - 1; ++j) fetch(begin + j, j);
+    uint32_t slot = 0;  // the row's
     float next_rstd = begin < end ? __ldg(a.rstd + begin) : 0.f;
-    for (int64_t row = begin; row < end; ++row) {
-        fetch(row + SLOTS - 1);
+    for (int64_t row = begin; row < end; ++row, slot = (slot + 1) % SLOTS) {
+        fetch(row + SLOTS - 1, (slot + SLOTS - 1) % SLOTS);
         const float rstd = next_rstd;
         if (row + 1 < end) next_rstd = __ldg(a.rstd + row + 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
-        const uint16_t* dy = reinterpret_cast<const uint16_t*>(smem + (row - begin) % SLOTS * slot_bytes);
+        const uint16_t* dy = reinterpret_cast<const uint16_t*>(smem + slot * slot_bytes);
         const S* s = reinterpret_cast<const S*>(dy + H);
         const int64_t at = row * H;
         float xhat[kRingGroups][4], t[kRingGroups][4];
