@@ -141,6 +141,13 @@ __device__ __forceinline__ void tensor_load_4d(void* dst, const CUtensorMap* map
         : "memory");
 }
 
+// Out of shared memory; clipped at the array's end, tracked by the thread's bulk groups.
+__device__ __forceinline__ void tensor_store_3d(const CUtensorMap* map, int x, int y, int z, const void* src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(smem_addr(src))
+                 : "memory");
+}
+
 }  // namespace moe
 
 // ---------------------------------------------------------------- host side
