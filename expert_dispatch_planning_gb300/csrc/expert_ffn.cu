@@ -23,8 +23,8 @@
 // Warp 0 of each block brings its operands' slices of 128 bytes of k into a
 // ring of shared-memory stages (tensor copies, 128-byte swizzle): 128 rows of
 // the M side and half of the tile's N side, of which the hardware shows both
-// halves to both SMs.  Warp 1 of the pair's first block issues the matrix
-// instructions.  Warps 2-9 read the accumulators (a warp sees 32 channels),
+// halves to both SMs.  In the pair's first block warp 10 waits for the slices
+// and warp 1 issues the matrix instructions.  Warps 2-9 read the accumulators (a warp sees 32 channels),
 // turn them through shared memory so that a row's channels lie side by side,
 // and write the output.  In the gated product every 32 rows of the M side are
 // 16 channels of the gate and the same 16 of the up projection, so that a
@@ -37,7 +37,7 @@
 // of dgate and dx, both sides of dw) it holds rows of 64 of the M or N index,
 // one for each k, and the instruction reads it transposed.  Slices that leave
 // an array are filled with zeros by the copy.  In dw a group's last slice runs
-// on into other rows, which may hold anything: warp 10 of each block zeroes
+// on into other rows, which may hold anything: warp 11 of each block zeroes
 // them in both operands as soon as the slice is there, while the instructions
 // of the slices before it run.
 #include <cuda_fp8.h>
@@ -54,16 +54,20 @@ constexpr int kHalf = 128;         // a block's part of it
 constexpr int kSlice = 128;        // bytes of a stage's row
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
-constexpr int kMendWarp = 2 + kEpilogueWarps;  // of launches with dw
+constexpr int kWatchWarp = 2 + kEpilogueWarps;
+constexpr int kMendWarp = kWatchWarp + 1;  // of launches with dw
+constexpr int kOrders = 16;        // tiles whose orders are kept: more than slices that can be ready
 constexpr int kChunk = 16;         // accumulator columns that a warp turns at a time
 
-__host__ __device__ constexpr int ffn_threads(int p) { return 64 + 32 * kEpilogueWarps + (p == kGrads ? 32 : 0); }
+__host__ __device__ constexpr int ffn_threads(int p) { return 96 + 32 * kEpilogueWarps + (p == kGrads ? 32 : 0); }
 __host__ __device__ constexpr int ffn_jobs(int p) { return p == kGrads ? 3 : 1; }
 
 struct Job {
     CUtensorMap map_m, map_n;
-    CUtensorMap map_x;      // the N side by 16 rows; dw: the output
+    CUtensorMap map_n32, map_n16;  // the N side by 32 and by 16 rows
+    CUtensorMap map_out;    // dw: the output
     int M, N, K;            // M: output channels; K: contraction length; dw: output M x N; M = 0: no work
+    int m_whole, n_whole;   // a block's part of a slice is one copy (see make_job)
     uint16_t* out;
 };
 
@@ -91,6 +95,8 @@ struct Shared {
     uint4 turn[kEpilogueWarps][256];  // a warp's 4 KB (1024-byte aligned: dw's boxes are swizzled)
     uint64_t full[kMaxStages], empty[kMaxStages], tail_full[kMaxStages], tail_ready[kMaxStages], acc_full[2],
         acc_empty[2];
+    uint4 order[kOrders];   // the tiles' instructions: descriptor, slices (0: the end), steps of the last, dw
+    uint32_t ready;         // slices that the instructions may use, counted from the launch's start
     uint32_t tmem;
     int stop;               // the plan's status held an error
     int scan[kMendWarp + 1], most[kMendWarp + 1];
@@ -230,9 +236,10 @@ struct Producer {
         for (; ok && turn.next < tiles.total; turn.next += turn.pairs) {
             const Tile t = tiles.at(g, turn.next, lane);
             const int mine = ((t.n + 15) & ~15) / 2;  // N-side rows (dw: columns) of a block
-            const int pieces = P == kDw ? (mine + 63) / 64 : mine > 64 ? 0 : (mine + 15) / 16;
-            const uint32_t bytes =
-                kHalf * kSlice + (P == kDw ? pieces * 8192 : pieces ? pieces * 16 * kSlice : kHalf * kSlice);
+            // the N side's copies: 128 rows, or 32 or 16 at a time (dw: 128 columns, or 64 at a time)
+            const int piece = P == kDw ? (job.n_whole ? 128 : 64) : mine > 64 ? 128 : mine > 16 ? 32 : 16;
+            const int pieces = (mine + piece - 1) / piece;
+            const uint32_t bytes = (kHalf + pieces * piece) * kSlice;
             const int m = t.m0 + rank * (P == kGated ? 64 : kHalf);
             for (int k = 0; k < t.slices && lane == 0; ++k) {
                 if (!(ok = wait(c, &sh->empty[s], phase ^ 1u))) break;
@@ -252,23 +259,34 @@ struct Producer {
                 }
                 const int at = k * kElems;
                 if constexpr (P == kGated) {
-                    for (int j = 0; j < 4; ++j) tensor_load_4d(sm + j * 4096, &job.map_m, at, m + 16 * j, 0, t.e, bar);
+                    if (job.m_whole)
+                        tensor_load_5d(sm, &job.map_m, at, 0, 0, m / 16, t.e, bar);
+                    else
+                        for (int j = 0; j < 4; ++j) tensor_load_4d(sm + j * 4096, &job.map_m, at, m + 16 * j, 0, t.e, bar);
                 } else if constexpr (P == kDown) {
                     tensor_load_3d(sm, &job.map_m, at, m, t.e, bar);
                 } else if constexpr (P == kDw) {
-                    for (int j = 0; j < 2; ++j)
-                        tensor_load_2d(sm + j * 8192, &job.map_m, m + 64 * j, t.first + k * 64, bar);
+                    if (job.m_whole)
+                        tensor_load_3d(sm, &job.map_m, 0, t.first + k * 64, m / 64, bar);
+                    else
+                        for (int j = 0; j < 2; ++j)
+                            tensor_load_2d(sm + j * 8192, &job.map_m, m + 64 * j, t.first + k * 64, bar);
                 } else {
-                    for (int j = 0; j < 2; ++j) tensor_load_3d(sm + j * 8192, &job.map_m, m + 64 * j, at, t.e, bar);
+                    if (job.m_whole)
+                        tensor_load_4d(sm, &job.map_m, 0, at, m / 64, t.e, bar);
+                    else
+                        for (int j = 0; j < 2; ++j) tensor_load_3d(sm + j * 8192, &job.map_m, m + 64 * j, at, t.e, bar);
                 }
                 if constexpr (P == kDw) {
-                    for (int j = 0; j < pieces; ++j)
-                        tensor_load_2d(sn + j * 8192, &job.map_n, t.n0 + rank * mine + 64 * j, t.first + k * 64, bar);
+                    if (job.n_whole)
+                        tensor_load_3d(sn, &job.map_n, 0, t.first + k * 64, (t.n0 + rank * mine) / 64, bar);
+                    else
+                        for (int j = 0; j < pieces; ++j)
+                            tensor_load_2d(sn + j * 8192, &job.map_n, t.n0 + rank * mine + 64 * j, t.first + k * 64, bar);
                 } else {
+                    const CUtensorMap* map = piece == 128 ? &job.map_n : piece == 32 ? &job.map_n32 : &job.map_n16;
                     const int row = t.first + t.n0 + rank * mine;
-                    if (pieces == 0) tensor_load_2d(sn, &job.map_n, at, row, bar);
-                    for (int j = 0; j < pieces; ++j)
-                        tensor_load_2d(sn + j * 16 * kSlice, &job.map_x, at, row + 16 * j, bar);
+                    for (int j = 0; j < pieces; ++j) tensor_load_2d(sn + j * piece * kSlice, map, at, row + piece * j, bar);
                 }
                 if (++s == ring.stages) {
                     s = 0;
@@ -282,59 +300,122 @@ struct Producer {
     }
 };
 
-// ---------------------------------------------------------------- matrix instructions (a warp of the pair, one lane)
-// One thread from end to end of a tile, the four instructions of a slice unrolled: gaps
-// between them cost (a loop over a slice's steps: dw 1650 us, this 1430 at
-// 32768 rows, H = I = 4096, 8 experts).
-struct Issuer {
+// ---------------------------------------------------------------- matrix instructions (two warps of the pair's first block)
+// A barrier's test between matrix instructions costs the thread that issues
+// them some 190 cycles even where the barrier is long complete (measured: 4
+// instructions and a commit take 270 cycles for N <= 64, 385 for N = 192, 513
+// for N = 256; with a test 458, 458, 513).  So another warp does all the
+// waiting: it walks over the tiles, leaves each one's orders in shared memory,
+// waits for its slices and counts those that are ready.  The issuing thread
+// reads the count, and only when it has used up what it read last.
+struct Watcher {
     Turn turn;
     int s = 0, buf = 0;
     uint32_t acc_phase = 0, full_phase = 0, tail_phase = 0;  // the latter two: a bit a stage
+    uint32_t slices = 0, tiles_seen = 0;
     bool ok = true;
 
+    __device__ __forceinline__ void publish(Shared* sh, int lane) {
+        ++slices;
+        if (lane == 0)
+            asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_addr(&sh->ready)), "r"(slices) : "memory");
+    }
+
     template <int P, bool FP8>
-    __device__ __forceinline__ void run(const Job& job, const Common& c, const Groups& g, Shared* sh,
-                                        const RingShape& ring, uint32_t tmem, int lane) {
-        constexpr bool kMt = m_transposed<P>(), kNt = n_transposed<P>();
-        constexpr int kStepM = (kMt ? 2048 : 32) >> 4, kStepN = (kNt ? 2048 : 32) >> 4;
+    __device__ __forceinline__ void run(const Job& job, const Common& c, const Groups& g, Shared* sh, int stages,
+                                        int lane) {
         Tiles<P, FP8> tiles(job, g);
         for (; ok && turn.next < tiles.total; turn.next += turn.pairs) {
             const Tile t = tiles.at(g, turn.next, lane);
             if (t.slices == 0) continue;
-            const uint32_t desc = mma_desc(FP8 ? 0u : 1u, kMt, kNt, kTile, (t.n + 15) & ~15);
-            const uint32_t acc = tmem + buf * kTile;
-            if (lane == 0) ok = wait(c, &sh->acc_empty[buf], acc_phase ^ 1u);
-            for (int k = 0; k < t.slices && ok && lane == 0; ++k) {
-                const bool last = k + 1 == t.slices;
-                if (P == kDw && last && (t.count & 15) != 0) {
-                    if (!(ok = wait(c, &sh->tail_ready[s], (tail_phase >> s) & 1u))) break;
+            const bool tail = P == kDw && (t.count & 15) != 0;
+            if (lane == 0)
+                sh->order[tiles_seen % kOrders] =
+                    make_uint4(mma_desc(FP8 ? 0u : 1u, m_transposed<P>(), n_transposed<P>(), kTile, (t.n + 15) & ~15),
+                               t.slices, P == kDw ? ((t.count - 1) % 64) / 16 + 1 : 4, P == kDw);
+            ++tiles_seen;
+            ok = __all_sync(FULL_MASK, wait(c, &sh->acc_empty[buf], acc_phase ^ 1u));
+            for (int k = 0; k < t.slices && ok; ++k) {
+                if (tail && k + 1 == t.slices) {
+                    ok = __all_sync(FULL_MASK, wait(c, &sh->tail_ready[s], (tail_phase >> s) & 1u));
                     tail_phase ^= 1u << s;
                 } else {
-                    if (!(ok = wait(c, &sh->full[s], (full_phase >> s) & 1u))) break;
+                    ok = __all_sync(FULL_MASK, wait(c, &sh->full[s], (full_phase >> s) & 1u));
                     full_phase ^= 1u << s;
                 }
-                tc_fence_after();
-                const uint32_t sm = smem_addr(ring.at + s * ring.stage_bytes);
-                const uint64_t dm = operand_desc(sm, kMt ? 8192 : 16, 1024);
-                const uint64_t dn = operand_desc(sm + kHalf * kSlice, kNt ? 8192 : 16, 1024);
-                // 32 bytes of k, or 16 rows of it, an instruction; dw's last slice may have fewer
-                const int steps = P == kDw && last ? ((t.count - 1) % 64) / 16 + 1 : 4;
-                if (P != kDw || steps == 4) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mma<FP8>(acc, dm + j * kStepM, dn + j * kStepN, desc, k > 0 || j > 0);
-                } else {
-                    for (int j = 0; j < steps; ++j)
-                        mma<FP8>(acc, dm + j * kStepM, dn + j * kStepN, desc, k > 0 || j > 0);
-                }
-                mma_commit(&sh->empty[s]);
-                if (last) mma_commit(&sh->acc_full[buf]);
-                if (++s == ring.stages) s = 0;
+                if (ok) publish(sh, lane);
+                if (++s == stages) s = 0;
             }
-            __syncwarp();
-            ok = __shfl_sync(FULL_MASK, static_cast<int>(ok), 0) != 0;
             if ((buf ^= 1) == 0) acc_phase ^= 1u;
         }
         turn.next -= tiles.total;
+    }
+
+    // After the last job, or after a wait that ran out: nothing comes any more.
+    __device__ __forceinline__ void end(Shared* sh, int lane) {
+        if (lane == 0) sh->order[tiles_seen % kOrders] = make_uint4(0u, 0u, 0u, 0u);
+        publish(sh, lane);
+    }
+};
+
+struct Issuer {
+    int s = 0, buf = 0;
+    uint32_t used = 0, ready = 0;
+    bool ok = true;
+
+    // Whether slice `used` is there; gives up after as long as any wait does.
+    __device__ __forceinline__ bool more(const Common& c, Shared* sh) {
+        if (used != ready) return true;
+        uint64_t t0 = 0;
+        for (uint32_t n = 0;; ++n) {
+            asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(ready) : "r"(smem_addr(&sh->ready)) : "memory");
+            if (used != ready) break;
+            if ((n & 255u) == 255u) {
+                const uint64_t now = globaltimer_ns();
+                if (t0 == 0) t0 = now;
+                else if (now - t0 > 2 * static_cast<uint64_t>(c.timeout_ns)) return ok = false;  // the watcher's limit first
+            }
+        }
+        tc_fence_after();
+        return true;
+    }
+
+    template <int P, bool FP8>
+    __device__ __forceinline__ void tile(const Common& c, Shared* sh, const RingShape& ring, uint32_t tmem,
+                                         const uint4& order) {
+        constexpr bool kMt = m_transposed<P>(), kNt = n_transposed<P>();
+        constexpr int kStepM = (kMt ? 2048 : 32) >> 4, kStepN = (kNt ? 2048 : 32) >> 4;
+        const uint32_t acc = tmem + buf * kTile, desc = order.x;
+        for (uint32_t k = 0; k < order.y; ++k) {
+            if (!more(c, sh)) return;
+            const bool last = k + 1 == order.y;
+            const uint32_t sm = smem_addr(ring.at + s * ring.stage_bytes);
+            const uint64_t dm = operand_desc(sm, kMt ? 8192 : 16, 1024);
+            const uint64_t dn = operand_desc(sm + kHalf * kSlice, kNt ? 8192 : 16, 1024);
+            // 32 bytes of k, or 16 rows of it, an instruction; dw's last slice may have fewer
+            if (P != kDw || !last || order.z == 4u) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma<FP8>(acc, dm + j * kStepM, dn + j * kStepN, desc, k > 0 || j > 0);
+            } else {
+                for (uint32_t j = 0; j < order.z; ++j)
+                    mma<FP8>(acc, dm + j * kStepM, dn + j * kStepN, desc, k > 0 || j > 0);
+            }
+            mma_commit(&sh->empty[s]);
+            if (last) mma_commit(&sh->acc_full[buf]);
+            if (++s == ring.stages) s = 0;
+            ++used;
+        }
+        buf ^= 1;
+    }
+
+    template <int P, bool FP8>
+    __device__ __forceinline__ void run(const Common& c, Shared* sh, const RingShape& ring, uint32_t tmem) {
+        for (uint32_t i = 0; ok && more(c, sh); ++i) {
+            const uint4 order = sh->order[i % kOrders];
+            if (order.y == 0) break;
+            if (P == kGrads && order.w != 0) tile<kDw, false>(c, sh, ring, tmem, order);
+            else tile<P == kGrads ? kDx : P, FP8>(c, sh, ring, tmem, order);
+        }
     }
 };
 
@@ -501,7 +582,7 @@ __device__ __forceinline__ void epilogue_dw(const Job& job, const Tile& t, int r
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0 && m < job.M) {
-        tensor_store_3d(&job.map_x, t.n0 + c0, m, t.e, box);
+        tensor_store_3d(&job.map_out, t.n0 + c0, m, t.e, box);
         bulk_commit();
     }
 }
@@ -583,6 +664,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
             mbar_init(&sh->acc_empty[i], 2 * kEpilogueWarps);
         }
         fence_mbar_init();
+        sh->ready = 0;
     }
     __syncwarp();
     if (warp == 1) tmem_alloc(&sh->tmem, 512);
@@ -629,7 +711,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     const Groups g = {first, count, padded, prefix, E};
     // short groups leave room for more stages: the N side's part is as long as the longest tile's half
     const int half = (min(longest, kTile) + 15) / 16 * 8;
-    const int n_rows = P == kGrads || half > 64 ? kHalf : max(16, (half + 15) / 16 * 16);
+    const int n_rows = P == kGrads || half > 64 ? kHalf : half > 16 ? (half + 31) / 32 * 32 : 16;
     RingShape ring;
     ring.at = base;
     ring.stage_bytes = static_cast<uint32_t>(kHalf + n_rows) * kSlice;
@@ -659,16 +741,22 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
             while (globaltimer_ns() - t0 < 20000000u) __nanosleep(1000);
         }
     } else if (run && warp == 1 && rank == 0) {
-        Issuer r;
+        if (lane == 0) {
+            Issuer r;
+            r.run<P, FP8>(c, sh, ring, tmem);
+        }
+    } else if (run && warp == kWatchWarp && rank == 0) {
+        Watcher r;
         r.turn = turn;
         if constexpr (P == kGrads) {
-            if (a.job[0].M > 0) r.run<kDx, false>(a.job[0], c, g, sh, ring, tmem, lane);
-            if (a.job[1].M > 0) r.run<kDw, false>(a.job[1], c, g, sh, ring, tmem, lane);
-            if (a.job[2].M > 0) r.run<kDw, false>(a.job[2], c, g, sh, ring, tmem, lane);
+            if (a.job[0].M > 0) r.run<kDx, false>(a.job[0], c, g, sh, ring.stages, lane);
+            if (a.job[1].M > 0) r.run<kDw, false>(a.job[1], c, g, sh, ring.stages, lane);
+            if (a.job[2].M > 0) r.run<kDw, false>(a.job[2], c, g, sh, ring.stages, lane);
         } else {
-            r.run<P, FP8>(a.job[0], c, g, sh, ring, tmem, lane);
+            r.run<P, FP8>(a.job[0], c, g, sh, ring.stages, lane);
         }
-    } else if (run && warp >= 2 && warp < kMendWarp) {
+        r.end(sh, lane);
+    } else if (run && warp >= 2 && warp < kWatchWarp) {
         Drain r;
         r.turn = turn;
         if constexpr (P == kGrads) {
@@ -723,18 +811,50 @@ int make_job(moe::Job* j, const void* weights, const void* row_data, int64_t row
     j->N = N;
     j->K = K;
     j->out = out;
+    // The thread that issues copies takes longer for a slice of many than the
+    // products do (some 50 cycles each and 200 for the stage's wait): a block's
+    // part of a slice is one copy where the extents allow it, with more
+    // extents than the array has.  Gated: the M side's 16 channels of the gate
+    // and of the up projection in turn, for M in whole 16s.  Transposed operands:
+    // two runs of 64 elements, for whole 64s (a run that left its row would read
+    // the next one's, and past the array's end at the last).
+    const int run = 128 / bytes, box_k = run;
+    const int64_t m = M, n = N, k = K, mk = m * k;
     int rc;
-    if constexpr (P == moe::kGated) rc = moe_host::make_tensor_map(&j->map_m, weights, bytes, {K, M, 2, E}, 16, 2);
-    else if constexpr (P == moe::kDown) rc = moe_host::make_tensor_map(&j->map_m, weights, 2, {K, M, E}, moe::kHalf);
-    else if constexpr (P == moe::kDw) rc = moe_host::make_tensor_map(&j->map_m, weights, 2, {M, rows}, 64);
-    else rc = moe_host::make_tensor_map(&j->map_m, weights, 2, {M, K, E}, 64);
+    if constexpr (P == moe::kGated) {
+        j->m_whole = M % 16 == 0;
+        if (j->m_whole)
+            rc = moe_host::make_tensor_map(&j->map_m, weights, bytes,
+                                           {{k, 1, box_k}, {16, k, 16}, {2, mk, 2}, {m / 16, 16 * k, 4}, {E, 2 * mk, 1}});
+        else
+            rc = moe_host::make_tensor_map(&j->map_m, weights, bytes, {{k, 1, box_k}, {m, k, 16}, {2, mk, 2}, {E, 2 * mk, 1}});
+    } else if constexpr (P == moe::kDown) {
+        rc = moe_host::make_tensor_map(&j->map_m, weights, 2, {{k, 1, run}, {m, k, moe::kHalf}, {E, mk, 1}});
+    } else if constexpr (P == moe::kDw) {
+        j->m_whole = M % 64 == 0;
+        if (j->m_whole)
+            rc = moe_host::make_tensor_map(&j->map_m, weights, 2, {{run, 1, run}, {rows, m, 64}, {m / run, run, 2}});
+        else
+            rc = moe_host::make_tensor_map(&j->map_m, weights, 2, {{m, 1, run}, {rows, m, 64}});
+    } else {
+        j->m_whole = M % 64 == 0;
+        if (j->m_whole)
+            rc = moe_host::make_tensor_map(&j->map_m, weights, 2, {{run, 1, run}, {k, m, 64}, {m / run, run, 2}, {E, mk, 1}});
+        else
+            rc = moe_host::make_tensor_map(&j->map_m, weights, 2, {{m, 1, run}, {k, m, 64}, {E, mk, 1}});
+    }
     if (rc != MOE_OK) return rc;
     if constexpr (P == moe::kDw) {
-        rc = moe_host::make_tensor_map(&j->map_n, row_data, 2, {N, rows}, 64);
-        return rc != MOE_OK ? rc : moe_host::make_tensor_map(&j->map_x, out, 2, {N, M, E}, 32);
+        j->n_whole = N % 128 == 0;  // and a block's half of the last tile starts at a run
+        if (j->n_whole)
+            rc = moe_host::make_tensor_map(&j->map_n, row_data, 2, {{run, 1, run}, {rows, n, 64}, {n / run, run, 2}});
+        else
+            rc = moe_host::make_tensor_map(&j->map_n, row_data, 2, {{n, 1, run}, {rows, n, 64}});
+        return rc != MOE_OK ? rc : moe_host::make_tensor_map(&j->map_out, out, 2, {{n, 1, run}, {m, n, 32}, {E, m * n, 1}});
     } else {
-        rc = moe_host::make_tensor_map(&j->map_n, row_data, bytes, {K, rows}, moe::kHalf);
-        return rc != MOE_OK ? rc : moe_host::make_tensor_map(&j->map_x, row_data, bytes, {K, rows}, 16);
+        rc = moe_host::make_tensor_map(&j->map_n, row_data, bytes, {{k, 1, box_k}, {rows, k, moe::kHalf}});
+        if (rc == MOE_OK) rc = moe_host::make_tensor_map(&j->map_n32, row_data, bytes, {{k, 1, box_k}, {rows, k, 32}});
+        return rc != MOE_OK ? rc : moe_host::make_tensor_map(&j->map_n16, row_data, bytes, {{k, 1, box_k}, {rows, k, 16}});
     }
 }
 

@@ -141,6 +141,14 @@ __device__ __forceinline__ void tensor_load_4d(void* dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ void tensor_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, int v,
+                                               uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
+        : "memory");
+}
 // Out of shared memory; clipped at the array's end, tracked by the thread's bulk groups.
 __device__ __forceinline__ void tensor_store_3d(const CUtensorMap* map, int x, int y, int z, const void* src) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
@@ -153,12 +161,17 @@ __device__ __forceinline__ void tensor_store_3d(const CUtensorMap* map, int x, i
 // ---------------------------------------------------------------- host side
 namespace moe_host {
 
-// Tensor map of a packed row-major array whose extents are `size` (the
-// contiguous one first), with boxes of 128 bytes by box1 by box2 rows (1 in
-// the rest), 128-byte swizzle, zeros outside the array.  bytes: element size,
-// 2 (bf16) or 1.
-inline int make_tensor_map(CUtensorMap* map, const void* base, int bytes, std::initializer_list<int64_t> size, int box1,
-                           int box2 = 1) {
+// One extent of a tensor map: its length, the elements from one index to the
+// next, and how many a copy takes.
+struct Extent {
+    int64_t size, stride;
+    int box;
+};
+
+// Tensor map of up to five extents, the contiguous one first (its copies take
+// 128 bytes; 128-byte swizzle), with zeros outside.  bytes: element size, 2
+// (bf16) or 1.
+inline int make_tensor_map(CUtensorMap* map, const void* base, int bytes, std::initializer_list<Extent> extents) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -172,19 +185,17 @@ inline int make_tensor_map(CUtensorMap* map, const void* base, int bytes, std::i
         return reinterpret_cast<Encode>(fn);
     }();
     if (encode == nullptr) return MOE_ERR_CUDA;
-    cuuint64_t extent[4] = {1, 1, 1, 1}, stride[4] = {0, 0, 0, 0};  // stride[i]: bytes of one step of extent i + 1
-    cuuint64_t step = static_cast<cuuint64_t>(bytes);
+    cuuint64_t size[5], stride[5];
+    cuuint32_t box[5], ones[5];
     int dims = 0;
-    for (const int64_t n : size) {
-        extent[dims] = static_cast<cuuint64_t>(n);
-        step *= extent[dims];
-        stride[dims++] = step;
+    for (const Extent& e : extents) {
+        size[dims] = static_cast<cuuint64_t>(e.size);
+        stride[dims] = static_cast<cuuint64_t>(e.stride * bytes);
+        box[dims] = static_cast<cuuint32_t>(e.box);
+        ones[dims++] = 1;
     }
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / bytes), static_cast<cuuint32_t>(box1),
-                               static_cast<cuuint32_t>(box2), 1};
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
     const CUresult rc = encode(map, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                               static_cast<cuuint32_t>(dims), const_cast<void*>(base), extent, stride, box, ones,
+                               static_cast<cuuint32_t>(dims), const_cast<void*>(base), size, stride + 1, box, ones,
                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return rc == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
