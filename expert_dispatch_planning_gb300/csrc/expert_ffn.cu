@@ -60,6 +60,8 @@ constexpr int kOrders = 16;        // tiles whose orders are kept: more than sli
 constexpr int kChunk = 16;         // accumulator columns that a warp turns at a time
 
 __host__ __device__ constexpr int ffn_threads(int p) { return 96 + 32 * kEpilogueWarps + (p == kGrads ? 32 : 0); }
+// a warp's bytes to turn a chunk in: dw sends boxes of 4 KB, which start at multiples of 1024 (they are swizzled)
+__host__ __device__ constexpr int ffn_turn(int p) { return p == kGrads ? 4096 : 2048; }
 __host__ __device__ constexpr int ffn_jobs(int p) { return p == kGrads ? 3 : 1; }
 
 struct Job {
@@ -92,7 +94,6 @@ struct Launch {
 };
 
 struct Shared {
-    uint4 turn[kEpilogueWarps][256];  // a warp's 4 KB (1024-byte aligned: dw's boxes are swizzled)
     uint64_t full[kMaxStages], empty[kMaxStages], tail_full[kMaxStages], tail_ready[kMaxStages], acc_full[2],
         acc_empty[2];
     uint4 order[kOrders];   // the tiles' instructions: descriptor, slices (0: the end), steps of the last, dw
@@ -595,11 +596,10 @@ struct Drain {
 
     template <int P, bool FP8>
     __device__ __forceinline__ void run(const Job& job, const Common& c, const Groups& g, Shared* sh, uint32_t tmem,
-                                        int rank, int warp, int lane) {
+                                        int rank, int warp, int lane, uint8_t* turn_buf) {
         const int quarter = warp & 3;           // the lanes of tensor memory that a warp may read
         const int half = (warp - 2) >> 2;       // two warps a quarter take every other chunk
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        uint4* turn_buf = sh->turn[warp - 2];
         Tiles<P, FP8> tiles(job, g);
         for (; ok && turn.next < tiles.total; turn.next += turn.pairs) {
             const Tile t = tiles.at(g, turn.next, lane);
@@ -610,7 +610,7 @@ struct Drain {
             }
             const uint32_t acc = tmem + buf * kTile + lanes;
             if constexpr (P == kDw) {
-                for (int n = half * 64; n < t.n; n += 128) epilogue_dw(job, t, rank, acc, n, quarter, lane, turn_buf);
+                for (int n = half * 64; n < t.n; n += 128) epilogue_dw(job, t, rank, acc, n, quarter, lane, reinterpret_cast<uint4*>(turn_buf));
             } else {
                 for (int n = half * kChunk; n < t.n; n += 2 * kChunk)
                     epilogue_chunk<P>(job, c, t, rank, acc, n, quarter, lane, reinterpret_cast<float*>(turn_buf));
@@ -643,7 +643,8 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     constexpr int kThreads = ffn_threads(P), kWarps = kThreads / 32;
     const Common& c = a.c;
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    Shared* sh = reinterpret_cast<Shared*>(base + c.ring_bytes);
+    uint8_t* turns = base + c.ring_bytes;
+    Shared* sh = reinterpret_cast<Shared*>(turns + kEpilogueWarps * ffn_turn(P));
     const int E = c.E;
     int* first = reinterpret_cast<int*>(sh + 1);
     int *count = first + E, *padded = count + E, *prefix = padded + E;  // prefix: E + 1
@@ -759,13 +760,14 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     } else if (run && warp >= 2 && warp < kWatchWarp) {
         Drain r;
         r.turn = turn;
+        uint8_t* turn_buf = turns + (warp - 2) * ffn_turn(P);
         if constexpr (P == kGrads) {
-            if (a.job[0].M > 0) r.run<kDx, false>(a.job[0], c, g, sh, tmem, rank, warp, lane);
-            if (a.job[1].M > 0) r.run<kDw, false>(a.job[1], c, g, sh, tmem, rank, warp, lane);
-            if (a.job[2].M > 0) r.run<kDw, false>(a.job[2], c, g, sh, tmem, rank, warp, lane);
+            if (a.job[0].M > 0) r.run<kDx, false>(a.job[0], c, g, sh, tmem, rank, warp, lane, turn_buf);
+            if (a.job[1].M > 0) r.run<kDw, false>(a.job[1], c, g, sh, tmem, rank, warp, lane, turn_buf);
+            if (a.job[2].M > 0) r.run<kDw, false>(a.job[2], c, g, sh, tmem, rank, warp, lane, turn_buf);
             if (lane == 0) bulk_wait<0>();
         } else {
-            r.run<P, FP8>(a.job[0], c, g, sh, tmem, rank, warp, lane);
+            r.run<P, FP8>(a.job[0], c, g, sh, tmem, rank, warp, lane, turn_buf);
         }
     } else if (P == kGrads && run && warp == kMendWarp) {
         if constexpr (P == kGrads) {
@@ -860,11 +862,12 @@ int make_job(moe::Job* j, const void* weights, const void* row_data, int64_t row
 
 template <int P, bool FP8 = false>
 int launch(moe::Launch<P>& a, cudaStream_t stream) {
-    // as many stages of 32 KB as fit: five (a sixth changed nothing)
+    // as many stages of 32 KB as fit: six, five with dw
     constexpr size_t kSmem = 227 * 1024, kStage = 2 * moe::kHalf * moe::kSlice;
-    const size_t fixed = 1024 + sizeof(moe::Shared) + sizeof(int) * (4 * static_cast<size_t>(a.c.E) + 1);
+    const size_t fixed = 1024 + moe::kEpilogueWarps * moe::ffn_turn(P) + sizeof(moe::Shared) +
+                         sizeof(int) * (4 * static_cast<size_t>(a.c.E) + 1);
     a.c.ring_bytes = static_cast<int>((kSmem - fixed) / kStage * kStage);
-    static_assert(1024 + sizeof(moe::Shared) + sizeof(int) * 4097 + 5 * kStage <= kSmem, "shared memory");
+    static_assert(1024 + moe::kEpilogueWarps * 4096 + sizeof(moe::Shared) + sizeof(int) * 4097 + 5 * kStage <= kSmem, "shared memory");
     if (cudaFuncSetAttribute(moe::ffn_kernel<P, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmem)) != cudaSuccess)
         return MOE_ERR_CUDA;
