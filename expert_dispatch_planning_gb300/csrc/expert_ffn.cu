@@ -84,6 +84,7 @@ struct Common {
     int64_t rows;
     int E;
     int ring_bytes;
+    int early;              // a call's second or later kernel
     int64_t timeout_ns;
 };
 
@@ -227,68 +228,113 @@ struct Producer {
     Turn turn;
     int s = 0;
     uint32_t phase = 0;
+    int ahead = 0;           // slices of the first tile whose M side is on its way already
     bool ok = true;
+
+    // The N side of a block's part of a tile: rows (dw: columns), and the copies
+    // for them: of 128 rows, or of 32 or 16 (dw: of 128 columns, or of 64).
+    struct NSide {
+        int rows, piece, pieces;
+        uint32_t bytes;      // of a block's part of a slice, both sides
+    };
+    template <int P>
+    __device__ __forceinline__ NSide n_side(const Job& job, const Tile& t) const {
+        NSide n;
+        n.rows = ((t.n + 15) & ~15) / 2;
+        n.piece = P == kDw ? (job.n_whole ? 128 : 64) : n.rows > 64 ? 128 : n.rows > 16 ? 32 : 16;
+        n.pieces = (n.rows + n.piece - 1) / n.piece;
+        n.bytes = static_cast<uint32_t>(kHalf + n.pieces * n.piece) * kSlice;
+        return n;
+    }
+
+    // Both blocks' copies are counted by the first one's barrier, but those of
+    // a slice that has to be mended by each block's own.
+    template <int P>
+    static __device__ __forceinline__ bool mended(const Tile& t, int k) {
+        return P == kDw && k + 1 == t.slices && (t.count & 15) != 0;
+    }
+    template <int P>
+    __device__ __forceinline__ void arm(Shared* sh, const Tile& t, int k, uint32_t bytes, int rank) const {
+        if (mended<P>(t, k)) mbar_arrive_expect_tx(&sh->tail_full[s], bytes);
+        else if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], 2 * bytes);
+    }
+    template <int P>
+    __device__ __forceinline__ uint32_t barrier(Shared* sh, const Tile& t, int k, int rank) const {
+        if (mended<P>(t, k)) return smem_addr(&sh->tail_full[s]);
+        return rank == 0 ? smem_addr(&sh->full[s]) : leader_addr(&sh->full[s]);
+    }
+    template <int P, bool FP8>
+    __device__ __forceinline__ void copy_m(const Job& job, const Tile& t, int k, uint8_t* to, int rank,
+                                           uint32_t bar) const {
+        const int m = t.m0 + rank * (P == kGated ? 64 : kHalf), at = k * (FP8 ? 128 : 64);
+        if constexpr (P == kGated) {
+            if (job.m_whole) tensor_load_5d(to, &job.map_m, at, 0, 0, m / 16, t.e, bar);
+            else
+                for (int j = 0; j < 4; ++j) tensor_load_4d(to + j * 4096, &job.map_m, at, m + 16 * j, 0, t.e, bar);
+        } else if constexpr (P == kDown) {
+            tensor_load_3d(to, &job.map_m, at, m, t.e, bar);
+        } else if constexpr (P == kDw) {
+            if (job.m_whole) tensor_load_3d(to, &job.map_m, 0, t.first + at, m / 64, bar);
+            else
+                for (int j = 0; j < 2; ++j) tensor_load_2d(to + j * 8192, &job.map_m, m + 64 * j, t.first + at, bar);
+        } else {
+            if (job.m_whole) tensor_load_4d(to, &job.map_m, 0, at, m / 64, t.e, bar);
+            else
+                for (int j = 0; j < 2; ++j) tensor_load_3d(to + j * 8192, &job.map_m, m + 64 * j, at, t.e, bar);
+        }
+    }
+    template <int P, bool FP8>
+    __device__ __forceinline__ void copy_n(const Job& job, const Tile& t, const NSide& n, int k, uint8_t* to, int rank,
+                                           uint32_t bar) const {
+        const int at = k * (FP8 ? 128 : 64);
+        if constexpr (P == kDw) {
+            const int col = t.n0 + rank * n.rows;
+            if (job.n_whole) tensor_load_3d(to, &job.map_n, 0, t.first + at, col / 64, bar);
+            else
+                for (int j = 0; j < n.pieces; ++j)
+                    tensor_load_2d(to + j * 8192, &job.map_n, col + 64 * j, t.first + at, bar);
+        } else {
+            const CUtensorMap* map = n.piece == 128 ? &job.map_n : n.piece == 32 ? &job.map_n32 : &job.map_n16;
+            const int row = t.first + t.n0 + rank * n.rows;
+            for (int j = 0; j < n.pieces; ++j)
+                tensor_load_2d(to + j * n.piece * kSlice, map, at, row + n.piece * j, bar);
+        }
+    }
+
+    // The M side (weights) of the first tile's first slices, before the rows are there.
+    template <int P, bool FP8>
+    __device__ __forceinline__ void start(const Job& job, const Groups& g, Shared* sh, const RingShape& ring, int rank,
+                                          int lane) {
+        Tiles<P, FP8> tiles(job, g);
+        if (turn.next >= tiles.total) return;
+        const Tile t = tiles.at(g, turn.next, lane);
+        ahead = min(ring.stages, t.slices);
+        if (lane == 0)
+            for (int k = 0; k < ahead; ++k, ++s) {
+                arm<P>(sh, t, k, n_side<P>(job, t).bytes, rank);
+                copy_m<P, FP8>(job, t, k, ring.at + s * ring.stage_bytes, rank, barrier<P>(sh, t, k, rank));
+            }
+        s = 0;
+    }
 
     template <int P, bool FP8>
     __device__ __forceinline__ void run(const Job& job, const Common& c, const Groups& g, Shared* sh,
                                         const RingShape& ring, int rank, int lane) {
         Tiles<P, FP8> tiles(job, g);
-        constexpr int kElems = FP8 ? 128 : 64;  // k's of a slice
         for (; ok && turn.next < tiles.total; turn.next += turn.pairs) {
             const Tile t = tiles.at(g, turn.next, lane);
-            const int mine = ((t.n + 15) & ~15) / 2;  // N-side rows (dw: columns) of a block
-            // the N side's copies: 128 rows, or 32 or 16 at a time (dw: 128 columns, or 64 at a time)
-            const int piece = P == kDw ? (job.n_whole ? 128 : 64) : mine > 64 ? 128 : mine > 16 ? 32 : 16;
-            const int pieces = (mine + piece - 1) / piece;
-            const uint32_t bytes = (kHalf + pieces * piece) * kSlice;
-            const int m = t.m0 + rank * (P == kGated ? 64 : kHalf);
+            const NSide n = n_side<P>(job, t);
             for (int k = 0; k < t.slices && lane == 0; ++k) {
-                if (!(ok = wait(c, &sh->empty[s], phase ^ 1u))) break;
-                uint8_t* sm = ring.at + s * ring.stage_bytes;
-                uint8_t* sn = sm + kHalf * kSlice;
-                // both blocks' copies are counted by the first one's barrier, but those
-                // of a slice that has to be mended by each block's own
-                uint32_t bar;
-                if (P == kDw && k + 1 == t.slices && (t.count & 15) != 0) {
-                    mbar_arrive_expect_tx(&sh->tail_full[s], bytes);
-                    bar = smem_addr(&sh->tail_full[s]);
-                } else if (rank == 0) {
-                    mbar_arrive_expect_tx(&sh->full[s], 2 * bytes);
-                    bar = smem_addr(&sh->full[s]);
+                uint8_t* to = ring.at + s * ring.stage_bytes;
+                const uint32_t bar = barrier<P>(sh, t, k, rank);
+                if (ahead > 0) {
+                    --ahead;
                 } else {
-                    bar = leader_addr(&sh->full[s]);
+                    if (!(ok = wait(c, &sh->empty[s], phase ^ 1u))) break;
+                    arm<P>(sh, t, k, n.bytes, rank);
+                    copy_m<P, FP8>(job, t, k, to, rank, bar);
                 }
-                const int at = k * kElems;
-                if constexpr (P == kGated) {
-                    if (job.m_whole)
-                        tensor_load_5d(sm, &job.map_m, at, 0, 0, m / 16, t.e, bar);
-                    else
-                        for (int j = 0; j < 4; ++j) tensor_load_4d(sm + j * 4096, &job.map_m, at, m + 16 * j, 0, t.e, bar);
-                } else if constexpr (P == kDown) {
-                    tensor_load_3d(sm, &job.map_m, at, m, t.e, bar);
-                } else if constexpr (P == kDw) {
-                    if (job.m_whole)
-                        tensor_load_3d(sm, &job.map_m, 0, t.first + k * 64, m / 64, bar);
-                    else
-                        for (int j = 0; j < 2; ++j)
-                            tensor_load_2d(sm + j * 8192, &job.map_m, m + 64 * j, t.first + k * 64, bar);
-                } else {
-                    if (job.m_whole)
-                        tensor_load_4d(sm, &job.map_m, 0, at, m / 64, t.e, bar);
-                    else
-                        for (int j = 0; j < 2; ++j) tensor_load_3d(sm + j * 8192, &job.map_m, m + 64 * j, at, t.e, bar);
-                }
-                if constexpr (P == kDw) {
-                    if (job.n_whole)
-                        tensor_load_3d(sn, &job.map_n, 0, t.first + k * 64, (t.n0 + rank * mine) / 64, bar);
-                    else
-                        for (int j = 0; j < pieces; ++j)
-                            tensor_load_2d(sn + j * 8192, &job.map_n, t.n0 + rank * mine + 64 * j, t.first + k * 64, bar);
-                } else {
-                    const CUtensorMap* map = piece == 128 ? &job.map_n : piece == 32 ? &job.map_n32 : &job.map_n16;
-                    const int row = t.first + t.n0 + rank * mine;
-                    for (int j = 0; j < pieces; ++j) tensor_load_2d(sn + j * piece * kSlice, map, at, row + piece * j, bar);
-                }
+                copy_n<P, FP8>(job, t, n, k, to + kHalf * kSlice, rank, bar);
                 if (++s == ring.stages) {
                     s = 0;
                     phase ^= 1u;
@@ -561,24 +607,25 @@ __device__ __forceinline__ void epilogue_dw(const Job& job, const Tile& t, int r
     const int m = t.m0 + rank * kHalf + quarter * 32;
     if (lane == 0) bulk_wait_read<0>();  // the box before has left
     __syncwarp();
-    uint32_t v[4][16];
-    if (t.slices > 0) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_load16(acc + c0 + 16 * q, v[q]);
-        tmem_wait_load();
-    } else {
+    for (int part = 0; part < 2; ++part) {
+        uint32_t v[2][16];
+        if (t.slices > 0) {
+            tmem_load16(acc + c0 + 32 * part, v[0]);
+            tmem_load16(acc + c0 + 32 * part + 16, v[1]);
+            tmem_wait_load();
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+            for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = 0u;
+        }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[q][j] = 0u;
-    }
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t* f = v[q / 2] + 8 * (q & 1);
+            uint32_t p[4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        uint32_t p[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            p[j] = pack2(__uint_as_float(v[q / 2][8 * (q & 1) + 2 * j]), __uint_as_float(v[q / 2][8 * (q & 1) + 2 * j + 1]));
-        box[lane * 8 + (q ^ (lane & 7))] = make_uint4(p[0], p[1], p[2], p[3]);
+            for (int j = 0; j < 4; ++j) p[j] = pack2(__uint_as_float(f[2 * j]), __uint_as_float(f[2 * j + 1]));
+            box[lane * 8 + ((4 * part + q) ^ (lane & 7))] = make_uint4(p[0], p[1], p[2], p[3]);
+        }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -668,10 +715,12 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         sh->ready = 0;
     }
     __syncwarp();
-    if (warp == 1) tmem_alloc(&sh->tmem, 512);
-    pdl_wait();
-    pdl_trigger();
-    if (tid == 0) sh->stop = ld_volatile_s32(c.status) != 0;
+    // A call's later kernels start while the one before still runs: the groups
+    // and the weights were there before that one began.
+    if (!c.early) {
+        pdl_wait();
+        pdl_trigger();
+    }
 
     // ---- the groups: row tiles before each expert, and the longest group
     const int per = (E + kThreads - 1) / kThreads;
@@ -717,20 +766,37 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     ring.at = base;
     ring.stage_bytes = static_cast<uint32_t>(kHalf + n_rows) * kSlice;
     ring.stages = min(kMaxStages, static_cast<int>(c.ring_bytes / ring.stage_bytes));
+    Turn turn;
+    turn.next = blockIdx.x >> 1;
+    turn.pairs = static_cast<int>(gridDim.x >> 1);
+    Producer producer;
+    producer.turn = turn;
+    if (c.early) {
+        if (tid == 0) sh->stop = ld_volatile_s32(c.status) != 0;
+        __syncthreads();
+        pair_sync();  // both blocks' barriers are ready
+        if (warp == 0 && sh->stop == 0) {
+            if constexpr (P == kDown) producer.start<P, FP8>(a.job[0], g, sh, ring, rank, lane);
+            if constexpr (P == kGrads)
+                if (a.job[0].M > 0) producer.start<kDx, false>(a.job[0], g, sh, ring, rank, lane);
+        }
+        __syncwarp();
+        pdl_wait();
+        pdl_trigger();
+    }
+    if (tid == 0) sh->stop = ld_volatile_s32(c.status) != 0;
+    if (warp == 1) tmem_alloc(&sh->tmem, 512);
     tc_fence_before();
     __syncthreads();
     pair_sync();  // both blocks' barriers and tensor memory are ready
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
     const bool run = sh->stop == 0;
-    Turn turn;
-    turn.next = blockIdx.x >> 1;
-    turn.pairs = static_cast<int>(gridDim.x >> 1);
 
-    if (run && warp == 0) {
-        Producer r;
-        r.turn = turn;
-        if constexpr (P == kGrads) {
+    if (warp == 0) {
+        Producer& r = producer;
+        if (!run) r.ok = r.ahead == 0;
+        else if constexpr (P == kGrads) {
             if (a.job[0].M > 0) r.run<kDx, false>(a.job[0], c, g, sh, ring, rank, lane);
             if (a.job[1].M > 0) r.run<kDw, false>(a.job[1], c, g, sh, ring, rank, lane);
             if (a.job[2].M > 0) r.run<kDw, false>(a.job[2], c, g, sh, ring, rank, lane);
@@ -887,13 +953,14 @@ int launch(moe::Launch<P>& a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, moe::ffn_kernel<P, FP8>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-moe::Common common_of(const MoePlanOut* plan, int64_t rows, int E) {
+moe::Common common_of(const MoePlanOut* plan, int64_t rows, int E, int early) {
     moe::Common c = {};
     c.cu = plan->cu_seqlens;
     c.count = plan->tokens_per_expert;
     c.status = plan->status;
     c.rows = rows;
     c.E = E;
+    c.early = early;
     c.timeout_ns = moe_host::timeout_ns();
     return c;
 }
@@ -902,7 +969,7 @@ template <bool FP8>
 int launch_gated(const void* x, const float* x_scale, const void* w_gate_up, const float* w_scale, int64_t rows, int E,
                  int H, int I, const MoePlanOut* plan, uint16_t* h, float* preact, cudaStream_t stream) {
     moe::Launch<moe::kGated> a = {};
-    a.c = common_of(plan, rows, E);
+    a.c = common_of(plan, rows, E, 0);
     a.c.a_scale = x_scale;
     a.c.b_scale = w_scale;
     a.c.preact_out = preact;
@@ -933,7 +1000,7 @@ extern "C" MOE_API int moe_expert_ffn(const void* x, const float* x_scale, const
                        : launch_gated<false>(x, nullptr, w_gate_up, nullptr, rows, E, H, I, plan, h, preact, stream);
     if (rg != MOE_OK) return rg;
     moe::Launch<moe::kDown> a = {};
-    a.c = common_of(plan, rows, E);
+    a.c = common_of(plan, rows, E, 1);
     const int rd = make_job<moe::kDown>(&a.job[0], w_down, h, rows, E, H, 0, I, y);
     return rd != MOE_OK ? rd : launch<moe::kDown>(a, stream);
 }
@@ -963,7 +1030,7 @@ extern "C" MOE_API int moe_expert_ffn_backward(const uint16_t* dy, const uint16_
     }
     if (dx != nullptr || dw_gate_up != nullptr) {
         moe::Launch<moe::kDgate> a = {};
-        a.c = common_of(plan, rows, E);
+        a.c = common_of(plan, rows, E, 0);
         a.c.preact_in = preact;
         rc = make_job<moe::kDgate>(&a.job[0], w_down, dy, rows, E, I, 0, H, dgate_up);
         if (rc == MOE_OK) rc = launch<moe::kDgate>(a, stream);
@@ -971,7 +1038,7 @@ extern "C" MOE_API int moe_expert_ffn_backward(const uint16_t* dy, const uint16_
     }
     if (dx == nullptr && dw_gate_up == nullptr && dw_down == nullptr) return MOE_OK;
     moe::Launch<moe::kGrads> a = {};
-    a.c = common_of(plan, rows, E);
+    a.c = common_of(plan, rows, E, dx != nullptr || dw_gate_up != nullptr);
     if (dx != nullptr) rc = make_job<moe::kDx>(&a.job[0], w_gate_up, dgate_up, rows, E, H, 0, 2 * I, dx);
     if (rc == MOE_OK && dw_gate_up != nullptr)
         rc = make_job<moe::kDw>(&a.job[1], dgate_up, x, rows, E, 2 * I, H, 0, dw_gate_up);
