@@ -715,18 +715,22 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         sh->ready = 0;
     }
     __syncwarp();
+    if (warp == 1) tmem_alloc(&sh->tmem, 512);
     // A call's later kernels start while the one before still runs: the groups
-    // and the weights were there before that one began.
+    // and the weights were there before that one began, and only the warps that
+    // touch the rows wait for it.
     if (!c.early) {
         pdl_wait();
         pdl_trigger();
     }
+    if (tid == 0) sh->stop = ld_volatile_s32(c.status) != 0;
 
-    // ---- the groups: row tiles before each expert, and the longest group
+    // ---- the groups: row tiles before each expert
     const int per = (E + kThreads - 1) / kThreads;
     int mine = 0, longest = 0;
     for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) {
-        const int64_t f = __ldg(c.cu + e), n = __ldg(c.count + e), p = n == 0 ? 0 : __ldg(c.cu + e + 1) - f;
+        const int64_t f = __ldg(c.cu + e), n = __ldg(c.count + e), after = __ldg(c.cu + e + 1);
+        const int64_t p = n == 0 ? 0 : after - f;
         const bool fits = n >= 0 && f >= 0 && p >= n && f + p <= c.rows;
         if (!fits) record_error(c.status, MOE_ERR_DEVICE_INDEX, e);
         first[e] = fits ? static_cast<int>(f) : 0;
@@ -769,34 +773,26 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     Turn turn;
     turn.next = blockIdx.x >> 1;
     turn.pairs = static_cast<int>(gridDim.x >> 1);
-    Producer producer;
-    producer.turn = turn;
-    if (c.early) {
-        if (tid == 0) sh->stop = ld_volatile_s32(c.status) != 0;
-        __syncthreads();
-        pair_sync();  // both blocks' barriers are ready
-        if (warp == 0 && sh->stop == 0) {
-            if constexpr (P == kDown) producer.start<P, FP8>(a.job[0], g, sh, ring, rank, lane);
-            if constexpr (P == kGrads)
-                if (a.job[0].M > 0) producer.start<kDx, false>(a.job[0], g, sh, ring, rank, lane);
-        }
-        __syncwarp();
-        pdl_wait();
-        pdl_trigger();
-    }
-    if (tid == 0) sh->stop = ld_volatile_s32(c.status) != 0;
-    if (warp == 1) tmem_alloc(&sh->tmem, 512);
     tc_fence_before();
     __syncthreads();
     pair_sync();  // both blocks' barriers and tensor memory are ready
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
     const bool run = sh->stop == 0;
+    if (!run && c.early) pdl_wait();
 
-    if (warp == 0) {
-        Producer& r = producer;
-        if (!run) r.ok = r.ahead == 0;
-        else if constexpr (P == kGrads) {
+    if (run && warp == 0) {
+        Producer r;
+        r.turn = turn;
+        if (c.early) {
+            if constexpr (P == kDown) r.start<P, FP8>(a.job[0], g, sh, ring, rank, lane);
+            if constexpr (P == kGrads)
+                if (a.job[0].M > 0) r.start<kDx, false>(a.job[0], g, sh, ring, rank, lane);
+            __syncwarp();
+            pdl_wait();
+            pdl_trigger();
+        }
+        if constexpr (P == kGrads) {
             if (a.job[0].M > 0) r.run<kDx, false>(a.job[0], c, g, sh, ring, rank, lane);
             if (a.job[1].M > 0) r.run<kDw, false>(a.job[1], c, g, sh, ring, rank, lane);
             if (a.job[2].M > 0) r.run<kDw, false>(a.job[2], c, g, sh, ring, rank, lane);
@@ -826,6 +822,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     } else if (run && warp >= 2 && warp < kWatchWarp) {
         Drain r;
         r.turn = turn;
+        if (c.early) pdl_wait();
         uint8_t* turn_buf = turns + (warp - 2) * ffn_turn(P);
         if constexpr (P == kGrads) {
             if (a.job[0].M > 0) r.run<kDx, false>(a.job[0], c, g, sh, tmem, rank, warp, lane, turn_buf);
