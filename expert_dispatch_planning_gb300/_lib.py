@@ -113,6 +113,23 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
+_binding = None
+
+
+def binding():
+    """The compiled torch binding (the operators around the experts); raise if it has not been built."""
+    global _binding
+    if _binding is None:
+        load()
+        try:
+            from . import _torch_binding
+        except ImportError as e:
+            raise ImportError("_torch_binding.so is not built for this torch (%s); run `python -c \"import __graft_entry__ "
+                              "as g; g.build()\"` first" % e) from e
+        _binding = _torch_binding
+    return _binding
+
+
 def status_string(code: int) -> str:
     try:
         return load().moe_status_string(int(code)).decode()

@@ -328,26 +328,11 @@ def combine(y: torch.Tensor, topk_w: torch.Tensor, p: Plan, out: torch.Tensor | 
 
 
 # ---------------------------------------------------------------- around the experts
-_DTYPE = {torch.bfloat16: _lib.MOE_DTYPE_BF16, torch.float32: _lib.MOE_DTYPE_F32,
-          torch.float8_e4m3fn: _lib.MOE_DTYPE_E4M3}
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
-def _plan_struct(p, names):
-    """The C struct of a plan: a Plan's own, or one over the arrays `names` of
-    any object that has them (a grouping the caller made without plan())."""
-    c = getattr(p, "c_struct", None)
-    if c is not None:
-        return ctypes.byref(c)
-    c = MoePlanOut()
-    for k in names:
-        t = getattr(p, k)
-        if t.dtype is not torch.int32 or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError("%s must be a contiguous CUDA int32 tensor" % k)
-        setattr(c, k, t.data_ptr())
-    return ctypes.byref(c)
-
-
-@dataclass
+@dataclass(slots=True)
 class NormOut:
     """Outputs of residual_norm (device tensors; None where not asked for)."""
     y: torch.Tensor | None
@@ -367,43 +352,11 @@ def residual_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
     residual_out=residual to update it in place); quantize adds the row-scaled
     8-bit output, q float8_e4m3fn[N,H] with q * q_scale[:, None] = y.
     """
-    N, H = x.shape
-    dev = x.device
-    _need(x, torch.bfloat16, (N, H), "x")
-    if weight.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("weight must be bfloat16 or float32 (got %s)" % weight.dtype)
-    _need(weight, weight.dtype, (H,), "weight")
-    if residual is not None:
-        if residual.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError("residual must be bfloat16 or float32 (got %s)" % residual.dtype)
-        _need(residual, residual.dtype, (N, H), "residual")
-        if residual_out is None:
-            residual_out = torch.empty_like(residual)
-        else:
-            _need(residual_out, residual.dtype, (N, H), "residual_out")
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    if out is None:
-        out = torch.empty_like(x)
-    else:
-        _need(out, torch.bfloat16, (N, H), "out")
-    rstd = torch.empty(N, dtype=torch.float32, device=dev)
-    if quantize:
-        if q is None:
-            q = torch.empty((N, H), dtype=torch.float8_e4m3fn, device=dev)
-        else:
-            _need(q, torch.float8_e4m3fn, (N, H), "q")
-        if q_scale is None:
-            q_scale = torch.empty(N, dtype=torch.float32, device=dev)
-        else:
-            _need(q_scale, torch.float32, (N,), "q_scale")
-    elif q is not None or q_scale is not None:
-        raise ValueError("q and q_scale need quantize=True")
-    rc = load().moe_residual_norm(_ptr(x), _ptr(residual), _DTYPE[torch.bfloat16 if residual is None else residual.dtype],
-                                  _ptr(weight), _DTYPE[weight.dtype], N, H, float(eps), _ptr(out), _ptr(residual_out),
-                                  _ptr(rstd), _ptr(q), _ptr(q_scale), _stream(stream))
-    check("moe_residual_norm", rc)
-    return NormOut(out, residual_out, rstd, q, q_scale)
+    r = _lib.binding().residual_norm(x, weight, residual, eps, bool(quantize), out, residual_out, q, q_scale,
+                                     _handle(stream))
+    if type(r) is int:
+        check("moe_residual_norm", r)
+    return NormOut(*r)
 
 
 def residual_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -414,28 +367,10 @@ def residual_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tens
     reaches it from the residual stream, in its type.  dx is the gradient of x,
     and of a bf16 residual; dres that of a float32 one.
     """
-    N, H = dy.shape
-    dev = dy.device
-    _need(dy, torch.bfloat16, (N, H), "dy")
-    if s.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("s must be bfloat16 or float32 (got %s)" % s.dtype)
-    _need(s, s.dtype, (N, H), "s")
-    if weight.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("weight must be bfloat16 or float32 (got %s)" % weight.dtype)
-    _need(weight, weight.dtype, (H,), "weight")
-    _need(rstd, torch.float32, (N,), "rstd")
-    if ds is not None:
-        _need(ds, s.dtype, (N, H), "ds")
-    dx = torch.empty((N, H), dtype=torch.bfloat16, device=dev)
-    dres = torch.empty((N, H), dtype=torch.float32, device=dev) if s.dtype == torch.float32 else None
-    dweight = torch.empty(H, dtype=torch.float32, device=dev)
-    lib = load()
-    ws = torch.empty(int(lib.moe_residual_norm_backward_workspace_size(N, H)), dtype=torch.uint8, device=dev)
-    rc = lib.moe_residual_norm_backward(_ptr(dy), _ptr(s), _DTYPE[s.dtype], _ptr(weight), _DTYPE[weight.dtype],
-                                        _ptr(rstd), _ptr(ds), N, H, _ptr(dx), _ptr(dres), _ptr(dweight), _ptr(ws),
-                                        ws.numel(), _stream(stream))
-    check("moe_residual_norm_backward", rc)
-    return dx, dres, dweight
+    r = _lib.binding().residual_norm_backward(dy, s, weight, rstd, ds, _handle(stream))
+    if type(r) is int:
+        check("moe_residual_norm_backward", r)
+    return r
 
 
 def expert_ffn(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, p, x_scale: torch.Tensor | None = None,
@@ -450,39 +385,11 @@ def expert_ffn(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, p
     float32[rows,2,I]; the call fills them.  Rows of no group are not read; in
     y a group's padding rows become zeros and rows past the groups are untouched.
     """
-    rows, H = x.shape
-    if w_gate_up.dim() != 4:
-        raise ValueError("w_gate_up must have shape [E, 2, I, H] (got %s)" % (tuple(w_gate_up.shape),))
-    E, _, I, _ = w_gate_up.shape  # noqa: E741
-    if x.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise ValueError("x must be bfloat16 or float8_e4m3fn (got %s)" % x.dtype)
-    _need(x, x.dtype, (rows, H), "x")
-    _need(w_gate_up, x.dtype, (E, 2, I, H), "w_gate_up")
-    _need(w_down, torch.bfloat16, (E, H, I), "w_down")
-    if x.dtype == torch.float8_e4m3fn:
-        if x_scale is None or w_scale is None:
-            raise ValueError("8-bit rows and weights need x_scale and w_scale")
-        _need(x_scale, torch.float32, (rows,), "x_scale")
-        _need(w_scale, torch.float32, (E, 2, I), "w_scale")
-    elif x_scale is not None or w_scale is not None:
-        raise ValueError("x_scale and w_scale go with 8-bit rows and weights")
-    if p.tokens_per_expert.numel() != E:
-        raise ValueError("the plan has %d experts, w_gate_up %d" % (p.tokens_per_expert.numel(), E))
-    if h is None:
-        h = torch.empty((rows, I), dtype=torch.bfloat16, device=x.device)
-    else:
-        _need(h, torch.bfloat16, (rows, I), "h")
-    if preact is not None:
-        _need(preact, torch.float32, (rows, 2, I), "preact")
-    if out is None:
-        out = torch.empty((rows, H), dtype=torch.bfloat16, device=x.device)
-    else:
-        _need(out, torch.bfloat16, (rows, H), "out")
-    rc = load().moe_expert_ffn(_ptr(x), _ptr(x_scale), _ptr(w_gate_up), _ptr(w_scale), _ptr(w_down), rows, E, H, I,
-                               _DTYPE[x.dtype], _plan_struct(p, ("cu_seqlens", "tokens_per_expert", "status")), _ptr(h),
-                               _ptr(preact), _ptr(out), _stream(stream))
-    check("moe_expert_ffn", rc)
-    return out
+    r = _lib.binding().expert_ffn(x, w_gate_up, w_down, p.cu_seqlens, p.tokens_per_expert, p.status, x_scale, w_scale, h,
+                                  preact, out, _handle(stream))
+    if type(r) is int:
+        check("moe_expert_ffn", r)
+    return r
 
 
 def expert_ffn_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, preact: torch.Tensor,
@@ -493,37 +400,11 @@ def expert_ffn_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, prea
     h and preact as the forward call filled them.  dgate_up bf16[rows,2,I] is a
     workspace.  need_dx / need_dw = False leaves those out (None is returned).
     """
-    rows, H = x.shape
-    if w_gate_up.dim() != 4:
-        raise ValueError("w_gate_up must have shape [E, 2, I, H] (got %s)" % (tuple(w_gate_up.shape),))
-    E, _, I, _ = w_gate_up.shape  # noqa: E741
-    bf16 = torch.bfloat16
-    _need(x, bf16, (rows, H), "x")
-    _need(dy, bf16, (rows, H), "dy")
-    _need(h, bf16, (rows, I), "h")
-    _need(preact, torch.float32, (rows, 2, I), "preact")
-    _need(w_gate_up, bf16, (E, 2, I, H), "w_gate_up")
-    _need(w_down, bf16, (E, H, I), "w_down")
-    if p.tokens_per_expert.numel() != E:
-        raise ValueError("the plan has %d experts, w_gate_up %d" % (p.tokens_per_expert.numel(), E))
-    if dgate_up is None:
-        dgate_up = torch.empty((rows, 2, I), dtype=bf16, device=x.device)
-    else:
-        _need(dgate_up, bf16, (rows, 2, I), "dgate_up")
-    if need_dx:
-        if dx is None:
-            dx = torch.empty_like(x)
-        else:
-            _need(dx, bf16, (rows, H), "dx")
-    elif dx is not None:
-        raise ValueError("dx is given but need_dx is False")
-    dwgu = torch.empty_like(w_gate_up) if need_dw else None
-    dwd = torch.empty_like(w_down) if need_dw else None
-    rc = load().moe_expert_ffn_backward(_ptr(dy), _ptr(x), _ptr(h), _ptr(preact), _ptr(w_gate_up), _ptr(w_down), rows, E,
-                                        H, I, _plan_struct(p, ("cu_seqlens", "tokens_per_expert", "status")),
-                                        _ptr(dgate_up), _ptr(dx), _ptr(dwgu), _ptr(dwd), _stream(stream))
-    check("moe_expert_ffn_backward", rc)
-    return dx, dwgu, dwd
+    r = _lib.binding().expert_ffn_backward(dy, x, h, preact, w_gate_up, w_down, p.cu_seqlens, p.tokens_per_expert, p.status,
+                                           dx, dgate_up, bool(need_dx), bool(need_dw), _handle(stream))
+    if type(r) is int:
+        check("moe_expert_ffn_backward", r)
+    return r
 
 
 def combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor, p, dy: torch.Tensor | None = None,
@@ -534,26 +415,10 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor, 
     object with dst, zero_fill_ranges and status.  In dy the groups' padding
     rows become zeros and rows past the groups are untouched.
     """
-    N, H = dout.shape
-    rows = y.shape[0]
-    K, E = p.dst.shape[1], p.zero_fill_ranges.shape[0]
-    _need(dout, torch.bfloat16, (N, H), "dout")
-    _need(y, torch.bfloat16, (rows, H), "y")
-    _need(topk_w, torch.float32, (N, K), "topk_w")
-    _need(p.dst, torch.int32, (N, K), "dst")
-    if dy is None:
-        dy = torch.empty_like(y)
-    else:
-        _need(dy, torch.bfloat16, (rows, H), "dy")
-    if dw is None:
-        dw = torch.empty_like(topk_w)
-    else:
-        _need(dw, torch.float32, (N, K), "dw")
-    rc = load().moe_combine_backward(_ptr(dout), _ptr(y), _ptr(topk_w), N, K, H, E, rows,
-                                     _plan_struct(p, ("dst", "zero_fill_ranges", "status")), _ptr(dy), _ptr(dw),
-                                     _stream(stream))
-    check("moe_combine_backward", rc)
-    return dy, dw
+    r = _lib.binding().combine_backward(dout, y, topk_w, p.dst, p.zero_fill_ranges, p.status, dy, dw, _handle(stream))
+    if type(r) is int:
+        check("moe_combine_backward", r)
+    return r
 
 
 def get_status(p: Plan, stream=None) -> int:

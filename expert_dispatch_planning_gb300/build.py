@@ -3,6 +3,8 @@
 Each ``csrc/*.cu`` file is compiled to an object in parallel, then linked
 into one shared library with the CUDA runtime linked statically (so the
 library does not depend on which libcudart the process already loaded).
+``csrc/torch_binding.cpp`` becomes ``_torch_binding.so``, a Python module that
+calls the library on tensors of the installed torch.
 """
 from __future__ import annotations
 
@@ -19,6 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libmoe_dispatch.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
+BINDING_PATH = os.path.join(HERE, "_torch_binding.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -61,6 +65,41 @@ def _compile(src, extra, verbose):
     return obj
 
 
+def _compile_binding():
+    """The object of the torch binding (compiled against the installed torch)."""
+    import sysconfig
+
+    import torch
+    obj = os.path.join(BUILD_DIR, "torch_binding.o")
+    root = os.path.dirname(torch.__file__)
+    if not _stale(obj, [BINDING_SRC, __file__, os.path.join(root, "version.py")] + _headers()):
+        return obj
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    includes = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *["-I" + d for d in includes], "-c", BINDING_SRC,
+           "-o", obj + ".tmp"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (BINDING_SRC, " ".join(cmd), res.stderr))
+    os.replace(obj + ".tmp", obj)
+    return obj
+
+
+def _link_binding(obj):
+    import torch
+    if not _stale(BINDING_PATH, [obj, LIB_PATH]):
+        return
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:" + LIB_NAME, "-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(verbose: bool = False, extra_flags=None, force: bool = False) -> str:
     """Compile and link; returns the path of the shared library."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -69,8 +108,10 @@ def build(verbose: bool = False, extra_flags=None, force: bool = False) -> str:
     if force:
         for f in os.listdir(BUILD_DIR):
             os.remove(os.path.join(BUILD_DIR, f))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(10, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, extra, verbose), srcs))
+        binding = binding.result()
     if _stale(LIB_PATH, objs) or extra or force:
         tmp = LIB_PATH + ".tmp%d" % os.getpid()
         cmd = [nvcc(), *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -78,6 +119,7 @@ def build(verbose: bool = False, extra_flags=None, force: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
         os.replace(tmp, LIB_PATH)
+    _link_binding(binding)
     return LIB_PATH
 
 

@@ -716,6 +716,9 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     }
     __syncwarp();
     if (warp == 1) tmem_alloc(&sh->tmem, 512);
+    tc_fence_before();
+    __syncwarp();
+    pair_arrive();  // this warp's part of the block is set up; the wait comes after the groups' scan
     // A call's later kernels start while the one before still runs: the groups
     // and the weights were there before that one began, and only the warps that
     // touch the rows wait for it.
@@ -773,9 +776,8 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     Turn turn;
     turn.next = blockIdx.x >> 1;
     turn.pairs = static_cast<int>(gridDim.x >> 1);
-    tc_fence_before();
     __syncthreads();
-    pair_sync();  // both blocks' barriers and tensor memory are ready
+    pair_wait();  // both blocks' barriers and tensor memory are ready
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
     const bool run = sh->stop == 0;
@@ -844,7 +846,8 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    pair_sync();  // neither block leaves while the other may still use its barriers or tensor memory
+    pair_arrive();
+    pair_wait();  // neither block leaves while the other may still use its barriers or tensor memory
     if (warp == 1) {
         tc_fence_after();
         tmem_free(tmem, 512);
@@ -858,10 +861,13 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Row indexes and a tile's past them stay within 32 bits.
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - (1 << 24);
+
 int check_sizes(int64_t rows, int E, int H, int I, const MoePlanOut* plan) {
     if (plan == nullptr || plan->cu_seqlens == nullptr || plan->tokens_per_expert == nullptr || plan->status == nullptr)
         return MOE_ERR_INVALID_ARG;
-    if (rows < 0 || rows >= (int64_t(1) << 31) || E < 1 || E > 1024 || H < 8 || H % 8 != 0 || H >= (1 << 20) || I < 8 ||
+    if (rows < 0 || rows > kMaxRows || E < 1 || E > 1024 || H < 8 || H % 8 != 0 || H >= (1 << 20) || I < 8 ||
         I % 8 != 0 || I >= (1 << 20))
         return MOE_ERR_INVALID_ARG;
     return MOE_OK;

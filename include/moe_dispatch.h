@@ -466,7 +466,7 @@ MOE_API int moe_residual_norm_backward(const uint16_t* dy, const void* s, int s_
  *   w_scale    (device) float32[E][2][I] with e4m3, one scale a channel; else NULL.
  *   w_down     (device) bf16[E][H][I].
  *   rows       rows of x, h, preact and y (the plan's capacity, or at least
- *              cu_seqlens[E]); rows < 2^31.
+ *              cu_seqlens[E]); at most 2^31 - 2^24.
  *   plan       uses cu_seqlens, tokens_per_expert and status.  A group that
  *              leaves [0, rows) sets MOE_ERR_DEVICE_INDEX and is not touched
  *              (the other outputs are then unspecified); with an error in
