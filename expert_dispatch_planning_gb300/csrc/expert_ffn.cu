@@ -247,57 +247,53 @@ struct Producer {
         return n;
     }
 
-    // Both blocks' copies are counted by the first one's barrier, but those of
-    // a slice that has to be mended by each block's own.
+    // Where a tile's copies come from: the coordinates that stay for all its slices.
+    struct Source {
+        int m, e, first;     // M side: channel, expert; dw: the group's first row
+        int n;               // N side: first row (dw: column)
+        const CUtensorMap* map_n;
+        NSide side;
+    };
     template <int P>
-    static __device__ __forceinline__ bool mended(const Tile& t, int k) {
-        return P == kDw && k + 1 == t.slices && (t.count & 15) != 0;
+    __device__ __forceinline__ Source source(const Job& job, const Tile& t, int rank) const {
+        Source f;
+        f.side = n_side<P>(job, t);
+        f.m = t.m0 + rank * (P == kGated ? 64 : kHalf);
+        f.e = t.e;
+        f.first = t.first;
+        f.n = (P == kDw ? t.n0 : t.first + t.n0) + rank * f.side.rows;
+        f.map_n = P == kDw || f.side.piece == 128 ? &job.map_n : f.side.piece == 32 ? &job.map_n32 : &job.map_n16;
+        return f;
     }
+    // A block's part of the slice that starts at k.
     template <int P>
-    __device__ __forceinline__ void arm(Shared* sh, const Tile& t, int k, uint32_t bytes, int rank) const {
-        if (mended<P>(t, k)) mbar_arrive_expect_tx(&sh->tail_full[s], bytes);
-        else if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], 2 * bytes);
-    }
-    template <int P>
-    __device__ __forceinline__ uint32_t barrier(Shared* sh, const Tile& t, int k, int rank) const {
-        if (mended<P>(t, k)) return smem_addr(&sh->tail_full[s]);
-        return rank == 0 ? smem_addr(&sh->full[s]) : leader_addr(&sh->full[s]);
-    }
-    template <int P, bool FP8>
-    __device__ __forceinline__ void copy_m(const Job& job, const Tile& t, int k, uint8_t* to, int rank,
-                                           uint32_t bar) const {
-        const int m = t.m0 + rank * (P == kGated ? 64 : kHalf), at = k * (FP8 ? 128 : 64);
+    static __device__ __forceinline__ void copy_m(const Job& job, const Source& f, int k, uint32_t to, uint32_t bar) {
         if constexpr (P == kGated) {
-            if (job.m_whole) tensor_load_5d(to, &job.map_m, at, 0, 0, m / 16, t.e, bar);
+            if (job.m_whole) tensor_load_5d(to, &job.map_m, k, 0, 0, f.m / 16, f.e, bar);
             else
-                for (int j = 0; j < 4; ++j) tensor_load_4d(to + j * 4096, &job.map_m, at, m + 16 * j, 0, t.e, bar);
+                for (int j = 0; j < 4; ++j) tensor_load_4d(to + j * 4096, &job.map_m, k, f.m + 16 * j, 0, f.e, bar);
         } else if constexpr (P == kDown) {
-            tensor_load_3d(to, &job.map_m, at, m, t.e, bar);
+            tensor_load_3d(to, &job.map_m, k, f.m, f.e, bar);
         } else if constexpr (P == kDw) {
-            if (job.m_whole) tensor_load_3d(to, &job.map_m, 0, t.first + at, m / 64, bar);
+            if (job.m_whole) tensor_load_3d(to, &job.map_m, 0, f.first + k, f.m / 64, bar);
             else
-                for (int j = 0; j < 2; ++j) tensor_load_2d(to + j * 8192, &job.map_m, m + 64 * j, t.first + at, bar);
+                for (int j = 0; j < 2; ++j) tensor_load_2d(to + j * 8192, &job.map_m, f.m + 64 * j, f.first + k, bar);
         } else {
-            if (job.m_whole) tensor_load_4d(to, &job.map_m, 0, at, m / 64, t.e, bar);
+            if (job.m_whole) tensor_load_4d(to, &job.map_m, 0, k, f.m / 64, f.e, bar);
             else
-                for (int j = 0; j < 2; ++j) tensor_load_3d(to + j * 8192, &job.map_m, m + 64 * j, at, t.e, bar);
+                for (int j = 0; j < 2; ++j) tensor_load_3d(to + j * 8192, &job.map_m, f.m + 64 * j, k, f.e, bar);
         }
     }
-    template <int P, bool FP8>
-    __device__ __forceinline__ void copy_n(const Job& job, const Tile& t, const NSide& n, int k, uint8_t* to, int rank,
-                                           uint32_t bar) const {
-        const int at = k * (FP8 ? 128 : 64);
+    template <int P>
+    static __device__ __forceinline__ void copy_n(const Job& job, const Source& f, int k, uint32_t to, uint32_t bar) {
         if constexpr (P == kDw) {
-            const int col = t.n0 + rank * n.rows;
-            if (job.n_whole) tensor_load_3d(to, &job.map_n, 0, t.first + at, col / 64, bar);
+            if (job.n_whole) tensor_load_3d(to, f.map_n, 0, f.first + k, f.n / 64, bar);
             else
-                for (int j = 0; j < n.pieces; ++j)
-                    tensor_load_2d(to + j * 8192, &job.map_n, col + 64 * j, t.first + at, bar);
+                for (int j = 0; j < f.side.pieces; ++j) tensor_load_2d(to + j * 8192, f.map_n, f.n + 64 * j, f.first + k, bar);
         } else {
-            const CUtensorMap* map = n.piece == 128 ? &job.map_n : n.piece == 32 ? &job.map_n32 : &job.map_n16;
-            const int row = t.first + t.n0 + rank * n.rows;
-            for (int j = 0; j < n.pieces; ++j)
-                tensor_load_2d(to + j * n.piece * kSlice, map, at, row + n.piece * j, bar);
+            tensor_load_2d(to, f.map_n, k, f.n, bar);
+            for (int j = 1; j < f.side.pieces; ++j)
+                tensor_load_2d(to + j * f.side.piece * kSlice, f.map_n, k, f.n + f.side.piece * j, bar);
         }
     }
 
@@ -308,33 +304,45 @@ struct Producer {
         Tiles<P, FP8> tiles(job, g);
         if (turn.next >= tiles.total) return;
         const Tile t = tiles.at(g, turn.next, lane);
+        const Source f = source<P>(job, t, rank);
         ahead = min(ring.stages, t.slices);
         if (lane == 0)
-            for (int k = 0; k < ahead; ++k, ++s) {
-                arm<P>(sh, t, k, n_side<P>(job, t).bytes, rank);
-                copy_m<P, FP8>(job, t, k, ring.at + s * ring.stage_bytes, rank, barrier<P>(sh, t, k, rank));
+            for (int k = 0; k < ahead; ++k) {
+                const uint32_t bar = rank == 0 ? smem_addr(&sh->full[k]) : leader_addr(&sh->full[k]);
+                if (rank == 0) mbar_expect(bar, 2 * f.side.bytes);
+                copy_m<P>(job, f, k * (FP8 ? 128 : 64), smem_addr(ring.at + k * ring.stage_bytes), bar);
             }
-        s = 0;
     }
 
     template <int P, bool FP8>
     __device__ __forceinline__ void run(const Job& job, const Common& c, const Groups& g, Shared* sh,
                                         const RingShape& ring, int rank, int lane) {
+        constexpr int kElems = FP8 ? 128 : 64;
         Tiles<P, FP8> tiles(job, g);
+        const uint32_t base = smem_addr(ring.at);
+        const uint32_t full = rank == 0 ? smem_addr(&sh->full[0]) : leader_addr(&sh->full[0]);
         for (; ok && turn.next < tiles.total; turn.next += turn.pairs) {
             const Tile t = tiles.at(g, turn.next, lane);
-            const NSide n = n_side<P>(job, t);
+            const Source f = source<P>(job, t, rank);
+            // Both blocks' copies are counted by the first one's barrier, but those
+            // of a slice that has to be mended by each block's own.
+            const int mended = P == kDw && (t.count & 15) != 0 ? t.slices - 1 : -1;
             for (int k = 0; k < t.slices && lane == 0; ++k) {
-                uint8_t* to = ring.at + s * ring.stage_bytes;
-                const uint32_t bar = barrier<P>(sh, t, k, rank);
+                const uint32_t to = base + static_cast<uint32_t>(s) * ring.stage_bytes;
+                uint32_t bar = full + 8u * static_cast<uint32_t>(s);
                 if (ahead > 0) {
                     --ahead;
                 } else {
                     if (!(ok = wait(c, &sh->empty[s], phase ^ 1u))) break;
-                    arm<P>(sh, t, k, n.bytes, rank);
-                    copy_m<P, FP8>(job, t, k, to, rank, bar);
+                    if (P == kDw && k == mended) {
+                        bar = smem_addr(&sh->tail_full[s]);
+                        mbar_expect(bar, f.side.bytes);
+                    } else if (rank == 0) {
+                        mbar_expect(bar, 2 * f.side.bytes);
+                    }
+                    copy_m<P>(job, f, k * kElems, to, bar);
                 }
-                copy_n<P, FP8>(job, t, n, k, to + kHalf * kSlice, rank, bar);
+                copy_n<P>(job, f, k * kElems, to + kHalf * kSlice, bar);
                 if (++s == ring.stages) {
                     s = 0;
                     phase ^= 1u;
@@ -518,13 +526,32 @@ __device__ __forceinline__ void store4_bf16(uint16_t* p, float a, float b, float
     *reinterpret_cast<uint2*>(p) = make_uint2(pack2(a, b), pack2(c, d));
 }
 
+// dgate: the pre-activations that a lane needs for a chunk.
+struct Saved {
+    float4 g[kChunk / 4], u[kChunk / 4];
+};
+__device__ __forceinline__ void load_saved(Saved& s, const Job& job, const Common& a, const Tile& t, int rank, int c0,
+                                           int quarter, int lane) {
+    const int64_t M = job.M;
+    const int c = t.m0 + rank * kHalf + quarter * 32 + (lane & 7) * 4;
+#pragma unroll
+    for (int it = 0; it < kChunk / 4; ++it) {
+        const int n = c0 + it * 4 + (lane >> 3);
+        if (n < t.n && c < M) {
+            const float* pre = a.preact_in + (t.first + static_cast<int64_t>(t.n0 + n)) * 2 * M + c;
+            s.g[it] = ld_stream_f4(pre);
+            s.u[it] = ld_stream_f4(pre + M);
+        }
+    }
+}
+
 // One chunk of a row product: 16 rows of the group by the warp's 32 channels,
 // turned through `turn` [16][32] so that neighbouring lanes hold neighbouring
 // channels.  Odd rows have their halves swapped: the gated product reads two
 // rows' same half at a time.
 template <int P>
 __device__ __forceinline__ void epilogue_chunk(const Job& job, const Common& a, const Tile& t, int rank, uint32_t acc,
-                                               int c0, int quarter, int lane, float* turn) {
+                                               int c0, int quarter, int lane, float* turn, const Saved& saved) {
     const int64_t M = job.M;
     uint32_t v[kChunk];
     auto turned = [&](int j, int c) { return reinterpret_cast<float4*>(turn + j * 32 + (c ^ ((j & 1) << 4))); };
@@ -562,18 +589,6 @@ __device__ __forceinline__ void epilogue_chunk(const Job& job, const Common& a, 
     } else {
         const int c = t.m0 + rank * kHalf + quarter * 32 + (lane & 7) * 4;
         constexpr int kIts = kChunk / 4;
-        float4 g[P == kDgate ? kIts : 1], u[P == kDgate ? kIts : 1];
-        if constexpr (P == kDgate) {  // asked for before the accumulators are read
-#pragma unroll
-            for (int it = 0; it < kIts; ++it) {
-                const int n = c0 + it * 4 + (lane >> 3);
-                if (n < t.n && c < M) {
-                    const float* pre = a.preact_in + (t.first + static_cast<int64_t>(t.n0 + n)) * 2 * M + c;
-                    g[it] = ld_stream_f4(pre);
-                    u[it] = ld_stream_f4(pre + M);
-                }
-            }
-        }
         turn_in();
 #pragma unroll
         for (int it = 0; it < kIts; ++it) {
@@ -582,8 +597,8 @@ __device__ __forceinline__ void epilogue_chunk(const Job& job, const Common& a, 
             const int64_t row = t.first + static_cast<int64_t>(t.n0 + n);
             const float4 d = *turned(j, (lane & 7) * 4);
             if constexpr (P == kDgate) {
-                const float dh[4] = {d.x, d.y, d.z, d.w}, gs[4] = {g[it].x, g[it].y, g[it].z, g[it].w},
-                            us[4] = {u[it].x, u[it].y, u[it].z, u[it].w};
+                const float dh[4] = {d.x, d.y, d.z, d.w}, gs[4] = {saved.g[it].x, saved.g[it].y, saved.g[it].z, saved.g[it].w},
+                            us[4] = {saved.u[it].x, saved.u[it].y, saved.u[it].z, saved.u[it].w};
                 float dg[4], du[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -650,6 +665,8 @@ struct Drain {
         Tiles<P, FP8> tiles(job, g);
         for (; ok && turn.next < tiles.total; turn.next += turn.pairs) {
             const Tile t = tiles.at(g, turn.next, lane);
+            Saved now, next;  // dgate: asked for before the products are done, and a chunk ahead
+            if constexpr (P == kDgate) load_saved(now, job, c, t, rank, half * kChunk, quarter, lane);
             if (t.slices > 0) {
                 ok = __all_sync(FULL_MASK, wait(c, &sh->acc_full[buf], acc_phase));
                 if (!ok) break;
@@ -659,8 +676,11 @@ struct Drain {
             if constexpr (P == kDw) {
                 for (int n = half * 64; n < t.n; n += 128) epilogue_dw(job, t, rank, acc, n, quarter, lane, reinterpret_cast<uint4*>(turn_buf));
             } else {
-                for (int n = half * kChunk; n < t.n; n += 2 * kChunk)
-                    epilogue_chunk<P>(job, c, t, rank, acc, n, quarter, lane, reinterpret_cast<float*>(turn_buf));
+                for (int n = half * kChunk; n < t.n; n += 2 * kChunk) {
+                    if constexpr (P == kDgate) load_saved(next, job, c, t, rank, n + 2 * kChunk, quarter, lane);
+                    epilogue_chunk<P>(job, c, t, rank, acc, n, quarter, lane, reinterpret_cast<float*>(turn_buf), now);
+                    if constexpr (P == kDgate) now = next;
+                }
             }
             if (t.slices > 0) {
                 tc_fence_before();
