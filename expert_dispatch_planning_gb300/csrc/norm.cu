@@ -17,6 +17,10 @@
 //     works on a row, so that the row's reductions never empty the memory
 //     pipeline.  A thread reads only what it copied, so the ring needs no
 //     barrier; the row's sums take one each.
+// Measured (GB300, copy rate 6.68 TB/s): forward with a bf16 residual and the
+// 8-bit output at 8192 x 7168, 84 us, 6.3 TB/s (a block a row: 95 us; issue
+// slots bound it, 66% taken, until the values' divisions became products);
+// backward with fp32 sums at 16384 x 4096, 165 us, 6.5 TB/s (a block a row: 228).
 #include <cuda_fp8.h>
 
 #include <cmath>

@@ -470,7 +470,8 @@ MOE_API int moe_residual_norm_backward(const uint16_t* dy, const void* s, int s_
  *   plan       uses cu_seqlens, tokens_per_expert and status.  A group that
  *              leaves [0, rows) sets MOE_ERR_DEVICE_INDEX and is not touched
  *              (the other outputs are then unspecified); with an error in
- *              the status before the call nothing is written.
+ *              the status before the call nothing is written.  A wait inside
+ *              the kernels that runs out (1 s) sets MOE_ERR_DEVICE_TIMEOUT.
  *   h          (device) bf16[rows][I] out (the groups' rows), also the
  *              call's workspace.
  *   preact     (device) float32[rows][2][I] out, or NULL: g and u for the
@@ -478,7 +479,7 @@ MOE_API int moe_residual_norm_backward(const uint16_t* dy, const void* s, int s_
  *              rounded once).  bf16 only.
  *   y          (device) bf16[rows][H] out; must not alias x.
  * H % 8 == 0 (H % 16 == 0 with e4m3), I % 8 == 0, H and I < 2^20, 1 <= E <= 1024;
- * 16-byte aligned arrays.  rows = 0 launches nothing.
+ * 16-byte aligned arrays.  Two launches; rows = 0 launches nothing.
  */
 MOE_API int moe_expert_ffn(const void* x, const float* x_scale, const void* w_gate_up, const float* w_scale,
                            const uint16_t* w_down, int64_t rows, int E, int H, int I, int x_dtype,
@@ -499,8 +500,8 @@ MOE_API int moe_expert_ffn(const void* x, const float* x_scale, const void* w_ga
  *   dx          (device) bf16[rows][H] out, or NULL if not wanted.
  *   dw_gate_up  (device) bf16[E][2][I][H] out, or NULL.
  *   dw_down     (device) bf16[E][H][I] out, or NULL.
- * Sizes, plan and errors as in the forward call.  rows = 0 zeroes the
- * weights' gradients.
+ * Sizes, plan and errors as in the forward call.  Two launches; rows = 0
+ * zeroes the weights' gradients.
  */
 MOE_API int moe_expert_ffn_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* h,
                                     const float* preact, const uint16_t* w_gate_up, const uint16_t* w_down,
