@@ -534,7 +534,8 @@ __device__ __forceinline__ void store4_bf16(uint16_t* p, float a, float b, float
     *reinterpret_cast<uint2*>(p) = make_uint2(pack2(a, b), pack2(c, d));
 }
 
-// dgate: the pre-activations that a lane needs for a chunk.
+// dgate: the pre-activations that a lane needs for a chunk.  Gated in 8 bits:
+// the scales of its four channels (g[0], u[0]).
 struct Saved {
     float4 g[kChunk / 4], u[kChunk / 4];
 };
@@ -557,7 +558,7 @@ __device__ __forceinline__ void load_saved(Saved& s, const Job& job, const Commo
 // turned through `turn` [16][32] so that neighbouring lanes hold neighbouring
 // channels.  Odd rows have their halves swapped: the gated product reads two
 // rows' same half at a time.
-template <int P>
+template <int P, bool FP8>
 __device__ __forceinline__ void epilogue_chunk(const Job& job, const Common& a, const Tile& t, int rank, uint32_t acc,
                                                int c0, int quarter, int lane, float* turn, const Saved& saved) {
     const int64_t M = job.M;
@@ -581,10 +582,9 @@ __device__ __forceinline__ void epilogue_chunk(const Job& job, const Common& a, 
             const int64_t row = t.first + static_cast<int64_t>(t.n0 + n);
             float4 g = *turned(j, (lane & 3) * 4);
             float4 u = *turned(j, 16 + (lane & 3) * 4);
-            if (a.a_scale != nullptr) {
+            if constexpr (FP8) {
                 const float s = __ldg(a.a_scale + row);
-                const float4 sg = __ldg(reinterpret_cast<const float4*>(a.b_scale + 2 * M * t.e + c));
-                const float4 su = __ldg(reinterpret_cast<const float4*>(a.b_scale + 2 * M * t.e + M + c));
+                const float4 sg = saved.g[0], su = saved.u[0];
                 g = make_float4(g.x * (s * sg.x), g.y * (s * sg.y), g.z * (s * sg.z), g.w * (s * sg.w));
                 u = make_float4(u.x * (s * su.x), u.y * (s * su.y), u.z * (s * su.z), u.w * (s * su.w));
             }
@@ -675,6 +675,14 @@ struct Drain {
             const Tile t = tiles.at(g, turn.next, lane);
             Saved now, next;  // dgate: asked for before the products are done, and a chunk ahead
             if constexpr (P == kDgate) load_saved(now, job, c, t, rank, half * kChunk, quarter, lane);
+            if constexpr (P == kGated && FP8) {
+                const int channel = t.m0 + rank * 64 + quarter * 16 + (lane & 3) * 4;
+                if (channel < job.M) {
+                    const float* scale = c.b_scale + 2 * static_cast<int64_t>(job.M) * t.e + channel;
+                    now.g[0] = __ldg(reinterpret_cast<const float4*>(scale));
+                    now.u[0] = __ldg(reinterpret_cast<const float4*>(scale + job.M));
+                }
+            }
             if (t.slices > 0) {
                 ok = __all_sync(FULL_MASK, wait(c, &sh->acc_full[buf], acc_phase));
                 if (!ok) break;
@@ -686,7 +694,7 @@ struct Drain {
             } else {
                 for (int n = half * kChunk; n < t.n; n += 2 * kChunk) {
                     if constexpr (P == kDgate) load_saved(next, job, c, t, rank, n + 2 * kChunk, quarter, lane);
-                    epilogue_chunk<P>(job, c, t, rank, acc, n, quarter, lane, reinterpret_cast<float*>(turn_buf), now);
+                    epilogue_chunk<P, FP8>(job, c, t, rank, acc, n, quarter, lane, reinterpret_cast<float*>(turn_buf), now);
                     if constexpr (P == kDgate) now = next;
                 }
             }
