@@ -244,3 +244,79 @@ def test_guard_zones(m):
     torch.cuda.synchronize()
     for raw, t in (y, h, pre, ws, dx):
         assert (raw[:128] == 3).all() and (raw[128 + t.numel():] == 3).all()
+
+
+def step(m, case, bufs=None):
+    """A forward and backward pass; its outputs."""
+    p, x, wgu, wd, dy = case
+    M, H, I = x.shape[0], x.shape[1], wd.shape[2]  # noqa: E741
+    h = torch.empty(M, I, dtype=BF16, device="cuda")
+    pre = torch.empty(M, 2, I, device="cuda")
+    y = m.expert_ffn(x, wgu, wd, p, h=h, preact=pre, out=torch.zeros_like(x))
+    return (y, *m.expert_ffn_backward(dy, x, h, pre, wgu, wd, p, dx=torch.zeros_like(x)))
+
+
+def cases():
+    out = []
+    for i, (counts, align, H, I) in enumerate([([300, 2, 0, 77, 256, 900], 8, 520, 264), ([64] * 40, 16, 256, 512)]):  # noqa: E741
+        p, x, wgu, wd = make(counts, align, H, I, seed=10 + i)
+        out.append((p, x, wgu, wd, torch.randn(p.rows, H, device="cuda").to(BF16)))
+    return out
+
+
+def test_two_streams_at_once(m):
+    """Steps of different sizes on two streams, overlapping: the bits of the steps alone."""
+    cs = cases()
+    want = [step(m, c) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(10):
+        got = []
+        for c, st in zip(cs, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                got.append(step(m, c))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+    assert all(int(c[0].status[0]) == 0 for c in cs)
+
+
+def test_training_step_in_a_graph(m):
+    """Forward and backward captured and replayed, four kernels that start before their predecessors end."""
+    c = cases()[0]
+    want = step(m, c)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step(m, c)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(m, c)
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_without_programmatic_launches(m, tmp_path):
+    """MOE_PDL=0, every kernel in plain stream order: the same bits."""
+    import os
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+    code = ("import sys; sys.path[:0] = [%r, %r]\n"
+            "import torch, test_gpu_expert_ffn as t, expert_dispatch_planning_gb300 as m\n"
+            "torch.manual_seed(0)\n"
+            "torch.save([[v.cpu() for v in t.step(m, c)] for c in t.cases()], sys.argv[1])\n"
+            % (ROOT, os.path.join(ROOT, "tests")))
+    runs = []
+    for pdl in ("1", "0"):
+        path = str(tmp_path / ("out%s.pt" % pdl))
+        res = subprocess.run([sys.executable, "-c", code, path], env=dict(os.environ, MOE_PDL=pdl), capture_output=True,
+                             text=True, timeout=300)
+        assert res.returncode == 0, res.stderr[-2000:]
+        runs.append(torch.load(path))
+    assert all(torch.equal(a, b) for s, t in zip(*runs) for a, b in zip(s, t))
