@@ -109,6 +109,7 @@ struct Shared {
     uint32_t ready;         // slices that the instructions may use, counted from the launch's start
     uint32_t tmem;
     int stop;               // the plan's status held an error
+    int failed;             // a wait of this block ran out
     int scan[kMendWarp + 1], most[kMendWarp + 1];
 };
 
@@ -749,6 +750,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         }
         fence_mbar_init();
         sh->ready = 0;
+        sh->failed = 0;
     }
     __syncwarp();
     if (warp == 1) tmem_alloc(&sh->tmem, 512);
@@ -837,14 +839,12 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         } else {
             r.run<P, FP8>(a.job[0], c, g, sh, ring, rank, lane);
         }
-        if (!r.ok) {  // time for the copies in flight to land before the block's shared memory goes
-            const uint64_t t0 = globaltimer_ns();
-            while (globaltimer_ns() - t0 < 20000000u) __nanosleep(1000);
-        }
+        if (!r.ok) sh->failed = 1;
     } else if (run && warp == 1 && rank == 0) {
         if (lane == 0) {
             Issuer r;
             r.run<P, FP8>(c, sh, ring, tmem);
+            if (!r.ok) sh->failed = 1;
         }
     } else if (run && warp == kWatchWarp && rank == 0) {
         Watcher r;
@@ -857,6 +857,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
             r.run<P, FP8>(a.job[0], c, g, sh, ring.stages, lane);
         }
         r.end(sh, lane);
+        if (!r.ok) sh->failed = 1;
     } else if (run && warp >= 2 && warp < kWatchWarp) {
         Drain r;
         r.turn = turn;
@@ -870,6 +871,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         } else {
             r.run<P, FP8>(a.job[0], c, g, sh, tmem, rank, warp, lane, turn_buf);
         }
+        if (!r.ok) sh->failed = 1;
     } else if (P == kGrads && run && warp == kMendWarp) {
         if constexpr (P == kGrads) {
             Mender r;
@@ -877,11 +879,17 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
             if (a.job[0].M > 0) r.run<kDx>(a.job[0], c, g, sh, ring, lane);
             if (a.job[1].M > 0) r.run<kDw>(a.job[1], c, g, sh, ring, lane);
             if (a.job[2].M > 0) r.run<kDw>(a.job[2], c, g, sh, ring, lane);
+            if (!r.ok) sh->failed = 1;
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (sh->failed) {  // time for the copies and instructions on their way to end before the block goes
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 20000000u) __nanosleep(1000);
+        __syncthreads();
+    }
     pair_arrive();
     pair_wait();  // neither block leaves while the other may still use its barriers or tensor memory
     if (warp == 1) {

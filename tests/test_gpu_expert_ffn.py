@@ -320,3 +320,25 @@ def test_without_programmatic_launches(m, tmp_path):
         assert res.returncode == 0, res.stderr[-2000:]
         runs.append(torch.load(path))
     assert all(torch.equal(a, b) for s, t in zip(*runs) for a, b in zip(s, t))
+
+
+def test_wait_that_runs_out(m):
+    """With a limit far below what a long product takes, the kernel gives up, says so and leaves the GPU usable."""
+    p, x, wgu, wd = make([40_000, 50], 16, 256, 256)
+    dy = torch.randn(x.shape, device="cuda").to(BF16)
+    want = step(m, (p, x, wgu, wd, dy))
+    torch.cuda.synchronize()
+    assert int(p.status[0]) == 0
+    try:
+        m.set_plan_fault(-1, 1000)          # 1 us a wait; a tile of dw here takes hundreds
+        step(m, (p, x, wgu, wd, dy))
+        torch.cuda.synchronize()
+        assert int(p.status[0]) == 5        # MOE_ERR_DEVICE_TIMEOUT
+    finally:
+        m.set_plan_fault()
+    out = torch.full_like(x, 7.0)
+    m.expert_ffn(x, wgu, wd, p, out=out)    # the error stands: nothing is written
+    assert (out == 7).all()
+    p.status.zero_()
+    got = step(m, (p, x, wgu, wd, dy))
+    assert int(p.status[0]) == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
