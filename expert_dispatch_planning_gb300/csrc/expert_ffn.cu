@@ -73,8 +73,8 @@ __host__ __device__ constexpr int ffn_turn(int p) { return p == kGrads ? 4096 : 
 __host__ __device__ constexpr int ffn_jobs(int p) { return p == kGrads ? 3 : 1; }
 
 struct Job {
-    CUtensorMap map_m, map_n;
-    CUtensorMap map_n32, map_n16;  // the N side by 32 and by 16 rows
+    CUtensorMap map_m;
+    CUtensorMap map_n[5];   // the N side by 16, 32, 64, 96 and 128 rows (dw: [0], by columns)
     CUtensorMap map_out;    // dw: the output
     int M, N, K;            // M: output channels; K: contraction length; dw: output M x N; M = 0: no work
     int m_whole, n_whole;   // a block's part of a slice is one copy (see make_job)
@@ -240,8 +240,9 @@ struct Producer {
     int ahead = 0;           // slices of the first tile whose M side is on its way already
     bool ok = true;
 
-    // The N side of a block's part of a tile: rows (dw: columns), and the copies
-    // for them: of 128 rows, or of 32 or 16 (dw: of 128 columns, or of 64).
+    // The N side of a block's part of a tile: its rows, brought by one copy of
+    // 16 or a multiple of 32 of them (dw: columns, by one copy of 128 or by
+    // copies of 64).
     struct NSide {
         int rows, piece, pieces;
         uint32_t bytes;      // of a block's part of a slice, both sides
@@ -250,8 +251,8 @@ struct Producer {
     __device__ __forceinline__ NSide n_side(const Job& job, const Tile& t) const {
         NSide n;
         n.rows = ((t.n + 15) & ~15) / 2;
-        n.piece = P == kDw ? (job.n_whole ? 128 : 64) : n.rows > 64 ? 128 : n.rows > 16 ? 32 : 16;
-        n.pieces = (n.rows + n.piece - 1) / n.piece;
+        n.piece = P == kDw ? (job.n_whole ? 128 : 64) : n.rows > 16 ? (n.rows + 31) & ~31 : 16;
+        n.pieces = P == kDw ? (n.rows + n.piece - 1) / n.piece : 1;
         n.bytes = static_cast<uint32_t>(kHalf + n.pieces * n.piece) * kSlice;
         return n;
     }
@@ -271,7 +272,7 @@ struct Producer {
         f.e = t.e;
         f.first = t.first;
         f.n = (P == kDw ? t.n0 : t.first + t.n0) + rank * f.side.rows;
-        f.map_n = P == kDw || f.side.piece == 128 ? &job.map_n : f.side.piece == 32 ? &job.map_n32 : &job.map_n16;
+        f.map_n = &job.map_n[P == kDw ? 0 : f.side.piece / 32];
         return f;
     }
     // A block's part of the slice that starts at k.
@@ -301,8 +302,6 @@ struct Producer {
                 for (int j = 0; j < f.side.pieces; ++j) tensor_load_2d(to + j * 8192, f.map_n, f.n + 64 * j, f.first + k, bar);
         } else {
             tensor_load_2d(to, f.map_n, k, f.n, bar);
-            for (int j = 1; j < f.side.pieces; ++j)
-                tensor_load_2d(to + j * f.side.piece * kSlice, f.map_n, k, f.n + f.side.piece * j, bar);
         }
     }
 
@@ -737,7 +736,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     const int rank = static_cast<int>(pair_rank());
     if (tid == 0) {
         tensor_prefetch(&a.job[0].map_m);
-        tensor_prefetch(&a.job[0].map_n);
+        tensor_prefetch(&a.job[0].map_n[4]);
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sh->full[i], 1);
             mbar_init(&sh->empty[i], 1);
@@ -806,7 +805,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     const Groups g = {first, count, padded, prefix, E};
     // short groups leave room for more stages: the N side's part is as long as the longest tile's half
     const int half = (min(longest, kTile) + 15) / 16 * 8;
-    const int n_rows = P == kGrads || half > 64 ? kHalf : half > 16 ? (half + 31) / 32 * 32 : 16;
+    const int n_rows = P == kGrads ? kHalf : half > 16 ? (half + 31) / 32 * 32 : 16;
     RingShape ring;
     ring.at = base;
     ring.stage_bytes = static_cast<uint32_t>(kHalf + n_rows) * kSlice;
@@ -962,14 +961,14 @@ int make_job(moe::Job* j, const void* weights, const void* row_data, int64_t row
     if constexpr (P == moe::kDw) {
         j->n_whole = N % 128 == 0;  // and a block's half of the last tile starts at a run
         if (j->n_whole)
-            rc = moe_host::make_tensor_map(&j->map_n, row_data, 2, {{run, 1, run}, {rows, n, 64}, {n / run, run, 2}});
+            rc = moe_host::make_tensor_map(&j->map_n[0], row_data, 2, {{run, 1, run}, {rows, n, 64}, {n / run, run, 2}});
         else
-            rc = moe_host::make_tensor_map(&j->map_n, row_data, 2, {{n, 1, run}, {rows, n, 64}});
+            rc = moe_host::make_tensor_map(&j->map_n[0], row_data, 2, {{n, 1, run}, {rows, n, 64}});
         return rc != MOE_OK ? rc : moe_host::make_tensor_map(&j->map_out, out, 2, {{n, 1, run}, {m, n, 32}, {E, m * n, 1}});
     } else {
-        rc = moe_host::make_tensor_map(&j->map_n, row_data, bytes, {{k, 1, box_k}, {rows, k, moe::kHalf}});
-        if (rc == MOE_OK) rc = moe_host::make_tensor_map(&j->map_n32, row_data, bytes, {{k, 1, box_k}, {rows, k, 32}});
-        return rc != MOE_OK ? rc : moe_host::make_tensor_map(&j->map_n16, row_data, bytes, {{k, 1, box_k}, {rows, k, 16}});
+        for (int i = 0; i < 5 && rc == MOE_OK; ++i)
+            rc = moe_host::make_tensor_map(&j->map_n[i], row_data, bytes, {{k, 1, box_k}, {rows, k, i == 0 ? 16 : 32 * i}});
+        return rc;
     }
 }
 
