@@ -12,6 +12,7 @@
 // Memory bound: every element is read once and written once.  Three forms:
 //   - H <= 512: a warp a row, four rows a block;
 //   - few rows, or very wide ones: a block a row, 8, 16 or 32 elements a thread;
+//     (past 8192 columns the gradient spills registers: right, but not tuned);
 //   - else a ring: blocks that stay, each thread copying its own columns of the
 //     next rows into its own places in shared memory (cp.async) while the block
 //     works on a row, so that the row's reductions never empty the memory
