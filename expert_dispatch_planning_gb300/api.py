@@ -328,6 +328,9 @@ def combine(y: torch.Tensor, topk_w: torch.Tensor, p: Plan, out: torch.Tensor | 
 
 
 # ---------------------------------------------------------------- around the experts
+# With stream= a call launches there and takes what it allocates (outputs not
+# given, workspaces) from that stream's memory; the arguments have to be ready
+# on it and live until it has passed the call.
 def _handle(stream):
     return None if stream is None else stream.cuda_stream
 

@@ -11,6 +11,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -117,12 +118,36 @@ int dtype_of(const Tensor& t) {
     return t.scalar_type() == kF32 ? MOE_DTYPE_F32 : t.scalar_type() == kE4m3 ? MOE_DTYPE_E4M3 : MOE_DTYPE_BF16;
 }
 
-cudaStream_t stream_of(PyObject* o) {  // an integer handle, or None for the current stream
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-    void* p = PyLong_AsVoidPtr(o);
-    if (p == nullptr && PyErr_Occurred()) throw BadArgument();
-    return static_cast<cudaStream_t>(p);
-}
+// The stream that a call launches on: an integer handle, or None for the
+// current one.  While it lives, the handle's stream is the current one, so that
+// what the call allocates comes from the memory of the stream that uses it: a
+// workspace that is released as the call returns can only go to later work of
+// that stream, and no earlier work of another stream still writes to it.
+class OnStream {
+public:
+    explicit OnStream(PyObject* o) : current_(c10::cuda::getCurrentCUDAStream()), handle_(current_.stream()) {
+        if (o == Py_None) return;
+        void* p = PyLong_AsVoidPtr(o);
+        if (p == nullptr && PyErr_Occurred()) throw BadArgument();
+        handle_ = static_cast<cudaStream_t>(p);
+        if (handle_ == current_.stream()) return;
+        const c10::DeviceIndex device = current_.device_index();
+        guard_.reset_stream(p == nullptr ? c10::cuda::getDefaultCUDAStream(device)
+                                         : c10::cuda::getStreamFromExternal(handle_, device));
+        other_ = true;
+    }
+    cudaStream_t handle() const { return handle_; }
+    // An output that the call allocated: the caller's current stream goes on to use it.
+    void hand_over(const Tensor& out, PyObject* given) const {
+        if (other_ && given == Py_None && out.defined()) out.record_stream(current_.unwrap());
+    }
+
+private:
+    c10::cuda::CUDAStream current_;
+    cudaStream_t handle_;
+    c10::cuda::OptionalCUDAStreamGuard guard_;
+    bool other_ = false;
+};
 
 int as_int(int64_t n, const char* name) {
     if (n > INT32_MAX) refuse(std::string(name) + " is too large");
@@ -169,6 +194,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const double eps = PyFloat_AsDouble(a[3]);
         if (eps == -1.0 && PyErr_Occurred()) return nullptr;
         const bool quantize = a[4] == Py_True;
+        const OnStream stream(a[9]);
         Tensor residual_out = tensor(a[6], "residual_out"), q = tensor(a[7], "q"), q_scale = tensor(a[8], "q_scale");
         need_dims(x, 2, "x");
         const int64_t N = x.size(0), H = x.size(1);
@@ -192,7 +218,12 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int rc = moe_residual_norm(ptr<uint16_t>(x), ptr<>(residual), residual.defined() ? dtype_of(residual) : 0,
                                          ptr<>(weight), dtype_of(weight), as_int(N, "N"), as_int(H, "H"),
                                          static_cast<float>(eps), ptr<uint16_t>(y), ptr<>(residual_out), ptr<float>(rstd),
-                                         ptr<uint8_t>(q), ptr<float>(q_scale), stream_of(a[9]));
+                                         ptr<uint8_t>(q), ptr<float>(q_scale), stream.handle());
+        stream.hand_over(y, a[5]);
+        stream.hand_over(residual_out, a[6]);
+        stream.hand_over(rstd, Py_None);
+        stream.hand_over(q, a[7]);
+        stream.hand_over(q_scale, a[8]);
         return rc != MOE_OK ? PyLong_FromLong(rc) : wrap({y, residual_out, rstd, q, q_scale});
     } catch (const BadArgument&) {
         return nullptr;
@@ -207,6 +238,7 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
         const Tensor dy = tensor(a[0], "dy"), s = tensor(a[1], "s"), weight = tensor(a[2], "weight"),
                      rstd = tensor(a[3], "rstd"), ds = tensor(a[4], "ds");
+        const OnStream stream(a[5]);
         need_dims(dy, 2, "dy");
         const int64_t N = dy.size(0), H = dy.size(1);
         need(dy, kBf16, {N, H}, "dy");
@@ -225,7 +257,8 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                                   dtype_of(weight), ptr<float>(rstd), ptr<>(ds), static_cast<int>(N),
                                                   static_cast<int>(H), ptr<uint16_t>(dx), ptr<float>(dres),
                                                   ptr<float>(dweight), ptr<>(ws), static_cast<size_t>(bytes),
-                                                  stream_of(a[5]));
+                                                  stream.handle());
+        for (const Tensor& t : {dx, dres, dweight}) stream.hand_over(t, Py_None);
         return rc != MOE_OK ? PyLong_FromLong(rc) : wrap({dx, dres, dweight});
     } catch (const BadArgument&) {
         return nullptr;
@@ -240,6 +273,7 @@ PyObject* expert_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
         const Tensor x = tensor(a[0], "x"), wgu = tensor(a[1], "w_gate_up"), wd = tensor(a[2], "w_down"),
                      x_scale = tensor(a[6], "x_scale"), w_scale = tensor(a[7], "w_scale"), preact = tensor(a[9], "preact");
+        const OnStream stream(a[11]);
         need_dims(x, 2, "x");
         need_dims(wgu, 4, "w_gate_up");
         const int64_t rows = x.size(0), H = x.size(1), E = wgu.size(0), I = wgu.size(2);
@@ -263,7 +297,8 @@ PyObject* expert_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor y = output(tensor(a[10], "out"), {rows, H}, kBf16, x, "out");
         const int rc = moe_expert_ffn(ptr<>(x), ptr<float>(x_scale), ptr<>(wgu), ptr<float>(w_scale), ptr<uint16_t>(wd),
                                       rows, as_int(E, "E"), as_int(H, "H"), as_int(I, "I"), dtype_of(x), &plan,
-                                      ptr<uint16_t>(h), ptr<float>(preact), ptr<uint16_t>(y), stream_of(a[11]));
+                                      ptr<uint16_t>(h), ptr<float>(preact), ptr<uint16_t>(y), stream.handle());
+        stream.hand_over(y, a[10]);
         return rc != MOE_OK ? PyLong_FromLong(rc) : wrap(y);
     } catch (const BadArgument&) {
         return nullptr;
@@ -281,6 +316,7 @@ PyObject* expert_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      wgu = tensor(a[4], "w_gate_up"), wd = tensor(a[5], "w_down");
         Tensor dx = tensor(a[9], "dx");
         const bool need_dx = a[11] == Py_True, need_dw = a[12] == Py_True;
+        const OnStream stream(a[13]);
         need_dims(x, 2, "x");
         need_dims(wgu, 4, "w_gate_up");
         const int64_t rows = x.size(0), H = x.size(1), E = wgu.size(0), I = wgu.size(2);
@@ -300,7 +336,9 @@ PyObject* expert_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int rc = moe_expert_ffn_backward(
             ptr<uint16_t>(dy), ptr<uint16_t>(x), ptr<uint16_t>(h), ptr<float>(preact), ptr<uint16_t>(wgu),
             ptr<uint16_t>(wd), rows, as_int(E, "E"), as_int(H, "H"), as_int(I, "I"), &plan, ptr<uint16_t>(dgu),
-            ptr<uint16_t>(dx), ptr<uint16_t>(dwgu), ptr<uint16_t>(dwd), stream_of(a[13]));
+            ptr<uint16_t>(dx), ptr<uint16_t>(dwgu), ptr<uint16_t>(dwd), stream.handle());
+        stream.hand_over(dx, a[9]);
+        for (const Tensor& t : {dwgu, dwd}) stream.hand_over(t, Py_None);
         return rc != MOE_OK ? PyLong_FromLong(rc) : wrap({dx, dwgu, dwd});
     } catch (const BadArgument&) {
         return nullptr;
@@ -315,6 +353,7 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
         const Tensor dout = tensor(a[0], "dout"), y = tensor(a[1], "y"), w = tensor(a[2], "topk_w"),
                      dst = tensor(a[3], "dst"), zfr = tensor(a[4], "zero_fill_ranges"), status = tensor(a[5], "status");
+        const OnStream stream(a[8]);
         need_dims(dout, 2, "dout");
         need_dims(y, 2, "y");
         need_dims(dst, 2, "dst");
@@ -334,7 +373,9 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         plan.status = ptr<int32_t>(status);
         const int rc = moe_combine_backward(ptr<uint16_t>(dout), ptr<uint16_t>(y), ptr<float>(w), as_int(N, "N"),
                                             as_int(K, "K"), as_int(H, "H"), as_int(E, "E"), rows, &plan, ptr<uint16_t>(dy),
-                                            ptr<float>(dw), stream_of(a[8]));
+                                            ptr<float>(dw), stream.handle());
+        stream.hand_over(dy, a[6]);
+        stream.hand_over(dw, a[7]);
         return rc != MOE_OK ? PyLong_FromLong(rc) : wrap({dy, dw});
     } catch (const BadArgument&) {
         return nullptr;
