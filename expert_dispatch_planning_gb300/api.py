@@ -5,6 +5,7 @@ routing / planning / row-movement path runs in the library's own kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass, field
 
@@ -279,8 +280,9 @@ def rank_layout_workspace(N: int, R: int, device="cuda") -> torch.Tensor:
 def rank_layout(p: Plan, num_channels: int, workspace: torch.Tensor | None = None, out=None, stream=None):
     """(channel_prefix_matrix[R, C], token_rank_slot[N, R]) of a plan."""
     dev = p.dst.device
-    if workspace is None:
-        workspace = rank_layout_workspace(p.N, p.R, device=dev)
+    if workspace is None:  # from the memory of the stream that uses it: it is released as the call returns
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = rank_layout_workspace(p.N, p.R, device=dev)
     if out is None:
         out = (torch.empty((p.R, num_channels), dtype=torch.int32, device=dev),
                torch.empty((p.N, p.R), dtype=torch.int32, device=dev))
