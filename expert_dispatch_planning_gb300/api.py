@@ -32,6 +32,11 @@ def _stream(stream=None) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _on(stream):
+    """Allocations and fills of a call that runs on `stream` (None: the current one) belong to that stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -103,21 +108,27 @@ class Plan:
         if cap < 0 or ws == 0:
             raise ValueError("unsupported plan sizes N=%d E=%d K=%d R=%d alignment=%d" % (N, E, K, R, alignment))
         i32 = dict(dtype=torch.int32, device=device)
-        p = cls(N=N, E=E, K=K, R=R, alignment=alignment,
-                tokens_per_expert=torch.empty(E, **i32), cu_seqlens=torch.empty(E + 1, **i32),
-                zero_fill_ranges=torch.empty((E, 2), **i32), pairs_per_rank=torch.empty(R, **i32),
-                tokens_per_rank=torch.empty(R, **i32), rank_prefix=torch.empty(R + 1, **i32),
-                rank_slot_offsets=torch.empty(R + 1, **i32),
-                is_token_in_rank=torch.empty((N, R), dtype=torch.uint8, device=device),
-                dst=torch.empty((N, K), **i32), src_of_slot=torch.empty(cap, **i32),
-                dup_groups=torch.empty((max(1, N * (K // 2)), 3), **i32),
-                dup_loffs=torch.empty(max(1, N * (K - 1)), **i32), dup_counts=torch.empty(2, **i32),
-                status=torch.zeros(4, **i32), workspace=torch.empty(ws, dtype=torch.uint8, device=device))
+        with _on(stream):  # the status is zeroed there, before the plan
+            p = cls(N=N, E=E, K=K, R=R, alignment=alignment,
+                    tokens_per_expert=torch.empty(E, **i32), cu_seqlens=torch.empty(E + 1, **i32),
+                    zero_fill_ranges=torch.empty((E, 2), **i32), pairs_per_rank=torch.empty(R, **i32),
+                    tokens_per_rank=torch.empty(R, **i32), rank_prefix=torch.empty(R + 1, **i32),
+                    rank_slot_offsets=torch.empty(R + 1, **i32),
+                    is_token_in_rank=torch.empty((N, R), dtype=torch.uint8, device=device),
+                    dst=torch.empty((N, K), **i32), src_of_slot=torch.empty(cap, **i32),
+                    dup_groups=torch.empty((max(1, N * (K // 2)), 3), **i32),
+                    dup_loffs=torch.empty(max(1, N * (K - 1)), **i32), dup_counts=torch.empty(2, **i32),
+                    status=torch.zeros(4, **i32), workspace=torch.empty(ws, dtype=torch.uint8, device=device))
         check("moe_plan_workspace_init", lib.moe_plan_workspace_init(_ptr(p.workspace), ws, _stream(stream)))
         p.c_struct = MoePlanOut(*[t.data_ptr() for t in (
             p.tokens_per_expert, p.cu_seqlens, p.zero_fill_ranges, p.pairs_per_rank, p.tokens_per_rank,
             p.rank_prefix, p.rank_slot_offsets, p.is_token_in_rank, p.dst, p.src_of_slot, p.dup_groups,
             p.dup_loffs, p.dup_counts, p.status)])
+        if stream is not None:  # the caller's current stream may go on to use them
+            current = torch.cuda.current_stream()
+            for t in vars(p).values():
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(current)
         return p
 
     def clone(self, stream=None) -> "Plan":
@@ -281,7 +292,7 @@ def rank_layout(p: Plan, num_channels: int, workspace: torch.Tensor | None = Non
     """(channel_prefix_matrix[R, C], token_rank_slot[N, R]) of a plan."""
     dev = p.dst.device
     if workspace is None:  # from the memory of the stream that uses it: it is released as the call returns
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with _on(stream):
             workspace = rank_layout_workspace(p.N, p.R, device=dev)
     if out is None:
         out = (torch.empty((p.R, num_channels), dtype=torch.int32, device=dev),

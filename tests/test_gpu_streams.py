@@ -38,3 +38,24 @@ def test_rank_layout_workspace_outlives_the_call(m):
         assert all((t == 0x5a).all() for t in others)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         del got, others
+
+
+def test_plan_status_is_ready_on_the_calls_stream(m):
+    """The plan's status is zeroed on the stream that plans, not behind the current stream's work."""
+    idx = choice(300, 16, 2)
+    want = m.plan(idx, 16, 4, 8)
+    st = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        dirty = [torch.full((4,), 6, dtype=torch.int32, device="cuda") for _ in range(64)]
+        torch.cuda.synchronize()
+        del dirty
+        torch.cuda._sleep(SLEEP)
+        p = m.plan(idx, 16, 4, 8, stream=st)
+        st.synchronize()
+        with torch.cuda.stream(st):
+            got = [t.cpu() for t in (p.status, p.cu_seqlens, p.dst)]
+        assert not got[0].any()
+        assert torch.equal(got[1], want.cu_seqlens.cpu()) and torch.equal(got[2], want.dst.cpu())
+        torch.cuda.synchronize()
+        assert m.get_status(p) == 0
