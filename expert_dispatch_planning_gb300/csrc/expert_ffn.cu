@@ -108,7 +108,7 @@ struct Shared {
     uint4 order[kOrders];   // the tiles' instructions: descriptor, slices (0: the end), steps of the last, dw
     uint32_t ready;         // slices that the instructions may use, counted from the launch's start
     uint32_t tmem;
-    int stop;               // the plan's status held an error
+    int stop;               // the plan's status held an error (the pair's first block's counts)
     int failed;             // a wait of this block ran out
     int scan[kMendWarp + 1], most[kMendWarp + 1];
 };
@@ -753,9 +753,6 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     }
     __syncwarp();
     if (warp == 1) tmem_alloc(&sh->tmem, 512);
-    tc_fence_before();
-    __syncwarp();
-    pair_arrive();  // this warp's part of the block is set up; the wait comes after the groups' scan
     // A call's later kernels start while the one before still runs: the groups
     // and the weights were there before that one began, and only the warps that
     // touch the rows wait for it.
@@ -763,7 +760,13 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         pdl_wait();
         pdl_trigger();
     }
+    // The pair's first block decides for both whether there is an error already:
+    // other blocks may record one between two reads, and a block that worked
+    // alone would wait out its limit.
     if (tid == 0) sh->stop = ld_volatile_s32(c.status) != 0;
+    tc_fence_before();
+    __syncwarp();
+    pair_arrive();  // this warp's part of the block is set up; the wait comes after the groups' scan
 
     // ---- the groups: row tiles before each expert
     const int per = (E + kThreads - 1) / kThreads;
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     pair_wait();  // both blocks' barriers and tensor memory are ready
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    const bool run = sh->stop == 0;
+    const bool run = leader_value(&sh->stop) == 0;
     if (!run && c.early) pdl_wait();
 
     if (run && warp == 0) {
