@@ -36,7 +36,9 @@ __global__ void __launch_bounds__(32 * kWarps, 3) combine_grad_kernel(const Comb
     __shared__ float sums[kWarps][kMaxK];
     pdl_wait();
     pdl_trigger();
-    if (ld_volatile_s32(a.status) != 0) return;
+    // Decided by the block as a whole: another block may record an error between
+    // two warps' reads, and a token's warps meet at barriers below.
+    if (__syncthreads_or(ld_volatile_s32(a.status) != 0)) return;
     const int64_t H = a.H;
     const int nvec = a.H / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
