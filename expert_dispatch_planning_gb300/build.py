@@ -4,7 +4,8 @@ Each ``csrc/*.cu`` file is compiled to an object in parallel, then linked
 into one shared library with the CUDA runtime linked statically (so the
 library does not depend on which libcudart the process already loaded).
 ``csrc/torch_binding.cpp`` becomes ``_torch_binding.so``, a Python module that
-calls the library on tensors of the installed torch.
+calls the library on tensors of the installed torch; where there is no torch
+with CUDA the library is all that is built.
 """
 from __future__ import annotations
 
@@ -65,13 +66,20 @@ def _compile(src, extra, verbose):
     return obj
 
 
-def _compile_binding():
-    """The object of the torch binding (compiled against the installed torch)."""
-    import sysconfig
-
-    import torch
-    obj = os.path.join(BUILD_DIR, "torch_binding.o")
+def _torch_root():
+    """The installed torch's folder; None without one that has CUDA."""
+    try:
+        import torch
+    except ImportError:
+        return None
     root = os.path.dirname(torch.__file__)
+    return root if os.path.exists(os.path.join(root, "lib", "libtorch_cuda.so")) else None
+
+
+def _compile_binding(root):
+    """The object of the torch binding (compiled against the torch in `root`)."""
+    import sysconfig
+    obj = os.path.join(BUILD_DIR, "torch_binding.o")
     if not _stale(obj, [BINDING_SRC, __file__, os.path.join(root, "version.py")] + _headers()):
         return obj
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -86,11 +94,10 @@ def _compile_binding():
     return obj
 
 
-def _link_binding(obj):
-    import torch
+def _link_binding(obj, root):
     if not _stale(BINDING_PATH, [obj, LIB_PATH]):
         return
-    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    libs = os.path.join(root, "lib")
     tmp = BINDING_PATH + ".tmp%d" % os.getpid()
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:" + LIB_NAME, "-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu",
            "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
@@ -108,10 +115,10 @@ def build(verbose: bool = False, extra_flags=None, force: bool = False) -> str:
     if force:
         for f in os.listdir(BUILD_DIR):
             os.remove(os.path.join(BUILD_DIR, f))
+    root = _torch_root()
     with cf.ThreadPoolExecutor(max_workers=min(10, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding, root) if root else None
         objs = list(ex.map(lambda s: _compile(s, extra, verbose), srcs))
-        binding = binding.result()
     if _stale(LIB_PATH, objs) or extra or force:
         tmp = LIB_PATH + ".tmp%d" % os.getpid()
         cmd = [nvcc(), *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -119,7 +126,8 @@ def build(verbose: bool = False, extra_flags=None, force: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
         os.replace(tmp, LIB_PATH)
-    _link_binding(binding)
+    if binding is not None:  # after the library, which does not need it
+        _link_binding(binding.result(), root)
     return LIB_PATH
 
 
