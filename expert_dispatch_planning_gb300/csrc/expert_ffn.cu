@@ -215,8 +215,12 @@ struct Turn {
 };
 
 // Bounded wait; on a timeout the caller gives up and the plan's status says so.
-__device__ __forceinline__ bool wait(const Common& c, uint64_t* bar, uint32_t parity) {
-    if (mbar_wait_pair(bar, parity, static_cast<uint64_t>(c.timeout_ns))) return true;
+// The limit is for a slice's steps.  A wait that lasts for many slices, a whole
+// tile's or more, gets a 65536th of it for each (15 us of the usual second,
+// where a slice takes 0.3 to 0.8).
+__device__ __forceinline__ bool wait(const Common& c, uint64_t* bar, uint32_t parity, uint64_t slices = 0) {
+    const uint64_t limit = static_cast<uint64_t>(c.timeout_ns);
+    if (mbar_wait_pair(bar, parity, limit + (limit >> 16) * slices)) return true;
     record_error(c.status, MOE_ERR_DEVICE_TIMEOUT, blockIdx.x);
     return false;
 }
@@ -487,6 +491,7 @@ struct Mender {
     Turn turn;
     int s = 0;
     uint32_t tail_phase = 0;
+    uint64_t passed = 0;     // slices since the last one waited for
     bool ok = true;
 
     template <int P>
@@ -496,14 +501,17 @@ struct Mender {
         for (; ok && turn.next < tiles.total; turn.next += turn.pairs) {
             if (P != kDw) {  // only to know where in the ring the next job starts
                 s = (s + tiles.k_slices) % ring.stages;
+                passed += tiles.k_slices;
                 continue;
             }
             const Tile t = tiles.at(g, turn.next, lane);
             if (t.slices == 0) continue;
             s = (s + t.slices - 1) % ring.stages;
+            passed += t.slices;
             if ((t.count & 15) != 0) {
-                ok = __all_sync(FULL_MASK, wait(c, &sh->tail_full[s], (tail_phase >> s) & 1u));
+                ok = __all_sync(FULL_MASK, wait(c, &sh->tail_full[s], (tail_phase >> s) & 1u, passed));
                 if (!ok) break;
+                passed = 0;
                 tail_phase ^= 1u << s;
                 // rows from the group's end to a multiple of 16; the N side's boxes of
                 // 64 columns follow the M side's two in the stage
@@ -684,7 +692,7 @@ struct Drain {
                 }
             }
             if (t.slices > 0) {
-                ok = __all_sync(FULL_MASK, wait(c, &sh->acc_full[buf], acc_phase));
+                ok = __all_sync(FULL_MASK, wait(c, &sh->acc_full[buf], acc_phase, t.slices));
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -754,8 +762,8 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     __syncwarp();
     if (warp == 1) tmem_alloc(&sh->tmem, 512);
     // A call's later kernels start while the one before still runs: the groups
-    // and the weights were there before that one began, and only the warps that
-    // touch the rows wait for it.
+    // and the weights were there before that one began, and its warps wait for
+    // it only once the first weights are on their way.
     if (!c.early) {
         pdl_wait();
         pdl_trigger();
@@ -843,6 +851,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         }
         if (!r.ok) sh->failed = 1;
     } else if (run && warp == 1 && rank == 0) {
+        if (c.early) pdl_wait();  // a wait's limit does not run while the kernel ahead does
         if (lane == 0) {
             Issuer r;
             r.run<P, FP8>(c, sh, ring, tmem);
@@ -851,6 +860,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     } else if (run && warp == kWatchWarp && rank == 0) {
         Watcher r;
         r.turn = turn;
+        if (c.early) pdl_wait();
         if constexpr (P == kGrads) {
             if (a.job[0].M > 0) r.run<kDx, false>(a.job[0], c, g, sh, ring.stages, lane);
             if (a.job[1].M > 0) r.run<kDw, false>(a.job[1], c, g, sh, ring.stages, lane);
@@ -878,6 +888,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         if constexpr (P == kGrads) {
             Mender r;
             r.turn = turn;
+            if (c.early) pdl_wait();
             if (a.job[0].M > 0) r.run<kDx>(a.job[0], c, g, sh, ring, lane);
             if (a.job[1].M > 0) r.run<kDw>(a.job[1], c, g, sh, ring, lane);
             if (a.job[2].M > 0) r.run<kDw>(a.job[2], c, g, sh, ring, lane);

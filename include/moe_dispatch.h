@@ -471,7 +471,8 @@ MOE_API int moe_residual_norm_backward(const uint16_t* dy, const void* s, int s_
  *              leaves [0, rows) sets MOE_ERR_DEVICE_INDEX and is not touched
  *              (the other outputs are then unspecified); with an error in
  *              the status before the call nothing is written.  A wait inside
- *              the kernels that runs out (1 s) sets MOE_ERR_DEVICE_TIMEOUT.
+ *              the kernels that runs out (1 s, and 15 us more for every 64
+ *              rows of a group) sets MOE_ERR_DEVICE_TIMEOUT.
  *   h          (device) bf16[rows][I] out (the groups' rows), also the
  *              call's workspace.
  *   preact     (device) float32[rows][2][I] out, or NULL: g and u for the

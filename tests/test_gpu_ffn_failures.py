@@ -61,3 +61,26 @@ def test_a_group_outside_the_rows_is_reported_at_once(m, bad):
     p.status.zero_()
     got = step(m, p, *args)
     assert int(p.status[0]) == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_long_groups_are_not_taken_for_a_wait_that_ran_out(m):
+    """One group whose weights' gradients are a single tile of 625001 slices: some 0.1 s and more, during all of which
+    the output waits. With a limit of 60 ms a wait for one slice's steps has ages, and the tile's must not run out."""
+    rows, H, I = 40_000_005, 16, 16  # noqa: E741
+    p = bc.groups([rows], 1)
+    x = torch.ones(rows, H, dtype=BF16, device="cuda")
+    wgu, wd = torch.ones(1, 2, I, H, dtype=BF16, device="cuda"), torch.ones(1, H, I, dtype=BF16, device="cuda")
+    try:
+        m.set_plan_fault(-1, 60_000_000)
+        t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        h, pre = torch.empty(rows, I, dtype=BF16, device="cuda"), torch.empty(rows, 2, I, device="cuda")
+        m.expert_ffn(x, wgu, wd, p, h=h, preact=pre)
+        torch.cuda.synchronize()
+        t0.record()
+        m.expert_ffn_backward(x, x, h, pre, wgu, wd, p)
+        t1.record()
+        torch.cuda.synchronize()
+    finally:
+        m.set_plan_fault()
+    assert int(p.status[0]) == 0
+    assert t0.elapsed_time(t1) > 60          # the case is one that takes longer than the limit
