@@ -38,7 +38,9 @@ struct NormArgs {
     const void* weight;
     int weight_f32;
     int N, H;
-    float eps, mean;  // mean: 1/H
+    float eps;
+    float down, mean;  // a power of two near 1/sqrt(H), and 1/(H down^2): the squares are summed scaled down, so
+                       // that a row overflows only where a mean square does
     uint16_t* y;
     void* residual_out;
     float* rstd;
@@ -69,25 +71,6 @@ __device__ __forceinline__ float row_reduce(float v, float* buf) {
         }
     }
     return v;
-}
-
-// 1/sqrt(mean square + eps), within 2^-22, from the sum of squares.  Where that
-// sum has left fp32's range, or both it and eps are so small that squares have
-// lost digits below the normal numbers, the row is summed once more with its
-// values scaled by a power of two: top() is the row's largest magnitude,
-// scaled(f) the sum of the squares of f times the values.  A row's threads hold
-// the same ss and take the same way.
-template <typename Top, typename Scaled>
-__device__ __forceinline__ float row_rstd(float ss, float mean, float eps, Top top, Scaled scaled) {
-    const float ms = fmaf(ss, mean, eps);
-    if (ss <= 3e38f && ms >= 0x1p-100f) return rsqrtf(ms);
-    if (isnan(ss)) return ss;
-    const float t = top();
-    if (!(t > 0.f) || isinf(t)) return rsqrtf(ms);  // zeros, or an infinity
-    const int e = min(max(ilogbf(t), -126), 126);
-    const float f = __int_as_float((127 - e) << 23);  // 2^-e
-    const float scaled_eps = eps * f * f;
-    return isinf(scaled_eps) ? rsqrtf(eps) : f * rsqrtf(fmaf(scaled(f), mean, scaled_eps));
 }
 
 __device__ __forceinline__ void load_weight8(const void* w, int f32, int c, float (&f)[8]) {
@@ -148,29 +131,14 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_kernel(const Norm
                 for (int j = 0; j < 8; ++j) s[i][j] += r[j];
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(s[i][j], s[i][j], ss);
+            for (int j = 0; j < 8; ++j) {
+                const float t = s[i][j] * a.down;
+                ss = fmaf(t, t, ss);
+            }
         }
     }
     ss = row_reduce<WARP, false>(ss, buf);
-    auto over_row = [&](auto f) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            if (lane + i * lanes < nvec)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f(s[i][j]);
-    };
-    const float rstd = row_rstd(
-        ss, a.mean, a.eps,
-        [&] {
-            float top = 0.f;
-            over_row([&](float v) { top = fmaxf(top, fabsf(v)); });
-            return row_reduce<WARP, true>(top, buf);
-        },
-        [&](float f) {
-            float sum = 0.f;
-            over_row([&](float v) { sum = fmaf(v * f, v * f, sum); });
-            return row_reduce<WARP, false>(sum, buf);
-        });
+    const float rstd = rsqrtf(fmaf(ss, a.mean, a.eps));  // within 2^-22
     if (a.rstd != nullptr && lane == 0) a.rstd[row] = rstd;
 
     float amax = 0.f;
@@ -419,31 +387,14 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
                     if (a.residual_out != nullptr) store4(static_cast<R*>(a.residual_out) + at + h, s[i]);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) ss = fmaf(s[i][j], s[i][j], ss);
+                for (int j = 0; j < 4; ++j) {
+                    const float t = s[i][j] * a.down;
+                    ss = fmaf(t, t, ss);
+                }
             }
         }
         ss = block_reduce<false>(ss, sums[0]);
-        auto over_row = [&](auto f) {
-#pragma unroll
-            for (int i = 0; i < kRingGroups; ++i)
-                if (4 * (threadIdx.x + i * T) < H)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) f(s[i][j]);
-        };
-        const float rstd = row_rstd(
-            ss, a.mean, a.eps,
-            [&] {
-                float top = 0.f;
-                over_row([&](float v) { top = fmaxf(top, fabsf(v)); });
-                __syncthreads();  // the sums before have been read
-                return block_reduce<true>(top, sums[0]);
-            },
-            [&](float f) {
-                float sum = 0.f;
-                over_row([&](float v) { sum = fmaf(v * f, v * f, sum); });
-                __syncthreads();
-                return block_reduce<false>(sum, sums[0]);
-            });
+        const float rstd = rsqrtf(fmaf(ss, a.mean, a.eps));  // within 2^-22
         if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
         float amax = 0.f;
 #pragma unroll
@@ -676,8 +627,11 @@ extern "C" MOE_API int moe_residual_norm(const uint16_t* x, const void* residual
         return MOE_ERR_INVALID_ARG;
     if (H > kMaxH) return MOE_ERR_UNSUPPORTED;
     if (N == 0) return MOE_OK;
-    const moe::NormArgs a = {x, residual, weight,       weight_dtype == MOE_DTYPE_F32, N, H, eps, 1.f / static_cast<float>(H),
-                             y, residual_out, rstd, q, q_scale};
+    int k = 0;
+    while ((int64_t(1) << (2 * k)) < H) ++k;
+    const float mean = static_cast<float>(static_cast<double>(int64_t(1) << (2 * k)) / H);
+    const moe::NormArgs a = {x, residual, weight,       weight_dtype == MOE_DTYPE_F32, N, H, eps, std::ldexp(1.f, -k),
+                             mean, y,     residual_out, rstd,                          q, q_scale};
     const int res = residual == nullptr ? 0 : residual_dtype == MOE_DTYPE_F32 ? 2 : 1;
     const Ring ring = ring_for(N, H, static_cast<size_t>(H) * (2 + 2 * res));
     if (ring.slots == 8) return launch_norm_ring<8>(ring, a, res, stream);
