@@ -412,7 +412,9 @@ MOE_API int moe_combine(const uint16_t* y, const float* topk_w, int N, int K, in
  *   rstd = 1 / sqrt(mean(s^2) + eps),  v = s * rstd * weight,
  *   residual_out = s,  y = bf16(v),
  *   q_scale = max|v| / 448 (1/448 for a row of zeros),  q = e4m3(v / q_scale).
- * v is taken from the unrounded s, and q from the unrounded v.
+ * v is taken from the unrounded s, and q from the unrounded v.  A mean(s^2)
+ * above fp32's largest number counts as infinity; however small, it is exact
+ * to fp32's precision, with any eps.
  *   x            (device) bf16[N][H]; H % 8 == 0; every row array 16-byte aligned.
  *   residual     (device) [N][H] of residual_dtype (MOE_DTYPE_BF16 or _F32), or NULL.
  *   weight       (device) [H] of weight_dtype (MOE_DTYPE_BF16 or _F32), 16-byte aligned.
