@@ -65,6 +65,7 @@ constexpr int kEpilogueWarps = 8;
 constexpr int kWatchWarp = 2 + kEpilogueWarps;
 constexpr int kMendWarp = kWatchWarp + 1;  // of launches with dw
 constexpr int kOrders = 16;        // tiles whose orders are kept: more than slices that can be ready
+constexpr int kRun = 1, kStop = 2;  // Shared::decision
 constexpr int kChunk = 16;         // accumulator columns that a warp turns at a time
 
 __host__ __device__ constexpr int ffn_threads(int p) { return 96 + 32 * kEpilogueWarps + (p == kGrads ? 32 : 0); }
@@ -108,7 +109,9 @@ struct Shared {
     uint4 order[kOrders];   // the tiles' instructions: descriptor, slices (0: the end), steps of the last, dw
     uint32_t ready;         // slices that the instructions may use, counted from the launch's start
     uint32_t tmem;
-    int stop;               // the plan's status held an error (the pair's first block's counts)
+    int stop;               // the plan's status held an error when this block read it
+    int decision;           // in the pair's second block: what the first one decided
+    int started;            // the kernel ahead has ended
     int failed;             // a wait of this block ran out
     int scan[kMendWarp + 1], most[kMendWarp + 1];
 };
@@ -215,14 +218,31 @@ struct Turn {
 };
 
 // Bounded wait; on a timeout the caller gives up and the plan's status says so.
-// The limit is for a slice's steps.  A wait that lasts for many slices, a whole
-// tile's or more, gets a 65536th of it for each (15 us of the usual second,
-// where a slice takes 0.3 to 0.8).
-__device__ __forceinline__ bool wait(const Common& c, uint64_t* bar, uint32_t parity, uint64_t slices = 0) {
-    const uint64_t limit = static_cast<uint64_t>(c.timeout_ns);
-    if (mbar_wait_pair(bar, parity, limit + (limit >> 16) * slices)) return true;
-    record_error(c.status, MOE_ERR_DEVICE_TIMEOUT, blockIdx.x);
-    return false;
+// It also gives up where the pair's first block has stopped.  The limit is for a
+// slice's steps.  A wait that lasts for many slices, a whole tile's or more, gets
+// a 65536th of it for each (15 us of the usual second, where a slice takes 0.3 to
+// 0.8).  Its clock does not run while the kernel ahead still does.  All but the
+// first test stays out of line: inlined at every wait it cost 0.6 us a call.
+__device__ __noinline__ bool wait_on(int64_t timeout_ns, int32_t* status, const Shared* sh, const uint64_t* bar,
+                                     uint32_t parity, uint64_t slices) {
+    const volatile Shared* v = sh;
+    const uint64_t limit = static_cast<uint64_t>(timeout_ns) + static_cast<uint64_t>(timeout_ns >> 16) * slices;
+    uint64_t t0 = 0;
+    do {
+        if (v->decision == kStop) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0 || v->started == 0) {
+            t0 = now;
+        } else if (now - t0 > limit) {
+            record_error(status, MOE_ERR_DEVICE_TIMEOUT, blockIdx.x);
+            return false;
+        }
+    } while (!mbar_try_pair(bar, parity));
+    return true;
+}
+__device__ __forceinline__ bool wait(const Common& c, const Shared* sh, const uint64_t* bar, uint32_t parity,
+                                     uint64_t slices = 0) {
+    return mbar_try_pair(bar, parity) || wait_on(c.timeout_ns, c.status, sh, bar, parity, slices);
 }
 
 template <int P>
@@ -345,7 +365,7 @@ struct Producer {
                 if (ahead > 0) {
                     --ahead;
                 } else {
-                    if (!(ok = wait(c, &sh->empty[s], phase ^ 1u))) break;
+                    if (!(ok = wait(c, sh, &sh->empty[s], phase ^ 1u))) break;
                     if (P == kDw && k == mended) {
                         bar = smem_addr(&sh->tail_full[s]);
                         mbar_expect(bar, f.side.bytes);
@@ -401,13 +421,13 @@ struct Watcher {
                     make_uint4(mma_desc(FP8 ? 0u : 1u, m_transposed<P>(), n_transposed<P>(), kTile, (t.n + 15) & ~15),
                                t.slices, P == kDw ? ((t.count - 1) % 64) / 16 + 1 : 4, P == kDw);
             ++tiles_seen;
-            ok = __all_sync(FULL_MASK, wait(c, &sh->acc_empty[buf], acc_phase ^ 1u));
+            ok = __all_sync(FULL_MASK, wait(c, sh, &sh->acc_empty[buf], acc_phase ^ 1u));
             for (int k = 0; k < t.slices && ok; ++k) {
                 if (tail && k + 1 == t.slices) {
-                    ok = __all_sync(FULL_MASK, wait(c, &sh->tail_ready[s], (tail_phase >> s) & 1u));
+                    ok = __all_sync(FULL_MASK, wait(c, sh, &sh->tail_ready[s], (tail_phase >> s) & 1u));
                     tail_phase ^= 1u << s;
                 } else {
-                    ok = __all_sync(FULL_MASK, wait(c, &sh->full[s], (full_phase >> s) & 1u));
+                    ok = __all_sync(FULL_MASK, wait(c, sh, &sh->full[s], (full_phase >> s) & 1u));
                     full_phase ^= 1u << s;
                 }
                 if (ok) publish(sh, lane);
@@ -439,7 +459,7 @@ struct Issuer {
             if (used != ready) break;
             if ((n & 255u) == 255u) {
                 const uint64_t now = globaltimer_ns();
-                if (t0 == 0) t0 = now;
+                if (t0 == 0 || static_cast<const volatile Shared*>(sh)->started == 0) t0 = now;
                 else if (now - t0 > 2 * static_cast<uint64_t>(c.timeout_ns)) return ok = false;  // the watcher's limit first
             }
         }
@@ -509,7 +529,7 @@ struct Mender {
             s = (s + t.slices - 1) % ring.stages;
             passed += t.slices;
             if ((t.count & 15) != 0) {
-                ok = __all_sync(FULL_MASK, wait(c, &sh->tail_full[s], (tail_phase >> s) & 1u, passed));
+                ok = __all_sync(FULL_MASK, wait(c, sh, &sh->tail_full[s], (tail_phase >> s) & 1u, passed));
                 if (!ok) break;
                 passed = 0;
                 tail_phase ^= 1u << s;
@@ -692,7 +712,7 @@ struct Drain {
                 }
             }
             if (t.slices > 0) {
-                ok = __all_sync(FULL_MASK, wait(c, &sh->acc_full[buf], acc_phase, t.slices));
+                ok = __all_sync(FULL_MASK, wait(c, sh, &sh->acc_full[buf], acc_phase, t.slices));
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -757,24 +777,23 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         }
         fence_mbar_init();
         sh->ready = 0;
+        sh->decision = 0;
+        sh->started = !c.early;
         sh->failed = 0;
     }
     __syncwarp();
     if (warp == 1) tmem_alloc(&sh->tmem, 512);
+    tc_fence_before();
+    __syncwarp();
+    pair_arrive();  // this warp's part of the block is set up; the wait comes after the groups' scan
     // A call's later kernels start while the one before still runs: the groups
-    // and the weights were there before that one began, and its warps wait for
-    // it only once the first weights are on their way.
+    // and the weights were there before that one began, and only the warps that
+    // touch the rows wait for it.
     if (!c.early) {
         pdl_wait();
         pdl_trigger();
     }
-    // The pair's first block decides for both whether there is an error already:
-    // other blocks may record one between two reads, and a block that worked
-    // alone would wait out its limit.
     if (tid == 0) sh->stop = ld_volatile_s32(c.status) != 0;
-    tc_fence_before();
-    __syncwarp();
-    pair_arrive();  // this warp's part of the block is set up; the wait comes after the groups' scan
 
     // ---- the groups: row tiles before each expert
     const int per = (E + kThreads - 1) / kThreads;
@@ -828,7 +847,19 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     pair_wait();  // both blocks' barriers and tensor memory are ready
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    const bool run = leader_value(&sh->stop) == 0;
+    // The pair's first block decides for both whether there is an error already:
+    // other blocks may record one between the two reads. The second block does
+    // not wait for the decision (that cost a launch 0.4 us) unless it has
+    // read an error itself: once it works, its waits look for it.
+    bool run = sh->stop == 0;
+    if (rank == 0) {
+        if (tid == 0) set_in_second(&sh->decision, run ? kRun : kStop);
+    } else if (!run) {
+        const uint64_t t0 = globaltimer_ns();
+        while (*static_cast<volatile int*>(&sh->decision) == 0)
+            if (globaltimer_ns() - t0 > static_cast<uint64_t>(c.timeout_ns)) break;
+        run = *static_cast<volatile int*>(&sh->decision) == kRun;
+    }
     if (!run && c.early) pdl_wait();
 
     if (run && warp == 0) {
@@ -841,6 +872,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
             __syncwarp();
             pdl_wait();
             pdl_trigger();
+            if (lane == 0) static_cast<volatile Shared*>(sh)->started = 1;
         }
         if constexpr (P == kGrads) {
             if (a.job[0].M > 0) r.run<kDx, false>(a.job[0], c, g, sh, ring, rank, lane);
@@ -851,7 +883,6 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         }
         if (!r.ok) sh->failed = 1;
     } else if (run && warp == 1 && rank == 0) {
-        if (c.early) pdl_wait();  // a wait's limit does not run while the kernel ahead does
         if (lane == 0) {
             Issuer r;
             r.run<P, FP8>(c, sh, ring, tmem);
@@ -860,7 +891,6 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     } else if (run && warp == kWatchWarp && rank == 0) {
         Watcher r;
         r.turn = turn;
-        if (c.early) pdl_wait();
         if constexpr (P == kGrads) {
             if (a.job[0].M > 0) r.run<kDx, false>(a.job[0], c, g, sh, ring.stages, lane);
             if (a.job[1].M > 0) r.run<kDw, false>(a.job[1], c, g, sh, ring.stages, lane);
@@ -888,7 +918,6 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
         if constexpr (P == kGrads) {
             Mender r;
             r.turn = turn;
-            if (c.early) pdl_wait();
             if (a.job[0].M > 0) r.run<kDx>(a.job[0], c, g, sh, ring, lane);
             if (a.job[1].M > 0) r.run<kDw>(a.job[1], c, g, sh, ring, lane);
             if (a.job[2].M > 0) r.run<kDw>(a.job[2], c, g, sh, ring, lane);

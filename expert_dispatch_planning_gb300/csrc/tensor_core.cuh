@@ -30,33 +30,29 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
     return r;
 }
-__device__ __forceinline__ int leader_value(const int* p) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(leader_addr(p)) : "memory");
-    return v;
+// Set the pair's second block's variable.
+__device__ __forceinline__ void set_in_second(int* p, int v) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 1;" : "=r"(a) : "r"(smem_addr(p)));
+    asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
 }
-// mbar_wait_bounded for arrivals from the other block.  The thread sleeps in
-// the barrier unit for up to 20 us at a time: ten waiting warps that poll take
-// issue slots and shared-memory cycles from the copies and the instructions.
-__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-    uint64_t t0 = 0;
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
-            : "memory");
-        if (ok) return true;
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        else if (now - t0 > limit_ns) return false;
-    }
+// Whether phase `parity` is complete, arrivals from the other block included.
+// The thread sleeps in the barrier unit for up to 20 us: ten waiting warps that
+// poll take issue slots and shared-memory cycles from the copies and the
+// instructions.
+__device__ __forceinline__ bool mbar_try_pair(const uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
 }
 
 // ---------------------------------------------------------------- tensor memory
