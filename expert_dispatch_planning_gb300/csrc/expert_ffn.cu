@@ -551,12 +551,19 @@ struct Mender {
 };
 
 // ---------------------------------------------------------------- output (eight warps of each block)
-// silu(g) = g * sigmoid(g) and sigmoid(g).  The hardware exponential and
-// division are within 2^-20 of the exact value for |g| < 16; beyond, where
-// the sigmoid is 0 or 1 to bf16's precision or the result tiny, the relative
-// error grows as |g| * 2^-24.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
+// sigmoid(g) and 1 - sigmoid(g) from e = exp(-|g|), which neither overflows nor
+// takes the division's divisor beyond 2.  __expf is documented to within
+// 2 + floor(1.173 |g|) units in the last place, __fdividef to within 2: for
+// |g| < 16 less than 23 units in all, under 2^-18.4 relative, and for any g under
+// |g| * 2^-22 and a few units, until e leaves the normal numbers at |g| > 87.3.
+struct Sigmoid {
+    float s, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float g) {
+    const float e = __expf(-fabsf(g)), near = __fdividef(1.f, 1.f + e), far = e * near;
+    return g < 0.f ? Sigmoid{far, near} : Sigmoid{near, far};
+}
+__device__ __forceinline__ float silu(float g) { return g * sigmoid(g).s; }
 
 __device__ __forceinline__ void store4_bf16(uint16_t* p, float a, float b, float c, float d) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack2(a, b), pack2(c, d));
@@ -638,9 +645,9 @@ __device__ __forceinline__ void epilogue_chunk(const Job& job, const Common& a, 
                 float dg[4], du[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float s = sigmoid(gs[i]);
-                    dg[i] = dh[i] * us[i] * s * fmaf(gs[i], 1.f - s, 1.f);
-                    du[i] = dh[i] * gs[i] * s;
+                    const Sigmoid s = sigmoid(gs[i]);
+                    dg[i] = dh[i] * us[i] * s.s * fmaf(gs[i], s.rest, 1.f);
+                    du[i] = dh[i] * gs[i] * s.s;
                 }
                 store4_bf16(job.out + row * 2 * M + c, dg[0], dg[1], dg[2], dg[3]);
                 store4_bf16(job.out + row * 2 * M + M + c, du[0], du[1], du[2], du[3]);
