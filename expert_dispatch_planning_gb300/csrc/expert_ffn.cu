@@ -132,6 +132,11 @@ struct Groups {
     int E;
 };
 
+// A group's row tiles; one without rows has one for its padding's zeros.
+__device__ __forceinline__ int group_tiles(int count, int padded) {
+    return count > 0 ? (count + kTile - 1) / kTile : padded > 0 ? 1 : 0;
+}
+
 // A product's tiles in order: expert by expert, and within one in bands of 8
 // tiles of the N side with the M side outermost, so that what the pairs work
 // on at one time is about square and stays in L2.  A warp walks over its own
@@ -205,7 +210,7 @@ struct Tiles {
         } else {
             r.n0 = j * length;
             r.n = min(length, r.count - r.n0);
-            r.slices = k_slices;
+            r.slices = r.n > 0 ? k_slices : 0;
         }
         return r;
     }
@@ -519,13 +524,13 @@ struct Mender {
                                         const RingShape& ring, int lane) {
         Tiles<P, false> tiles(job, g);
         for (; ok && turn.next < tiles.total; turn.next += turn.pairs) {
-            if (P != kDw) {  // only to know where in the ring the next job starts
-                s = (s + tiles.k_slices) % ring.stages;
-                passed += tiles.k_slices;
-                continue;
-            }
             const Tile t = tiles.at(g, turn.next, lane);
             if (t.slices == 0) continue;
+            if (P != kDw) {  // only to know where in the ring the next job starts
+                s = (s + t.slices) % ring.stages;
+                passed += t.slices;
+                continue;
+            }
             s = (s + t.slices - 1) % ring.stages;
             passed += t.slices;
             if ((t.count & 15) != 0) {
@@ -807,13 +812,13 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     int mine = 0, longest = 0;
     for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) {
         const int64_t f = __ldg(c.cu + e), n = __ldg(c.count + e), after = __ldg(c.cu + e + 1);
-        const int64_t p = n == 0 ? 0 : after - f;
+        const int64_t p = after - f;
         const bool fits = n >= 0 && f >= 0 && p >= n && f + p <= c.rows;
         if (!fits) record_error(c.status, MOE_ERR_DEVICE_INDEX, e);
         first[e] = fits ? static_cast<int>(f) : 0;
         count[e] = fits ? static_cast<int>(n) : 0;
         padded[e] = fits ? static_cast<int>(p) : 0;
-        mine += (count[e] + kTile - 1) / kTile;
+        mine += group_tiles(count[e], padded[e]);
         longest = max(longest, count[e]);
     }
     int before = mine;  // inclusive over the warp, then exclusive over the block
@@ -836,7 +841,7 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     }
     for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) {
         prefix[e] = before;
-        before += (count[e] + kTile - 1) / kTile;
+        before += group_tiles(count[e], padded[e]);
     }
     if (tid == 0) prefix[E] = row_tiles;
     const Groups g = {first, count, padded, prefix, E};

@@ -1,0 +1,71 @@
+"""The experts' feed-forward over other layouts of groups than the planner's, and many experts, against 64 bits."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import block_checks as bc
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def m():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import expert_dispatch_planning_gb300 as m
+    return m
+
+
+def layout(counts, sizes, extra=3):
+    """Groups of `counts` rows in places of `sizes` rows."""
+    begins = [0]
+    for s in sizes:
+        begins.append(begins[-1] + s)
+    rows = begins[-1] + extra
+    kind = torch.full((rows,), 2, dtype=torch.int64)
+    for b, n, s in zip(begins, counts, sizes):
+        kind[b:b + n], kind[b + n:b + s] = 0, 1
+    i32 = dict(dtype=torch.int32, device="cuda")
+    return SimpleNamespace(cu_seqlens=torch.tensor(begins, **i32), tokens_per_expert=torch.tensor(counts, **i32),
+                           status=torch.zeros(4, **i32), rows=rows, counts=list(counts), begins=begins, kind=kind.cuda())
+
+
+def check_step(m, p, H, I, seed=0):  # noqa: E741
+    """A forward and backward step with NaN and infinities in the rows of no group: every output against 64 bits."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    r = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(BF16)  # noqa: E731
+    E, M = len(p.counts), p.rows
+    x, dy, wgu, wd = r(M, H), r(M, H), r(E, 2, I, H, std=H ** -0.5), r(E, H, I, std=I ** -0.5)
+    live = p.kind == 0
+    x[~live], dy[~live] = float("nan"), float("inf")
+    full = lambda *s, t=BF16, v=7.0: torch.full(s, v, dtype=t, device="cuda")  # noqa: E731
+    h, pre = full(M, I), full(M, 2, I, t=torch.float32)
+    y = m.expert_ffn(x, wgu, wd, p, h=h, preact=pre, out=full(M, H))
+    dx, dwgu, dwd = m.expert_ffn_backward(dy, x, h, pre, wgu, wd, p, dx=full(M, H))
+    assert int(p.status[0]) == 0
+    W, D = wgu.double(), wd.double()
+    clean = lambda t: torch.where(live.reshape(-1, *[1] * (t.dim() - 1)), t.double(), 0.0)  # noqa: E731
+    o = bc.ffn_forward(clean(x), W, D, p)
+    bc.assert_within(h[live], o.h[live], bc.h_bound(o, H)[live], "h")
+    bc.assert_within(y[live], o.y[live], bc.y_bound(o, D, p, H)[live], "y")
+    pre = clean(pre)
+    b = bc.ffn_backward(clean(dy), clean(x), clean(h), pre[:, 0], pre[:, 1], W, D, p)
+    bc.assert_within(dx[live], b.dx[live], b.dx_tol[live], "dx")
+    bc.assert_within(dwgu, b.dwgu, b.dwgu_tol, "dw_gate_up")
+    bc.assert_within(dwd, b.dwd, b.dwd_tol, "dw_down")
+    for out in (y, dx):
+        assert (out[p.kind == 1] == 0).all() and (out[p.kind == 2] == 7).all()
+
+
+@pytest.mark.parametrize("counts,sizes", [
+    ([5, 0, 130, 0], [160, 160, 160, 160]),          # a place of fixed size for every expert, two of them empty
+    ([0, 0, 0], [16, 300, 1]),                       # nothing but padding
+    ([0, 257, 0, 0, 3], [40, 512, 0, 7, 3]),         # empty places first, in the middle and of no rows
+])
+def test_places_of_empty_experts(m, counts, sizes):
+    """The padding of a group without rows is written as zeros too."""
+    check_step(m, layout(counts, sizes), 136, 72)
