@@ -775,8 +775,10 @@ __global__ void __launch_bounds__(ffn_threads(P), 1) ffn_kernel(const __grid_con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(pair_rank());
     if (tid == 0) {
-        tensor_prefetch(&a.job[0].map_m);
-        tensor_prefetch(&a.job[0].map_n[4]);
+        if (a.job[0].M > 0) {  // else its maps are not set
+            tensor_prefetch(&a.job[0].map_m);
+            tensor_prefetch(&a.job[0].map_n[4]);
+        }
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sh->full[i], 1);
             mbar_init(&sh->empty[i], 1);

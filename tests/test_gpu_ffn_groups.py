@@ -69,3 +69,34 @@ def check_step(m, p, H, I, seed=0):  # noqa: E741
 def test_places_of_empty_experts(m, counts, sizes):
     """The padding of a group without rows is written as zeros too."""
     check_step(m, layout(counts, sizes), 136, 72)
+
+
+def test_any_of_the_gradients_alone(m):
+    """The C call with each choice of dx, dw_gate_up and dw_down: the bits of all three together."""
+    import ctypes
+    import itertools
+
+    from expert_dispatch_planning_gb300 import _lib
+    p, H, I = bc.groups([70, 0, 3, 300], 16), 136, 72  # noqa: E741
+    E, M = len(p.counts), p.rows
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    r = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(BF16)  # noqa: E731
+    x, dy, wgu, wd = r(M, H), r(M, H), r(E, 2, I, H, std=H ** -0.5), r(E, H, I, std=I ** -0.5)
+    h, pre = torch.empty(M, I, dtype=BF16, device="cuda"), torch.empty(M, 2, I, device="cuda")
+    m.expert_ffn(x, wgu, wd, p, h=h, preact=pre)
+    plan = _lib.MoePlanOut()
+    plan.cu_seqlens, plan.tokens_per_expert = p.cu_seqlens.data_ptr(), p.tokens_per_expert.data_ptr()
+    plan.status = p.status.data_ptr()
+    shapes, want = [(M, H), (E, 2, I, H), (E, H, I)], None
+    for pick in sorted(itertools.product((True, False), repeat=3), reverse=True):
+        out = [torch.full(s, 7.0, dtype=BF16, device="cuda") for s in shapes]
+        dgu = torch.empty(M, 2, I, dtype=BF16, device="cuda")
+        rc = _lib.load().moe_expert_ffn_backward(
+            dy.data_ptr(), x.data_ptr(), h.data_ptr(), pre.data_ptr(), wgu.data_ptr(), wd.data_ptr(), M, E, H, I,
+            ctypes.byref(plan), dgu.data_ptr(), *[t.data_ptr() if k else None for t, k in zip(out, pick)],
+            torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and int(p.status[0]) == 0
+        want = want or out
+        for t, k, w in zip(out, pick, want):
+            assert torch.equal(t, w) if k else (t == 7).all()
