@@ -72,16 +72,18 @@ Tensor tensor(PyObject* o, const char* name) {
     return THPVariable_Unpack(o);
 }
 
+// The kernels run on the current device and reach only its memory.
 bool fits(const Tensor& t, ScalarType type, Sizes sizes) {
-    return t.defined() && t.scalar_type() == type && t.is_cuda() && t.is_contiguous() &&
-           t.sizes() == at::IntArrayRef(sizes.begin(), sizes.size());
+    return t.defined() && t.scalar_type() == type && t.is_cuda() && t.get_device() == c10::cuda::current_device() &&
+           t.is_contiguous() && t.sizes() == at::IntArrayRef(sizes.begin(), sizes.size());
 }
 
 void need(const Tensor& t, ScalarType type, Sizes sizes, const char* name) {
     if (fits(t, type, sizes)) return;
     std::ostringstream s;
-    s << name << " must be a contiguous CUDA " << name_of(type) << " tensor of shape " << text(sizes) << " (got ";
-    if (t.defined()) s << name_of(t.scalar_type()) << " " << text(t.sizes());
+    s << name << " must be a contiguous CUDA " << name_of(type) << " tensor of shape " << text(sizes)
+      << " on the current device (got ";
+    if (t.defined()) s << name_of(t.scalar_type()) << " " << text(t.sizes()) << " on " << t.device().str();
     else s << "None";
     refuse(s.str() + ")");
 }
@@ -122,7 +124,8 @@ int dtype_of(const Tensor& t) {
 // current one.  While it lives, the handle's stream is the current one, so that
 // what the call allocates comes from the memory of the stream that uses it: a
 // workspace that is released as the call returns can only go to later work of
-// that stream, and no earlier work of another stream still writes to it.
+// that stream, and no earlier work of another stream still writes to it.  Made
+// once a CUDA tensor has been seen: without a GPU there is no stream to ask for.
 class OnStream {
 public:
     explicit OnStream(PyObject* o) : current_(c10::cuda::getCurrentCUDAStream()), handle_(current_.stream()) {
@@ -194,11 +197,11 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const double eps = PyFloat_AsDouble(a[3]);
         if (eps == -1.0 && PyErr_Occurred()) return nullptr;
         const bool quantize = a[4] == Py_True;
-        const OnStream stream(a[9]);
         Tensor residual_out = tensor(a[6], "residual_out"), q = tensor(a[7], "q"), q_scale = tensor(a[8], "q_scale");
         need_dims(x, 2, "x");
         const int64_t N = x.size(0), H = x.size(1);
         need(x, kBf16, {N, H}, "x");
+        const OnStream stream(a[9]);
         need_float(weight, "weight");
         need(weight, weight.scalar_type(), {H}, "weight");
         if (residual.defined()) {
@@ -238,10 +241,10 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
         const Tensor dy = tensor(a[0], "dy"), s = tensor(a[1], "s"), weight = tensor(a[2], "weight"),
                      rstd = tensor(a[3], "rstd"), ds = tensor(a[4], "ds");
-        const OnStream stream(a[5]);
         need_dims(dy, 2, "dy");
         const int64_t N = dy.size(0), H = dy.size(1);
         need(dy, kBf16, {N, H}, "dy");
+        const OnStream stream(a[5]);
         need_float(s, "s");
         need(s, s.scalar_type(), {N, H}, "s");
         need_float(weight, "weight");
@@ -273,7 +276,6 @@ PyObject* expert_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
         const Tensor x = tensor(a[0], "x"), wgu = tensor(a[1], "w_gate_up"), wd = tensor(a[2], "w_down"),
                      x_scale = tensor(a[6], "x_scale"), w_scale = tensor(a[7], "w_scale"), preact = tensor(a[9], "preact");
-        const OnStream stream(a[11]);
         need_dims(x, 2, "x");
         need_dims(wgu, 4, "w_gate_up");
         const int64_t rows = x.size(0), H = x.size(1), E = wgu.size(0), I = wgu.size(2);
@@ -281,6 +283,7 @@ PyObject* expert_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (type != kBf16 && type != kE4m3)
             refuse(std::string("x must be bfloat16 or float8_e4m3fn (got ") + name_of(type) + ")");
         need(x, type, {rows, H}, "x");
+        const OnStream stream(a[11]);
         need(wgu, type, {E, 2, I, H}, "w_gate_up");
         need(wd, kBf16, {E, H, I}, "w_down");
         if (type == kE4m3) {
@@ -316,11 +319,11 @@ PyObject* expert_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      wgu = tensor(a[4], "w_gate_up"), wd = tensor(a[5], "w_down");
         Tensor dx = tensor(a[9], "dx");
         const bool need_dx = a[11] == Py_True, need_dw = a[12] == Py_True;
-        const OnStream stream(a[13]);
         need_dims(x, 2, "x");
         need_dims(wgu, 4, "w_gate_up");
         const int64_t rows = x.size(0), H = x.size(1), E = wgu.size(0), I = wgu.size(2);
         need(x, kBf16, {rows, H}, "x");
+        const OnStream stream(a[13]);
         need(dy, kBf16, {rows, H}, "dy");
         need(h, kBf16, {rows, I}, "h");
         need(preact, kF32, {rows, 2, I}, "preact");
@@ -353,13 +356,13 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
         const Tensor dout = tensor(a[0], "dout"), y = tensor(a[1], "y"), w = tensor(a[2], "topk_w"),
                      dst = tensor(a[3], "dst"), zfr = tensor(a[4], "zero_fill_ranges"), status = tensor(a[5], "status");
-        const OnStream stream(a[8]);
         need_dims(dout, 2, "dout");
         need_dims(y, 2, "y");
         need_dims(dst, 2, "dst");
         need_dims(zfr, 2, "zero_fill_ranges");
         const int64_t N = dout.size(0), H = dout.size(1), rows = y.size(0), K = dst.size(1), E = zfr.size(0);
         need(dout, kBf16, {N, H}, "dout");
+        const OnStream stream(a[8]);
         need(y, kBf16, {rows, H}, "y");
         need(w, kF32, {N, K}, "topk_w");
         need(dst, kI32, {N, K}, "dst");
