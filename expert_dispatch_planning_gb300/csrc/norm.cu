@@ -654,9 +654,9 @@ extern "C" MOE_API int moe_residual_norm(const uint16_t* x, const void* residual
                              mean, y,     residual_out, rstd,                          q, q_scale};
     const int res = residual == nullptr ? 0 : residual_dtype == MOE_DTYPE_F32 ? 2 : 1;
     const Ring ring = eps >= moe::kLeastEps ? ring_for(N, H, static_cast<size_t>(H) * (2 + 2 * res)) : Ring();
+    // (four slots of at most 8192 columns in 6 bytes always fit)
     if (ring.slots == 8) return launch_norm_ring<8>(ring, a, res, stream);
     if (ring.slots == 4) return launch_norm_ring<4>(ring, a, res, stream);
-    if (ring.slots == 2) return launch_norm_ring<2>(ring, a, res, stream);
     if (H <= 512) {
         const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(N) + 3) / 4)), block(128);
         return H <= 256 ? launch_norm<1, true>(a, res, grid, block, stream)
