@@ -32,9 +32,22 @@ def _stream(stream=None) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+# With stream= a call launches there and takes what it allocates (outputs not
+# given, workspaces) from that stream's memory; the arguments have to be ready
+# on it and live until it has passed the call.
 def _on(stream):
     """Allocations and fills of a call that runs on `stream` (None: the current one) belong to that stream."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """A call's output, from the memory of the stream it runs on; the caller's current stream goes on to use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
 
 
 def _ptr(t) -> int:
@@ -58,9 +71,9 @@ def route_topk(logits: torch.Tensor, K: int, scoring="softmax", renormalize: boo
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
     if topk_idx is None:
-        topk_idx = torch.empty((N, K), dtype=torch.int32, device=logits.device)
+        topk_idx = _empty((N, K), torch.int32, logits.device, stream)
     if topk_w is None:
-        topk_w = torch.empty((N, K), dtype=torch.float32, device=logits.device)
+        topk_w = _empty((N, K), torch.float32, logits.device, stream)
     _need(topk_idx, torch.int32, (N, K), "topk_idx")
     _need(topk_w, torch.float32, (N, K), "topk_w")
     rc = load().moe_route_topk(_ptr(logits), _ptr(bias), N, E, K, SCORING[scoring], int(bool(renormalize)),
@@ -177,9 +190,9 @@ def route_plan(logits: torch.Tensor, K: int, R: int, alignment: int, scoring="so
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
     if topk_idx is None:
-        topk_idx = torch.empty((N, K), dtype=torch.int32, device=logits.device)
+        topk_idx = _empty((N, K), torch.int32, logits.device, stream)
     if topk_w is None:
-        topk_w = torch.empty((N, K), dtype=torch.float32, device=logits.device)
+        topk_w = _empty((N, K), torch.float32, logits.device, stream)
     _need(topk_idx, torch.int32, (N, K), "topk_idx")
     _need(topk_w, torch.float32, (N, K), "topk_w")
     if out is None:
@@ -234,13 +247,11 @@ class BalancedPlan:
               "rank_zero_fill", "expert_offsets", "dst")
 
     @classmethod
-    def allocate(cls, N, E, K, R, B, device="cuda") -> "BalancedPlan":
-        i32 = dict(dtype=torch.int32, device=device)
-        b = cls(N=N, E=E, K=K, R=R, B=B, z=torch.empty((R, R), **i32), alloc=torch.empty((R, E), **i32),
-                alloc_cumsum=torch.empty((E, R), **i32), experts_to_copy=torch.empty((R, max(B, 1)), **i32),
-                remote_stats=torch.empty((R, 2), **i32), rank_cu_seqlens=torch.empty((R, E + B), **i32),
-                rank_zero_fill=torch.empty((R, E + B, 2), **i32), expert_offsets=torch.empty((R, E), **i32),
-                dst=torch.empty((N, K), **i32))
+    def allocate(cls, N, E, K, R, B, device="cuda", stream=None) -> "BalancedPlan":
+        new = lambda *shape: _empty(shape, torch.int32, device, stream)  # noqa: E731
+        b = cls(N=N, E=E, K=K, R=R, B=B, z=new(R, R), alloc=new(R, E), alloc_cumsum=new(E, R),
+                experts_to_copy=new(R, max(B, 1)), remote_stats=new(R, 2), rank_cu_seqlens=new(R, E + B),
+                rank_zero_fill=new(R, E + B, 2), expert_offsets=new(R, E), dst=new(N, K))
         b.c_struct = MoeBalancedPlanOut(*[getattr(b, k).data_ptr() for k in cls.FIELDS])
         return b
 
@@ -256,7 +267,7 @@ def plan_balanced(topk_idx: torch.Tensor, p: Plan, token_padding: int, capacity:
     N, K = topk_idx.shape
     _need(topk_idx, torch.int32, (p.N, p.K), "topk_idx")
     if out is None:
-        out = BalancedPlan.allocate(N, p.E, K, p.R, B, device=topk_idx.device)
+        out = BalancedPlan.allocate(N, p.E, K, p.R, B, device=topk_idx.device, stream=stream)
     rc = load().moe_plan_balanced(ctypes.byref(p.c_struct), _ptr(topk_idx), N, p.E, K, p.R, int(token_padding),
                                   int(capacity), int(B), int(NvS), ctypes.byref(out.c_struct), _stream(stream))
     check("moe_plan_balanced", rc)
@@ -269,8 +280,7 @@ def tile_map(p: Plan, max_tiles: int | None = None, out=None, stream=None):
     if out is None:
         if max_tiles is None:
             max_tiles = max(1, p.P_cap // p.alignment)
-        out = (torch.empty(max_tiles, dtype=torch.int32, device=dev),
-               torch.empty(max_tiles, dtype=torch.int32, device=dev), torch.empty(2, dtype=torch.int32, device=dev))
+        out = tuple(_empty(n, torch.int32, dev, stream) for n in (max_tiles, max_tiles, 2))
     te, tl, sizes = out
     max_tiles = te.numel()
     _need(tl, torch.int32, (max_tiles,), "tile_row_limit")
@@ -295,8 +305,7 @@ def rank_layout(p: Plan, num_channels: int, workspace: torch.Tensor | None = Non
         with _on(stream):
             workspace = rank_layout_workspace(p.N, p.R, device=dev)
     if out is None:
-        out = (torch.empty((p.R, num_channels), dtype=torch.int32, device=dev),
-               torch.empty((p.N, p.R), dtype=torch.int32, device=dev))
+        out = tuple(_empty(n, torch.int32, dev, stream) for n in ((p.R, num_channels), (p.N, p.R)))
     cpm, trs = out
     _need(cpm, torch.int32, (p.R, num_channels), "channel_prefix_matrix")
     _need(trs, torch.int32, (p.N, p.R), "token_rank_slot")
@@ -317,7 +326,7 @@ def permute(x: torch.Tensor, p: Plan, out: torch.Tensor | None = None, stream=No
     N, H = x.shape
     _need(x, torch.bfloat16, (p.N, H), "x")
     if out is None:
-        out = torch.empty((p.P_cap, H), dtype=torch.bfloat16, device=x.device)
+        out = _empty((p.P_cap, H), torch.bfloat16, x.device, stream)
     _need(out, torch.bfloat16, (p.P_cap, H), "permuted")
     rc = load().moe_permute(_ptr(x), N, H, p.K, p.E, p.alignment, ctypes.byref(p.c_struct), _ptr(out),
                             MOE_PERMUTE_EARLY_X if early_x else 0, _stream(stream))
@@ -332,7 +341,7 @@ def combine(y: torch.Tensor, topk_w: torch.Tensor, p: Plan, out: torch.Tensor | 
     _need(y, torch.bfloat16, (p.P_cap, H), "y")
     _need(topk_w, torch.float32, (p.N, p.K), "topk_w")
     if out is None:
-        out = torch.empty((p.N, H), dtype=torch.bfloat16, device=y.device)
+        out = _empty((p.N, H), torch.bfloat16, y.device, stream)
     _need(out, torch.bfloat16, (p.N, H), "out")
     rc = load().moe_combine(_ptr(y), _ptr(topk_w), p.N, p.K, H, p.E, p.alignment, ctypes.byref(p.c_struct),
                             _ptr(out), _stream(stream))
@@ -341,9 +350,6 @@ def combine(y: torch.Tensor, topk_w: torch.Tensor, p: Plan, out: torch.Tensor | 
 
 
 # ---------------------------------------------------------------- around the experts
-# With stream= a call launches there and takes what it allocates (outputs not
-# given, workspaces) from that stream's memory; the arguments have to be ready
-# on it and live until it has passed the call.
 def _handle(stream):
     return None if stream is None else stream.cuda_stream
 
