@@ -72,9 +72,12 @@ Tensor tensor(PyObject* o, const char* name) {
     return THPVariable_Unpack(o);
 }
 
-// The kernels run on the current device and reach only its memory.
+// The kernels run on the current device and reach only its memory.  A call asks
+// for the device once (OnStream, which also looks at the tensors before it).
+thread_local int call_device = -1;
+
 bool fits(const Tensor& t, ScalarType type, Sizes sizes) {
-    return t.defined() && t.scalar_type() == type && t.is_cuda() && t.get_device() == c10::cuda::current_device() &&
+    return t.defined() && t.scalar_type() == type && t.is_cuda() && (call_device < 0 || t.get_device() == call_device) &&
            t.is_contiguous() && t.sizes() == at::IntArrayRef(sizes.begin(), sizes.size());
 }
 
@@ -128,10 +131,19 @@ int dtype_of(const Tensor& t) {
 // once a CUDA tensor has been seen: without a GPU there is no stream to ask for.
 class OnStream {
 public:
-    explicit OnStream(PyObject* o) : current_(c10::cuda::getCurrentCUDAStream()), handle_(current_.stream()) {
+    OnStream(PyObject* o, const Tensor& first, const char* name)
+        : current_(c10::cuda::getCurrentCUDAStream()), handle_(current_.stream()) {
+        call_device = current_.device_index();
+        if (first.get_device() != call_device) {
+            call_device = -1;
+            refuse(std::string(name) + " must be on the current device (got " + first.device().str() + ")");
+        }
         if (o == Py_None) return;
         void* p = PyLong_AsVoidPtr(o);
-        if (p == nullptr && PyErr_Occurred()) throw BadArgument();
+        if (p == nullptr && PyErr_Occurred()) {
+            call_device = -1;
+            throw BadArgument();
+        }
         handle_ = static_cast<cudaStream_t>(p);
         if (handle_ == current_.stream()) return;
         const c10::DeviceIndex device = current_.device_index();
@@ -139,6 +151,8 @@ public:
                                          : c10::cuda::getStreamFromExternal(handle_, device));
         other_ = true;
     }
+    ~OnStream() { call_device = -1; }
+    OnStream(const OnStream&) = delete;
     cudaStream_t handle() const { return handle_; }
     // An output that the call allocated: the caller's current stream goes on to use it.
     void hand_over(const Tensor& out, PyObject* given) const {
@@ -201,7 +215,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need_dims(x, 2, "x");
         const int64_t N = x.size(0), H = x.size(1);
         need(x, kBf16, {N, H}, "x");
-        const OnStream stream(a[9]);
+        const OnStream stream(a[9], x, "x");
         need_float(weight, "weight");
         need(weight, weight.scalar_type(), {H}, "weight");
         if (residual.defined()) {
@@ -244,7 +258,7 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need_dims(dy, 2, "dy");
         const int64_t N = dy.size(0), H = dy.size(1);
         need(dy, kBf16, {N, H}, "dy");
-        const OnStream stream(a[5]);
+        const OnStream stream(a[5], dy, "dy");
         need_float(s, "s");
         need(s, s.scalar_type(), {N, H}, "s");
         need_float(weight, "weight");
@@ -283,7 +297,7 @@ PyObject* expert_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (type != kBf16 && type != kE4m3)
             refuse(std::string("x must be bfloat16 or float8_e4m3fn (got ") + name_of(type) + ")");
         need(x, type, {rows, H}, "x");
-        const OnStream stream(a[11]);
+        const OnStream stream(a[11], x, "x");
         need(wgu, type, {E, 2, I, H}, "w_gate_up");
         need(wd, kBf16, {E, H, I}, "w_down");
         if (type == kE4m3) {
@@ -323,7 +337,7 @@ PyObject* expert_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need_dims(wgu, 4, "w_gate_up");
         const int64_t rows = x.size(0), H = x.size(1), E = wgu.size(0), I = wgu.size(2);
         need(x, kBf16, {rows, H}, "x");
-        const OnStream stream(a[13]);
+        const OnStream stream(a[13], x, "x");
         need(dy, kBf16, {rows, H}, "dy");
         need(h, kBf16, {rows, I}, "h");
         need(preact, kF32, {rows, 2, I}, "preact");
@@ -362,7 +376,7 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need_dims(zfr, 2, "zero_fill_ranges");
         const int64_t N = dout.size(0), H = dout.size(1), rows = y.size(0), K = dst.size(1), E = zfr.size(0);
         need(dout, kBf16, {N, H}, "dout");
-        const OnStream stream(a[8]);
+        const OnStream stream(a[8], dout, "dout");
         need(y, kBf16, {rows, H}, "y");
         need(w, kF32, {N, K}, "topk_w");
         need(dst, kI32, {N, K}, "dst");
