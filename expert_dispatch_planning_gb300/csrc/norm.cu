@@ -85,6 +85,18 @@ __device__ __forceinline__ void load_weight8(const void* w, int f32, int c, floa
     }
 }
 
+// The residual's elements 8c .. 8c+7: residual_out may be the residual itself,
+// so that they are not read-only for the kernel.
+__device__ __forceinline__ void load8_written(const uint16_t* row, int c, float (&f)[8]) {
+    unpack8(*reinterpret_cast<const uint4*>(row + 8 * static_cast<int64_t>(c)), f);
+}
+__device__ __forceinline__ void load8_written(const float* row, int c, float (&f)[8]) {
+    const float4* p = reinterpret_cast<const float4*>(row + 8 * static_cast<int64_t>(c));
+    const float4 a = p[0], b = p[1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
 // The 8-bit output's scale of a row and its values' rounding: a product with
 // the scale's reciprocal, both moved up by a power of two where the reciprocal
 // would overflow.
@@ -126,8 +138,8 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_kernel(const Norm
             load8(a.x + at, c, s[i]);
             if constexpr (RES != 0) {
                 float r[8];
-                if constexpr (RES == 2) load8(static_cast<const float*>(a.residual) + at, c, r);
-                else load8(static_cast<const uint16_t*>(a.residual) + at, c, r);
+                if constexpr (RES == 2) load8_written(static_cast<const float*>(a.residual) + at, c, r);
+                else load8_written(static_cast<const uint16_t*>(a.residual) + at, c, r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s[i][j] += r[j];
             }
