@@ -110,7 +110,7 @@ struct Quantum {
 };
 __device__ __forceinline__ Quantum quantum_of(float amax) {
     Quantum q;
-    q.scale = (amax > 0.f ? amax : 1.f) * (1.f / kE4m3Max);
+    q.scale = fmaxf((amax > 0.f ? amax : 1.f) * (1.f / kE4m3Max), 0x1p-149f);  // never 0
     q.up = q.scale < 1e-30f ? 0x1p64f : 1.f;
     q.inv = __fdividef(1.f, q.scale * q.up);
     return q;

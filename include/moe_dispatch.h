@@ -411,7 +411,7 @@ MOE_API int moe_combine(const uint16_t* y, const float* topk_w, int N, int K, in
  *   s = x + residual (x alone without a residual),
  *   rstd = 1 / sqrt(mean(s^2) + eps),  v = s * rstd * weight,
  *   residual_out = s,  y = bf16(v),
- *   q_scale = max|v| / 448 (1/448 for a row of zeros),  q = e4m3(v / q_scale).
+ *   q_scale = max|v| / 448 (1/448 for a row of zeros; at least 2^-149),  q = e4m3(v / q_scale).
  * v is taken from the unrounded s, and q from the unrounded v.  A mean(s^2)
  * above fp32's largest number counts as infinity; however small, it is exact
  * to fp32's precision, with any eps.

@@ -53,3 +53,19 @@ def test_mean_square_beyond_fp32(m):
         x = torch.full((N, 1032), 1e25, dtype=BF16, device="cuda")
         o = m.residual_norm(x, torch.ones(1032, dtype=BF16, device="cuda"), quantize=True)
         assert (o.rstd == 0).all() and (o.y == 0).all() and (o.q.float() == 0).all()
+
+
+@pytest.mark.parametrize("N", [2, 5000])
+def test_scale_at_the_end_of_fp32(m, N):
+    """Outputs so small that max|v| / 448 is no number of fp32: the scale stays above 0 and zeros stay zeros."""
+    H = 640
+    x = torch.randn(N, H, device="cuda").to(BF16)
+    x[:, ::3] = 0
+    w = torch.full((H,), 4e-44, dtype=F32, device="cuda")
+    o = m.residual_norm(x, w, quantize=True)
+    assert (o.q_scale == 2.0 ** -149).all()
+    assert torch.isfinite(o.q.float()).all() and (o.q.float()[:, ::3] == 0).all()
+    v = x.double() * (x.double().square().mean(1, keepdim=True) + 1e-6).rsqrt() * w.double()
+    back = o.q.float().double() * o.q_scale.double()[:, None]
+    # v itself is known to a unit of 2^-149, and q to 2^-4 of it
+    assert ((back - v).abs() <= 2.0 ** -4 * v.abs() + 2 * 2.0 ** -149).all()
