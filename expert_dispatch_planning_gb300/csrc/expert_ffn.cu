@@ -41,13 +41,18 @@
 // them in both operands as soon as the slice is there, while the instructions
 // of the slices before it run.
 //
+// The pair's blocks agree on whether to run: the first one decides (see
+// ffn_kernel).  A group without rows that has a place all the same gets one row
+// tile without slices, for its padding's zeros.
+//
 // What bounds it, measured on a GB300 (6.68 TB/s copied, 1914 TFLOP/s in bf16
 // at burst and 1721 under the power limit by the library): many rows, the tensor
-// cores: 32768 rows, 8 experts, H = I = 4096: forward and backward 6.2 ms, 1590
-// TFLOP/s, tensor pipes 70-87% busy; gated in 8 bits 3.2 PFLOP/s.  Few rows, the
-// weights' bytes: 61 tokens over 64 experts of 4096 x 1280, 211 us, 6.4 TB/s of
-// what has to be read.  One token through 8 experts of 2048 x 768, 26 us: 10 and 5
-// of them stream the weights, the rest are the two launches' fixed costs.
+// cores: 32768 rows, 8 experts, H = I = 4096: forward and backward 6.2 to 6.4 ms,
+// 1550 to 1600 TFLOP/s, tensor pipes 70-87% busy (gated in 8 bits, 8192 rows
+// profiled alone: 3.4 PFLOP/s).  Few rows, the weights' bytes: 61 tokens over 64 experts of 4096 x 1280,
+// 212 us, 6.3 TB/s of what has to be read.  One token through 8 experts of
+// 2048 x 768, 26 us: 10 and 5 of them stream the weights, the rest are the two
+// launches' fixed costs.
 #include <cuda_fp8.h>
 
 #include "tensor_core.cuh"
