@@ -25,6 +25,8 @@ MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F32 = 1
 MOE_DTYPE_E4M3 = 2
 
+MOE_LAYER_MAX_TOKENS = 64
+
 _P = ctypes.c_void_p
 _i32 = ctypes.c_int
 _i64 = ctypes.c_int64
@@ -75,6 +77,13 @@ SIGNATURES = [
     ("moe_expert_ffn_backward", _i32, [_P, _P, _P, _P, _P, _P, _i64, _i32, _i32, _i32, ctypes.POINTER(MoePlanOut), _P,
                                        _P, _P, _P, _P]),
     ("moe_combine_backward", _i32, [_P, _P, _P, _i32, _i32, _i32, _i32, _i64, ctypes.POINTER(MoePlanOut), _P, _P, _P]),
+    ("moe_block_norm", _i32, [_P, _P, _i32, _P, _i32, _P, _i32, _P, _i32, _i32, _i32, _f32, _f32, _P, _P, _P, _P, _P, _P, _P]),
+    ("moe_block_norm_backward_workspace_size", _size, [_i32, _i32]),
+    ("moe_block_norm_backward", _i32, [_P, _P, _P, _i32, _P, _P, _i32, _P, _i32, _P, _i32, _P, _P, _i32, _i32, _f32, _P, _P,
+                                       _P, _P, _P, _P, _size, _P]),
+    ("moe_layer_workspace_size", _size, [_i32, _i32, _i32]),
+    ("moe_layer", _i32, [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _P,
+                         _P, _P, _P, _size, _P]),
     ("moe_get_status", _i32, [ctypes.POINTER(MoePlanOut), ctypes.POINTER(ctypes.c_int32), _P]),
     ("moe_debug_set_plan_fault", _i32, [_i32, _i64]),
     ("moe_debug_route_sigmoid_error", _i32, [_P, _P]),

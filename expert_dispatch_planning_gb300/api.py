@@ -443,6 +443,74 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor, 
     return r
 
 
+@dataclass(slots=True)
+class BlockNormOut:
+    """Outputs of block_norm (device tensors; q and q_scale None where not asked for)."""
+    y: torch.Tensor
+    residual: torch.Tensor
+    post_rstd: torch.Tensor
+    rstd: torch.Tensor
+    q: torch.Tensor | None
+    q_scale: torch.Tensor | None
+
+
+def block_norm(x: torch.Tensor, residual: torch.Tensor, post_weight: torch.Tensor, weight: torch.Tensor,
+               gate: torch.Tensor | None = None, residual_scale: float = 1.0, eps: float = 1e-6, quantize: bool = False,
+               out: torch.Tensor | None = None, residual_out: torch.Tensor | None = None, q: torch.Tensor | None = None,
+               q_scale: torch.Tensor | None = None, stream=None) -> BlockNormOut:
+    """The norms between two blocks: BlockNormOut(y, residual, post_rstd, rstd, q, q_scale).
+
+    s = residual_scale * residual + gate * norm(x) * post_weight, y = norm(s) *
+    weight, both root-mean-square norms with eps.  x bf16[N,H], a block's
+    output; residual bf16 or float32 [N,H]; post_weight and weight bf16 or
+    float32 [H]; gate float32[N] (one a token), bf16[N,H] or None.
+    BlockNormOut.residual is s in the residual's type (pass
+    residual_out=residual to update it in place); quantize adds the row-scaled
+    8-bit output, as in residual_norm.
+    """
+    r = _lib.binding().block_norm(x, residual, post_weight, weight, gate, residual_scale, eps, bool(quantize), out,
+                                  residual_out, q, q_scale, _handle(stream))
+    if type(r) is int:
+        check("moe_block_norm", r)
+    return BlockNormOut(*r)
+
+
+def block_norm_backward(dy: torch.Tensor, x: torch.Tensor, s: torch.Tensor, post_weight: torch.Tensor,
+                        weight: torch.Tensor, post_rstd: torch.Tensor, rstd: torch.Tensor,
+                        gate: torch.Tensor | None = None, residual_scale: float = 1.0, ds: torch.Tensor | None = None,
+                        stream=None):
+    """Gradients of block_norm: (dx bf16[N,H], dres, dgate, dpost_weight float32[H], dweight float32[H]).
+
+    s is BlockNormOut.residual; ds the gradient that reaches it from the
+    residual stream, in its type, which is dres' type too.  dgate has the
+    gate's type and shape (None without a gate).
+    """
+    r = _lib.binding().block_norm_backward(dy, x, s, post_weight, weight, post_rstd, rstd, gate, residual_scale, ds,
+                                           _handle(stream))
+    if type(r) is int:
+        check("moe_block_norm_backward", r)
+    return r
+
+
+def layer(x: torch.Tensor, logits: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, K: int, scoring="softmax",
+          renormalize: bool = True, bias: torch.Tensor | None = None, n_group: int = 1, topk_group: int = 1,
+          routed_scaling: float = 1.0, x_scale: torch.Tensor | None = None, w_scale: torch.Tensor | None = None,
+          out: torch.Tensor | None = None, topk_idx: torch.Tensor | None = None, topk_w: torch.Tensor | None = None,
+          stream=None) -> torch.Tensor:
+    """A whole layer for up to 64 tokens, from the router's logits to the weighted sum: out bf16[N,H].
+
+    Routing as in route_topk; x, weights and scales as in expert_ffn (bf16, or
+    8-bit rows and gate/up weights with x_scale float32[N] and w_scale
+    float32[E,2,I]).  topk_idx int32[N,K] and topk_w float32[N,K], if given,
+    get the router's choice.
+    """
+    r = _lib.binding().layer(x, logits, w_gate_up, w_down, K, SCORING[scoring], bool(renormalize), bias, n_group, topk_group,
+                             routed_scaling, x_scale, w_scale, out, topk_idx, topk_w, _handle(stream))
+    if type(r) is int:
+        check("moe_layer", r)
+    return r
+
+
 def get_status(p: Plan, stream=None) -> int:
     """Synchronise and return (then clear) the plan's device status code."""
     v = ctypes.c_int32(0)

@@ -1,0 +1,494 @@
+// block_norm.cu -- the norms between two blocks, with the gate and the scaled
+// residual, and their gradient (sm_103a).
+//
+// Forward, for a row x (a block's output) and r (the residual stream):
+//   n = x * rp * wp,  rp = 1 / sqrt(mean(x^2) + eps)   the norm after the block,
+//   s = a r + c n                                      gate c, residual scale a,
+//   v = s * rs * w,   rs = 1 / sqrt(mean(s^2) + eps)   the norm before the next one,
+// v in bf16 and, on request, in 8 bits.  One pass: x, r and the gate come in
+// once, s stays in registers (fp32) between the row's two sums and its maximum.
+//
+// Backward, with sh = s rs, xh = x rp, t = dy w:
+//   d  = rs (t - sh mean(t sh)) + ds      the gradient of s,
+//   dr = a d,  dc = d n,
+//   dx = rp (e - xh mean(e xh)),  e = d c wp,
+//   dw = sum over rows of dy sh,  dwp = sum over rows of d c xh.
+// A row has two sums, the second over what the first one gives; with a gate for
+// each token both the gate's gradient and mean(e xh) come from sum(d n).  The
+// weights' sums stay in registers over a block's rows (a thread keeps its
+// columns); partial rows are joined in block order by a second launch.
+//
+// Forms as in norm.cu: a warp a row (H <= 512), a block a row, and for many
+// rows the ring of rows in shared memory.
+#include "norm_parts.cuh"
+
+namespace moe {
+
+enum Gate { kNoGate = 0, kTokenGate = 1, kFullGate = 2 };
+
+struct BlockNormArgs {
+    const uint16_t* x;
+    const void* residual;
+    const void* gate;  // float32[N] or bf16[N][H]
+    const void* post_weight;
+    const void* weight;
+    int post_f32, weight_f32;
+    int N, H;
+    float alpha, eps;
+    float down, mean;  // of the squares' sums (square_scale)
+    uint16_t* y;
+    void* residual_out;
+    float* post_rstd;
+    float* rstd;
+    uint8_t* q;
+    float* q_scale;
+};
+
+// 1 / sqrt(mean(v^2) + eps) of a row held in registers.
+template <int VPT, bool WARP>
+__device__ __forceinline__ float row_root(const float (&v)[VPT][8], int lane, int lanes, int nvec, const BlockNormArgs& a,
+                                          float* buf) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        if (lane + i * lanes < nvec)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float t = v[i][j] * a.down;
+                ss = fmaf(t, t, ss);
+            }
+    ss = row_reduce<WARP, false>(ss, buf);
+    float root = rsqrtf(fmaf(ss, a.mean, a.eps));  // within 2^-22
+    if (!(fmaf(ss, a.mean, a.eps) >= kLeastEps)) {
+        // Squares may have lost digits below the normal numbers, or vanished, and
+        // eps does not cover them: no value is above 2^-42, all are summed again,
+        // scaled.  (The row's threads hold the same sum and take the same way.)
+        constexpr float kUp = 0x1p90f;
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (lane + i * lanes < nvec)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float t = v[i][j] * kUp;
+                    ss = fmaf(t, t, ss);
+                }
+        ss = row_reduce<WARP, false>(ss, buf) * (a.down * a.down);
+        root = kUp * rsqrtf(fmaf(ss, a.mean, a.eps * kUp * kUp));
+    }
+    return root;
+}
+
+template <int VPT, bool WARP, typename R, int GATE>
+__global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) block_norm_kernel(const BlockNormArgs a) {
+    __shared__ float buf[32];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int lanes = WARP ? 32 : blockDim.x;
+    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= a.N) return;
+    const int nvec = a.H / 8;
+    const int64_t at = row * a.H;
+    const R* residual = static_cast<const R*>(a.residual) + at;
+    const uint16_t* gate = static_cast<const uint16_t*>(a.gate) + at;
+
+    // Everything the row needs is asked for before the first sum is waited for;
+    // the widest rows (VPT 4) have no registers for that.
+    constexpr bool kEarly = VPT <= 2;
+    float s[VPT][8], r[kEarly ? VPT : 1][8], g[kEarly && GATE == kFullGate ? VPT : 1][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * lanes;
+        if (c < nvec) {
+            load8(a.x + at, c, s[i]);
+            if constexpr (kEarly) load8_written(residual, c, r[i]);
+            if constexpr (kEarly && GATE == kFullGate) load8(gate, c, g[i]);
+        }
+    }
+    const float token_gate = GATE == kTokenGate ? __ldg(static_cast<const float*>(a.gate) + row) : 1.f;
+    const float post = row_root<VPT, WARP>(s, lane, lanes, nvec, a, buf);
+    if (lane == 0) a.post_rstd[row] = post;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * lanes;
+        if (c < nvec) {
+            constexpr int kOwn = kEarly ? 1 : 0;  // the place of chunk i: its own, or the only one
+            if constexpr (!kEarly) load8_written(residual, c, r[0]);
+            if constexpr (!kEarly && GATE == kFullGate) load8(gate, c, g[0]);
+            float w[8];
+            load_weight8(a.post_weight, a.post_f32, c, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float n = s[i][j] * post * w[j];
+                if constexpr (GATE == kTokenGate) n *= token_gate;
+                if constexpr (GATE == kFullGate) n *= g[i * kOwn][j];
+                s[i][j] = fmaf(a.alpha, r[i * kOwn][j], n);
+            }
+            store8(static_cast<R*>(a.residual_out) + at, c, s[i]);
+        }
+    }
+    const float rstd = row_root<VPT, WARP>(s, lane, lanes, nvec, a, buf);
+    if (lane == 0) a.rstd[row] = rstd;
+
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * lanes;
+        if (c < nvec) {
+            float w[8];
+            load_weight8(a.weight, a.weight_f32, c, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s[i][j] = s[i][j] * rstd * w[j];
+                amax = fmaxf(amax, fabsf(s[i][j]));
+            }
+            store8(a.y + at, c, s[i]);
+        }
+    }
+    if (a.q == nullptr) return;
+    amax = row_reduce<WARP, true>(amax, buf);
+    const Quantum q = quantum_of(amax);
+    if (lane == 0) a.q_scale[row] = q.scale;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = lane + i * lanes;
+        if (c < nvec)
+            *reinterpret_cast<uint2*>(a.q + at + 8 * static_cast<int64_t>(c)) =
+                make_uint2(q.round4(s[i]), q.round4(s[i] + 4));
+    }
+}
+
+// ---------------------------------------------------------------- backward
+struct BlockNormBackwardArgs {
+    const uint16_t* dy;
+    const uint16_t* x;
+    const void* s;
+    const void* ds;  // may be null
+    const void* gate;
+    const void* post_weight;
+    const void* weight;
+    int post_f32, weight_f32;
+    const float* post_rstd;
+    const float* rstd;
+    int N, H;
+    float alpha;
+    uint16_t* dx;
+    void* dres;
+    void* dgate;  // float32[N] or bf16[N][H]
+    float* partial;  // [gridDim.x][2][H]: dweight's, dpost_weight's
+};
+
+template <int VPT, bool WARP, typename S, int GATE>
+__global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) block_norm_backward_kernel(const BlockNormBackwardArgs a) {
+    extern __shared__ float sh[];  // WARP: [warps][2][H] for the block's sums
+    __shared__ float buf[32];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int lanes = WARP ? 32 : blockDim.x;
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+    const int per_step = WARP ? warps : 1;
+    const int nvec = a.H / 8;
+    const float over_h = 1.f / static_cast<float>(a.H);
+
+    float acc[VPT][8], post_acc[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = post_acc[i][j] = 0.f;
+    // rows of a block are consecutive: its partial sums have a fixed order
+    const int64_t steps = (static_cast<int64_t>(a.N) + per_step - 1) / per_step;
+    const int64_t begin = blockIdx.x * steps / gridDim.x, end = (blockIdx.x + 1) * steps / gridDim.x;
+    for (int64_t step = begin; step < end; ++step) {
+        const int64_t row = WARP ? step * per_step + warp : step;
+        if (row >= a.N) break;
+        const int64_t at = row * a.H;
+        const float rstd = __ldg(a.rstd + row), post = __ldg(a.post_rstd + row);
+        const float token_gate = GATE == kTokenGate ? __ldg(static_cast<const float*>(a.gate) + row) : 1.f;
+        const uint16_t* gate = static_cast<const uint16_t*>(a.gate) + at;
+        float hat[VPT][8], t[VPT][8], d[VPT][8], xh[VPT][8];  // all is asked for before the row's first sum
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * lanes;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[i][j] = 0.f;
+            if (c < nvec) {
+                load8(a.dy + at, c, t[i]);
+                load8(static_cast<const S*>(a.s) + at, c, hat[i]);
+                load8(a.x + at, c, xh[i]);
+                if (a.ds != nullptr) load8(static_cast<const S*>(a.ds) + at, c, d[i]);
+            }
+        }
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * lanes;
+            if (c < nvec) {
+                float w[8];
+                load_weight8(a.weight, a.weight_f32, c, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    hat[i][j] *= rstd;
+                    xh[i][j] *= post;
+                    acc[i][j] = fmaf(t[i][j], hat[i][j], acc[i][j]);
+                    t[i][j] *= w[j];
+                    dot = fmaf(t[i][j], hat[i][j], dot);
+                }
+            }
+        }
+        const float mean = row_reduce<WARP, false>(dot, buf) * over_h;
+        dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * lanes;
+            if (c < nvec) {
+                float w[8], g[8], o[8];
+                load_weight8(a.post_weight, a.post_f32, c, w);
+                if constexpr (GATE == kFullGate) load8(gate, c, g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    d[i][j] += rstd * (t[i][j] - hat[i][j] * mean);
+                    o[j] = a.alpha * d[i][j];
+                }
+                store8(static_cast<S*>(a.dres) + at, c, o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float n = xh[i][j] * w[j];
+                    if constexpr (GATE == kFullGate) {
+                        o[j] = d[i][j] * n;
+                        d[i][j] *= g[j];
+                        dot = fmaf(d[i][j], n, dot);
+                    } else {
+                        dot = fmaf(d[i][j], n, dot);
+                        d[i][j] *= token_gate;
+                    }
+                    post_acc[i][j] = fmaf(d[i][j], xh[i][j], post_acc[i][j]);
+                    d[i][j] *= w[j];
+                }
+                if constexpr (GATE == kFullGate) store8(static_cast<uint16_t*>(a.dgate) + at, c, o);
+            }
+        }
+        dot = row_reduce<WARP, false>(dot, buf);
+        if constexpr (GATE == kTokenGate) {
+            if (lane == 0) static_cast<float*>(a.dgate)[row] = dot;
+            dot *= token_gate;
+        }
+        const float post_mean = dot * over_h;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * lanes;
+            if (c < nvec) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[i][j] = post * (d[i][j] - xh[i][j] * post_mean);
+                store8(a.dx + at, c, d[i]);
+            }
+        }
+    }
+    float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
+    if constexpr (WARP) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * lanes;
+            if (c < nvec) {
+                store8(sh + (2 * warp) * a.H, c, acc[i]);
+                store8(sh + (2 * warp + 1) * a.H, c, post_acc[i]);
+            }
+        }
+        __syncthreads();
+        for (int h = threadIdx.x; h < 2 * a.H; h += blockDim.x) {
+            float v = 0.f;
+            for (int k = 0; k < warps; ++k) v += sh[2 * k * a.H + h];
+            out[h] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = lane + i * lanes;
+            if (c < nvec) {
+                store8(out, c, acc[i]);
+                store8(out + a.H, c, post_acc[i]);
+            }
+        }
+    }
+}
+
+// The weights' gradients from the blocks' partials: 32 columns a block; each
+// of its 32 warps adds every 32nd partial, and the warps' sums are joined in order.
+__global__ void __launch_bounds__(1024) block_norm_weights_kernel(const float* partial, int blocks, int H, float* dweight,
+                                                                  float* dpost) {
+    __shared__ float sh[32][33];
+    pdl_wait();
+    pdl_trigger();
+    const int h = blockIdx.x * 32 + threadIdx.x, g = threadIdx.y;
+    float v = 0.f;
+    if (h < 2 * H) {
+#pragma unroll 4
+        for (int b = g; b < blocks; b += 32) v += partial[static_cast<int64_t>(b) * 2 * H + h];
+    }
+    sh[g][threadIdx.x] = v;
+    __syncthreads();
+    v = warp_sum(sh[threadIdx.x][g]);  // warp g joins column g
+    const int c = blockIdx.x * 32 + g;
+    if (threadIdx.x == 0 && c < 2 * H) (c < H ? dweight[c] : dpost[c - H]) = v;
+}
+
+}  // namespace moe
+
+// ---------------------------------------------------------------- host
+namespace {
+
+using namespace moe_host;
+
+template <int VPT, bool WARP, typename R>
+int launch_gate(const moe::BlockNormArgs& a, int gate, dim3 grid, dim3 block, cudaStream_t stream) {
+    switch (gate) {
+        case moe::kNoGate: return launch(moe::block_norm_kernel<VPT, WARP, R, moe::kNoGate>, grid, block, 0, stream, a);
+        case moe::kTokenGate: return launch(moe::block_norm_kernel<VPT, WARP, R, moe::kTokenGate>, grid, block, 0, stream, a);
+        default: return launch(moe::block_norm_kernel<VPT, WARP, R, moe::kFullGate>, grid, block, 0, stream, a);
+    }
+}
+
+template <int VPT, bool WARP>
+int launch_forward(const moe::BlockNormArgs& a, bool f32, int gate, dim3 grid, dim3 block, cudaStream_t stream) {
+    return f32 ? launch_gate<VPT, WARP, float>(a, gate, grid, block, stream)
+               : launch_gate<VPT, WARP, uint16_t>(a, gate, grid, block, stream);
+}
+
+template <int VPT, bool WARP, typename S>
+int launch_backward_gate(const moe::BlockNormBackwardArgs& a, int gate, dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t stream) {
+    switch (gate) {
+        case moe::kNoGate:
+            return launch(moe::block_norm_backward_kernel<VPT, WARP, S, moe::kNoGate>, grid, block, smem, stream, a);
+        case moe::kTokenGate:
+            return launch(moe::block_norm_backward_kernel<VPT, WARP, S, moe::kTokenGate>, grid, block, smem, stream, a);
+        default: return launch(moe::block_norm_backward_kernel<VPT, WARP, S, moe::kFullGate>, grid, block, smem, stream, a);
+    }
+}
+
+template <int VPT, bool WARP>
+int launch_backward(const moe::BlockNormBackwardArgs& a, bool f32, int gate, dim3 grid, dim3 block, size_t smem,
+                    cudaStream_t stream) {
+    return f32 ? launch_backward_gate<VPT, WARP, float>(a, gate, grid, block, smem, stream)
+               : launch_backward_gate<VPT, WARP, uint16_t>(a, gate, grid, block, smem, stream);
+}
+
+// Blocks of the backward kernel: four an SM, no more than there are rows.
+int backward_blocks(int N, int H) {
+    const int64_t units = H <= 512 ? (static_cast<int64_t>(N) + 3) / 4 : N;
+    const int64_t cap = static_cast<int64_t>(num_sms()) * 4;
+    return static_cast<int>(units < cap ? units : cap);
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A gate is float32[N] or bf16[N][H]; 0: there is none, -1: not a gate.
+int gate_of(const void* gate, int gate_dtype) {
+    if (gate == nullptr) return moe::kNoGate;
+    if (gate_dtype == MOE_DTYPE_F32) return aligned4(gate) ? moe::kTokenGate : -1;
+    if (gate_dtype == MOE_DTYPE_BF16) return aligned16(gate) ? moe::kFullGate : -1;
+    return -1;
+}
+
+}  // namespace
+
+extern "C" MOE_API int moe_block_norm(const uint16_t* x, const void* residual, int residual_dtype, const void* gate,
+                                      int gate_dtype, const void* post_weight, int post_weight_dtype, const void* weight,
+                                      int weight_dtype, int N, int H, float residual_scale, float eps, uint16_t* y,
+                                      void* residual_out, float* post_rstd, float* rstd, uint8_t* q, float* q_scale,
+                                      cudaStream_t stream) {
+    if (N < 0 || H < 8 || H % 8 != 0 || !(eps >= 0.f) || std::isinf(eps) || !std::isfinite(residual_scale))
+        return MOE_ERR_INVALID_ARG;
+    if (!float_type(post_weight_dtype) || !float_type(weight_dtype) || !float_type(residual_dtype))
+        return MOE_ERR_INVALID_ARG;
+    const int kind = gate_of(gate, gate_dtype);
+    if (kind < 0) return MOE_ERR_INVALID_ARG;
+    if (N > 0 && (x == nullptr || residual == nullptr || post_weight == nullptr || weight == nullptr || y == nullptr ||
+                  residual_out == nullptr || post_rstd == nullptr || rstd == nullptr || (q == nullptr) != (q_scale == nullptr)))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(post_weight) || !aligned16(weight) || !aligned16(y) ||
+        !aligned16(residual_out) || !aligned4(post_rstd) || !aligned4(rstd) || !aligned4(q_scale) ||
+        (reinterpret_cast<uintptr_t>(q) & 7u) != 0)
+        return MOE_ERR_INVALID_ARG;
+    if (H > kMaxH) return MOE_ERR_UNSUPPORTED;
+    if (N == 0) return MOE_OK;
+    float down, mean;
+    square_scale(H, &down, &mean);
+    const bool f32 = residual_dtype == MOE_DTYPE_F32;
+    const moe::BlockNormArgs a = {x, residual, gate, post_weight, weight, post_weight_dtype == MOE_DTYPE_F32,
+                                  weight_dtype == MOE_DTYPE_F32, N, H, residual_scale, eps, down, mean, y,
+                                  residual_out, post_rstd, rstd, q, q_scale};
+    if (H <= 512) {
+        const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(N) + 3) / 4)), block(128);
+        return H <= 256 ? launch_forward<1, true>(a, f32, kind, grid, block, stream)
+                        : launch_forward<2, true>(a, f32, kind, grid, block, stream);
+    }
+    const dim3 grid(static_cast<unsigned>(N)), block(static_cast<unsigned>(norm_threads(H)));
+    switch (norm_vpt(H)) {
+        case 1: return launch_forward<1, false>(a, f32, kind, grid, block, stream);
+        case 2: return launch_forward<2, false>(a, f32, kind, grid, block, stream);
+        default: return launch_forward<4, false>(a, f32, kind, grid, block, stream);
+    }
+}
+
+extern "C" MOE_API size_t moe_block_norm_backward_workspace_size(int N, int H) {
+    if (N < 0 || H < 8 || H % 8 != 0 || H > kMaxH) return 0;
+    const int blocks = backward_blocks(N, H);
+    return static_cast<size_t>(blocks > 0 ? blocks : 1) * 2 * H * sizeof(float);
+}
+
+extern "C" MOE_API int moe_block_norm_backward(const uint16_t* dy, const uint16_t* x, const void* s, int s_dtype,
+                                               const void* ds, const void* gate, int gate_dtype, const void* post_weight,
+                                               int post_weight_dtype, const void* weight, int weight_dtype,
+                                               const float* post_rstd, const float* rstd, int N, int H,
+                                               float residual_scale, uint16_t* dx, void* dres, void* dgate,
+                                               float* dpost_weight, float* dweight, void* workspace,
+                                               size_t workspace_bytes, cudaStream_t stream) {
+    if (N < 0 || H < 8 || H % 8 != 0 || !std::isfinite(residual_scale)) return MOE_ERR_INVALID_ARG;
+    if (!float_type(post_weight_dtype) || !float_type(weight_dtype) || !float_type(s_dtype)) return MOE_ERR_INVALID_ARG;
+    const int kind = gate_of(gate, gate_dtype);
+    if (kind < 0 || (gate == nullptr && dgate != nullptr)) return MOE_ERR_INVALID_ARG;
+    if (dweight == nullptr || dpost_weight == nullptr) return MOE_ERR_INVALID_ARG;
+    if (N > 0 && (dy == nullptr || x == nullptr || s == nullptr || post_weight == nullptr || weight == nullptr ||
+                  post_rstd == nullptr || rstd == nullptr || dx == nullptr || dres == nullptr || workspace == nullptr ||
+                  (gate != nullptr) != (dgate != nullptr)))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(s) || !aligned16(ds) || !aligned16(post_weight) ||
+        !aligned16(weight) || !aligned16(dx) || !aligned16(dres) || !aligned16(workspace) || !aligned4(post_rstd) ||
+        !aligned4(rstd) || !aligned4(dweight) || !aligned4(dpost_weight) ||
+        !(kind == moe::kFullGate ? aligned16(dgate) : aligned4(dgate)))
+        return MOE_ERR_INVALID_ARG;
+    if (H > kMaxH) return MOE_ERR_UNSUPPORTED;
+    if (N == 0) {
+        if (cudaMemsetAsync(dweight, 0, sizeof(float) * H, stream) != cudaSuccess ||
+            cudaMemsetAsync(dpost_weight, 0, sizeof(float) * H, stream) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    if (workspace_bytes < moe_block_norm_backward_workspace_size(N, H)) return MOE_ERR_CAPACITY;
+    const bool f32 = s_dtype == MOE_DTYPE_F32;
+    const int blocks = backward_blocks(N, H);
+    float* partial = static_cast<float*>(workspace);
+    const moe::BlockNormBackwardArgs a = {dy, x, s, ds, gate, post_weight, weight, post_weight_dtype == MOE_DTYPE_F32,
+                                          weight_dtype == MOE_DTYPE_F32, post_rstd, rstd, N, H, residual_scale, dx, dres,
+                                          dgate, partial};
+    const dim3 grid(static_cast<unsigned>(blocks));
+    int rc;
+    if (H <= 512) {
+        const dim3 block(128);
+        const size_t smem = 8 * sizeof(float) * H;
+        rc = H <= 256 ? launch_backward<1, true>(a, f32, kind, grid, block, smem, stream)
+                      : launch_backward<2, true>(a, f32, kind, grid, block, smem, stream);
+    } else {
+        const dim3 block(static_cast<unsigned>(norm_threads(H)));
+        switch (norm_vpt(H)) {
+            case 1: rc = launch_backward<1, false>(a, f32, kind, grid, block, 0, stream); break;
+            case 2: rc = launch_backward<2, false>(a, f32, kind, grid, block, 0, stream); break;
+            default: rc = launch_backward<4, false>(a, f32, kind, grid, block, 0, stream); break;
+        }
+    }
+    if (rc != MOE_OK) return rc;
+    return launch(moe::block_norm_weights_kernel, dim3(static_cast<unsigned>((2 * H + 31) / 32)), dim3(32, 32), 0, stream,
+                  static_cast<const float*>(partial), blocks, H, dweight, dpost_weight);
+}

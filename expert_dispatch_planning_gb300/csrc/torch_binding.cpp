@@ -171,6 +171,38 @@ int as_int(int64_t n, const char* name) {
     return static_cast<int>(n);
 }
 
+double number(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw BadArgument();
+    return v;
+}
+
+int integer(PyObject* o, const char* name) {
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) throw BadArgument();
+    if (v < INT32_MIN || v > INT32_MAX) refuse(std::string(name) + " is out of range");
+    return static_cast<int>(v);
+}
+
+// A gate: float32[N], bfloat16[N][H], or none.
+void need_gate(const Tensor& gate, int64_t N, int64_t H, const char* name) {
+    if (!gate.defined()) return;
+    if (gate.dim() == 1) need(gate, kF32, {N}, name);
+    else need(gate, kBf16, {N, H}, name);
+}
+int gate_type(const Tensor& gate) { return gate.defined() && gate.dim() == 1 ? MOE_DTYPE_F32 : MOE_DTYPE_BF16; }
+
+// The scales that 8-bit rows and gate/up weights need, and others refuse.
+void need_scales(ScalarType type, const Tensor& x_scale, int64_t rows, const Tensor& w_scale, int64_t E, int64_t I) {
+    if (type == kE4m3) {
+        if (!x_scale.defined() || !w_scale.defined()) refuse("8-bit rows and weights need x_scale and w_scale");
+        need(x_scale, kF32, {rows}, "x_scale");
+        need(w_scale, kF32, {E, 2, I}, "w_scale");
+    } else if (x_scale.defined() || w_scale.defined()) {
+        refuse("x_scale and w_scale go with 8-bit rows and weights");
+    }
+}
+
 void groups_of(MoePlanOut* plan, PyObject* cu, PyObject* count, PyObject* status, int64_t E) {
     const Tensor c = tensor(cu, "cu_seqlens"), n = tensor(count, "tokens_per_expert"), s = tensor(status, "status");
     if (n.defined() && n.numel() != E)
@@ -300,13 +332,7 @@ PyObject* expert_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const OnStream stream(a[11], x, "x");
         need(wgu, type, {E, 2, I, H}, "w_gate_up");
         need(wd, kBf16, {E, H, I}, "w_down");
-        if (type == kE4m3) {
-            if (!x_scale.defined() || !w_scale.defined()) refuse("8-bit rows and weights need x_scale and w_scale");
-            need(x_scale, kF32, {rows}, "x_scale");
-            need(w_scale, kF32, {E, 2, I}, "w_scale");
-        } else if (x_scale.defined() || w_scale.defined()) {
-            refuse("x_scale and w_scale go with 8-bit rows and weights");
-        }
+        need_scales(type, x_scale, rows, w_scale, E, I);
         MoePlanOut plan = {};
         groups_of(&plan, a[3], a[4], a[5], E);
         const Tensor h = output(tensor(a[8], "h"), {rows, I}, kBf16, x, "h");
@@ -400,11 +426,152 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// block_norm(x, residual, post_weight, weight, gate, residual_scale, eps, quantize, out, residual_out, q, q_scale, stream)
+PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count_is(n, 13)) return nullptr;
+    try {
+        const Tensor x = tensor(a[0], "x"), residual = tensor(a[1], "residual"), post_weight = tensor(a[2], "post_weight"),
+                     weight = tensor(a[3], "weight"), gate = tensor(a[4], "gate");
+        const double alpha = number(a[5]), eps = number(a[6]);
+        const bool quantize = a[7] == Py_True;
+        Tensor q = tensor(a[10], "q"), q_scale = tensor(a[11], "q_scale");
+        need_dims(x, 2, "x");
+        const int64_t N = x.size(0), H = x.size(1);
+        need(x, kBf16, {N, H}, "x");
+        const OnStream stream(a[12], x, "x");
+        need_float(residual, "residual");
+        need(residual, residual.scalar_type(), {N, H}, "residual");
+        need_float(post_weight, "post_weight");
+        need(post_weight, post_weight.scalar_type(), {H}, "post_weight");
+        need_float(weight, "weight");
+        need(weight, weight.scalar_type(), {H}, "weight");
+        need_gate(gate, N, H, "gate");
+        const Tensor y = output(tensor(a[8], "out"), {N, H}, kBf16, x, "out"),
+                     sum = output(tensor(a[9], "residual_out"), {N, H}, residual.scalar_type(), x, "residual_out"),
+                     post_rstd = empty({N}, kF32, x), rstd = empty({N}, kF32, x);
+        if (quantize) {
+            q = output(q, {N, H}, kE4m3, x, "q");
+            q_scale = output(q_scale, {N}, kF32, x, "q_scale");
+        } else if (q.defined() || q_scale.defined()) {
+            refuse("q and q_scale need quantize=True");
+        }
+        const int rc = moe_block_norm(ptr<uint16_t>(x), ptr<>(residual), dtype_of(residual), ptr<>(gate), gate_type(gate),
+                                      ptr<>(post_weight), dtype_of(post_weight), ptr<>(weight), dtype_of(weight),
+                                      as_int(N, "N"), as_int(H, "H"), static_cast<float>(alpha), static_cast<float>(eps),
+                                      ptr<uint16_t>(y), ptr<>(sum), ptr<float>(post_rstd), ptr<float>(rstd),
+                                      ptr<uint8_t>(q), ptr<float>(q_scale), stream.handle());
+        stream.hand_over(y, a[8]);
+        stream.hand_over(sum, a[9]);
+        stream.hand_over(post_rstd, Py_None);
+        stream.hand_over(rstd, Py_None);
+        stream.hand_over(q, a[10]);
+        stream.hand_over(q_scale, a[11]);
+        return rc != MOE_OK ? PyLong_FromLong(rc) : wrap({y, sum, post_rstd, rstd, q, q_scale});
+    } catch (const BadArgument&) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// block_norm_backward(dy, x, s, post_weight, weight, post_rstd, rstd, gate, residual_scale, ds, stream)
+PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count_is(n, 11)) return nullptr;
+    try {
+        const Tensor dy = tensor(a[0], "dy"), x = tensor(a[1], "x"), s = tensor(a[2], "s"),
+                     post_weight = tensor(a[3], "post_weight"), weight = tensor(a[4], "weight"),
+                     post_rstd = tensor(a[5], "post_rstd"), rstd = tensor(a[6], "rstd"), gate = tensor(a[7], "gate"),
+                     ds = tensor(a[9], "ds");
+        const double alpha = number(a[8]);
+        need_dims(dy, 2, "dy");
+        const int64_t N = dy.size(0), H = dy.size(1);
+        need(dy, kBf16, {N, H}, "dy");
+        const OnStream stream(a[10], dy, "dy");
+        need(x, kBf16, {N, H}, "x");
+        need_float(s, "s");
+        need(s, s.scalar_type(), {N, H}, "s");
+        need_float(post_weight, "post_weight");
+        need(post_weight, post_weight.scalar_type(), {H}, "post_weight");
+        need_float(weight, "weight");
+        need(weight, weight.scalar_type(), {H}, "weight");
+        need(post_rstd, kF32, {N}, "post_rstd");
+        need(rstd, kF32, {N}, "rstd");
+        need_gate(gate, N, H, "gate");
+        if (ds.defined()) need(ds, s.scalar_type(), {N, H}, "ds");
+        Tensor dgate;
+        if (gate.defined()) dgate = gate.dim() == 1 ? empty({N}, kF32, dy) : empty({N, H}, kBf16, dy);
+        const Tensor dx = empty({N, H}, kBf16, dy), dres = empty({N, H}, s.scalar_type(), dy),
+                     dpost = empty({H}, kF32, dy), dweight = empty({H}, kF32, dy);
+        const int64_t bytes = static_cast<int64_t>(moe_block_norm_backward_workspace_size(as_int(N, "N"), as_int(H, "H")));
+        const Tensor ws = empty({bytes}, at::kByte, dy);
+        const int rc = moe_block_norm_backward(
+            ptr<uint16_t>(dy), ptr<uint16_t>(x), ptr<>(s), dtype_of(s), ptr<>(ds), ptr<>(gate), gate_type(gate),
+            ptr<>(post_weight), dtype_of(post_weight), ptr<>(weight), dtype_of(weight), ptr<float>(post_rstd),
+            ptr<float>(rstd), static_cast<int>(N), static_cast<int>(H), static_cast<float>(alpha), ptr<uint16_t>(dx),
+            ptr<>(dres), ptr<>(dgate), ptr<float>(dpost), ptr<float>(dweight), ptr<>(ws), static_cast<size_t>(bytes),
+            stream.handle());
+        for (const Tensor& t : {dx, dres, dgate, dpost, dweight}) stream.hand_over(t, Py_None);
+        return rc != MOE_OK ? PyLong_FromLong(rc) : wrap({dx, dres, dgate, dpost, dweight});
+    } catch (const BadArgument&) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// layer(x, logits, w_gate_up, w_down, K, scoring, renormalize, bias, n_group, topk_group, routed_scaling, x_scale, w_scale,
+//       out, topk_idx, topk_w, stream)
+PyObject* layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count_is(n, 17)) return nullptr;
+    try {
+        const Tensor x = tensor(a[0], "x"), logits = tensor(a[1], "logits"), wgu = tensor(a[2], "w_gate_up"),
+                     wd = tensor(a[3], "w_down"), bias = tensor(a[7], "bias"), x_scale = tensor(a[11], "x_scale"),
+                     w_scale = tensor(a[12], "w_scale"), idx = tensor(a[14], "topk_idx"), w = tensor(a[15], "topk_w");
+        const int K = integer(a[4], "K"), scoring = integer(a[5], "scoring"), n_group = integer(a[8], "n_group"),
+                  topk_group = integer(a[9], "topk_group");
+        const bool renormalize = a[6] == Py_True;
+        const double scaling = number(a[10]);
+        need_dims(x, 2, "x");
+        need_dims(wgu, 4, "w_gate_up");
+        const int64_t N = x.size(0), H = x.size(1), E = wgu.size(0), I = wgu.size(2);
+        const ScalarType type = x.scalar_type();
+        if (type != kBf16 && type != kE4m3)
+            refuse(std::string("x must be bfloat16 or float8_e4m3fn (got ") + name_of(type) + ")");
+        need(x, type, {N, H}, "x");
+        const OnStream stream(a[16], x, "x");
+        need(logits, kF32, {N, E}, "logits");
+        if (bias.defined()) need(bias, kF32, {E}, "bias");
+        need(wgu, type, {E, 2, I, H}, "w_gate_up");
+        need(wd, kBf16, {E, H, I}, "w_down");
+        need_scales(type, x_scale, N, w_scale, E, I);
+        if (idx.defined()) need(idx, kI32, {N, K}, "topk_idx");
+        if (w.defined()) need(w, kF32, {N, K}, "topk_w");
+        if (N > MOE_LAYER_MAX_TOKENS)
+            refuse("at most " + std::to_string(MOE_LAYER_MAX_TOKENS) + " tokens (got " + std::to_string(N) +
+                   "): plan, permute, expert_ffn and combine serve more");
+        const Tensor y = output(tensor(a[13], "out"), {N, H}, kBf16, x, "out");
+        const int64_t bytes = static_cast<int64_t>(moe_layer_workspace_size(static_cast<int>(N), K, as_int(I, "I")));
+        const Tensor ws = empty({bytes}, at::kByte, x);
+        const int rc = moe_layer(ptr<>(x), ptr<float>(x_scale), ptr<float>(logits), ptr<float>(bias), ptr<>(wgu),
+                                 ptr<float>(w_scale), ptr<uint16_t>(wd), static_cast<int>(N), as_int(E, "E"),
+                                 as_int(H, "H"), static_cast<int>(I), K, dtype_of(x), scoring, renormalize, n_group,
+                                 topk_group, static_cast<float>(scaling), ptr<int32_t>(idx), ptr<float>(w),
+                                 ptr<uint16_t>(y), ptr<>(ws), static_cast<size_t>(bytes), stream.handle());
+        stream.hand_over(y, a[13]);
+        return rc != MOE_OK ? PyLong_FromLong(rc) : wrap(y);
+    } catch (const BadArgument&) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
 #define MOE_ENTRY(f) \
     { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr }
 
 PyMethodDef methods[] = {MOE_ENTRY(residual_norm),       MOE_ENTRY(residual_norm_backward), MOE_ENTRY(expert_ffn),
-                         MOE_ENTRY(expert_ffn_backward), MOE_ENTRY(combine_backward),       {nullptr, nullptr, 0, nullptr}};
+                         MOE_ENTRY(expert_ffn_backward), MOE_ENTRY(combine_backward),       MOE_ENTRY(block_norm),
+                         MOE_ENTRY(block_norm_backward), MOE_ENTRY(layer),                  {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

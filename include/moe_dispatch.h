@@ -455,6 +455,68 @@ MOE_API int moe_residual_norm_backward(const uint16_t* dy, const void* s, int s_
                                        size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * The norms between two blocks, with the gate and the scaled residual.  Row by
+ * row, in fp32, for a block's output x and the residual stream:
+ *   n = x * post_rstd * post_weight,  post_rstd = 1 / sqrt(mean(x^2) + eps),
+ *   s = residual_scale * residual + gate * n,
+ *   v = s * rstd * weight,  rstd = 1 / sqrt(mean(s^2) + eps),
+ *   residual_out = s,  y = bf16(v),  q_scale and q from v as in moe_residual_norm.
+ * v is taken from the unrounded s, and q from the unrounded v.  Means of
+ * squares as in moe_residual_norm.
+ *   x            (device) bf16[N][H]; H % 8 == 0; every row array 16-byte aligned.
+ *   residual     (device) [N][H] of residual_dtype (MOE_DTYPE_BF16 or _F32).
+ *   gate         (device) float32[N] (gate_dtype MOE_DTYPE_F32: one a token),
+ *                bf16[N][H] (MOE_DTYPE_BF16: one an element), or NULL: 1.
+ *   post_weight, (device) [H] of their dtypes (MOE_DTYPE_BF16 or _F32), 16-byte
+ *   weight       aligned.
+ *   y            (device) bf16[N][H] out.
+ *   residual_out (device) [N][H] of residual_dtype out; may be residual itself.
+ *   post_rstd,   (device) float32[N] out.
+ *   rstd
+ *   q, q_scale   (device) e4m3[N][H] (8-byte aligned) and float32[N] out, both
+ *                or neither.
+ * eps >= 0 and finite, residual_scale finite, H <= 32768.  N = 0 launches
+ * nothing.  One launch.
+ */
+MOE_API int moe_block_norm(const uint16_t* x, const void* residual, int residual_dtype, const void* gate,
+                           int gate_dtype, const void* post_weight, int post_weight_dtype, const void* weight,
+                           int weight_dtype, int N, int H, float residual_scale, float eps, uint16_t* y,
+                           void* residual_out, float* post_rstd, float* rstd, uint8_t* q, float* q_scale,
+                           cudaStream_t stream);
+
+/*
+ * Gradient of moe_block_norm.  With sh = s * rstd, xh = x * post_rstd, t = dy * weight:
+ *   d = rstd * (t - sh * mean(t * sh)) + ds,
+ *   dres = residual_scale * d,  dgate = d * xh * post_weight (for a gate a
+ *   token: its sum over the row),
+ *   e = d * gate * post_weight,  dx = post_rstd * (e - xh * mean(e * xh)),
+ *   dweight = sum over the rows of dy * sh,
+ *   dpost_weight = sum over the rows of d * gate * xh.
+ *   dy           (device) bf16[N][H], gradient of y.
+ *   x, gate, post_weight, weight, residual_scale: as in the forward call.
+ *   s            (device) [N][H] of s_dtype (MOE_DTYPE_BF16 or _F32): its residual_out.
+ *   post_rstd,   (device) float32[N] from the forward call.
+ *   rstd
+ *   ds           (device) [N][H] of s_dtype, the gradient that reaches s from
+ *                elsewhere (the residual stream), or NULL.
+ *   dx           (device) bf16[N][H] out.
+ *   dres         (device) [N][H] of s_dtype out.
+ *   dgate        (device) out, of the gate's type and shape; NULL without a gate.
+ *   dpost_weight, (device) float32[H] out.  Summed in a fixed order.
+ *   dweight
+ *   workspace    (device) moe_block_norm_backward_workspace_size(N, H) bytes,
+ *                16-byte aligned, no initialisation.
+ * Two launches.  N = 0 zeroes the weights' gradients.
+ */
+MOE_API size_t moe_block_norm_backward_workspace_size(int N, int H);
+MOE_API int moe_block_norm_backward(const uint16_t* dy, const uint16_t* x, const void* s, int s_dtype, const void* ds,
+                                    const void* gate, int gate_dtype, const void* post_weight, int post_weight_dtype,
+                                    const void* weight, int weight_dtype, const float* post_rstd, const float* rstd,
+                                    int N, int H, float residual_scale, uint16_t* dx, void* dres, void* dgate,
+                                    float* dpost_weight, float* dweight, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
+/*
  * The experts' gated feed-forward over a plan's permuted rows.  For a row m
  * of expert e's group, [cu_seqlens[e], cu_seqlens[e] + tokens_per_expert[e]):
  *   g = x[m] . w_gate[e]^T,  u = x[m] . w_up[e]^T,
@@ -530,6 +592,36 @@ MOE_API int moe_expert_ffn_backward(const uint16_t* dy, const uint16_t* x, const
 MOE_API int moe_combine_backward(const uint16_t* dout, const uint16_t* y, const float* topk_w, int N, int K,
                                  int H, int E, int64_t rows, const MoePlanOut* plan, uint16_t* dy,
                                  float* dw, cudaStream_t stream);
+
+/*
+ * A whole layer for a few tokens: moe_route_topk's choice and, for every pair
+ * (s, k) with e = topk_idx[s][k],
+ *   g = x[s] . w_gate[e]^T,  u = x[s] . w_up[e]^T,  h = bf16(silu(g) * u),
+ *   out[s] = bf16(sum over k of topk_w[s][k] * (h . w_down[e]^T)),
+ * products and the sum over k accumulated in fp32, silu(g) = g / (1 + e^-g).
+ * No plan, permuted rows or padding; weights of experts that no token chose
+ * are not read.
+ *   x          (device) [N][H]: bf16, or e4m3 with x_scale; x_dtype says which.
+ *   x_scale    (device) float32[N] with e4m3: x[s] stands for x[s] * x_scale[s]; else NULL.
+ *   logits, bias, K, scoring, renormalize, n_group, topk_group, routed_scaling:
+ *              as in moe_route_topk.
+ *   w_gate_up, w_scale, w_down: as in moe_expert_ffn.
+ *   topk_idx   (device) int32[N][K] and
+ *   topk_w     float32[N][K]: the router's outputs, or NULL if not wanted.
+ *   out        (device) bf16[N][H] out; must not alias x.
+ *   workspace  (device) moe_layer_workspace_size(N, K, I) bytes, 16-byte aligned, no
+ *              initialisation; one call at a time.
+ * N <= MOE_LAYER_MAX_TOKENS (more: MOE_ERR_UNSUPPORTED; plan, permute, expert_ffn and
+ * combine serve those).  H % 8 == 0 (H % 16 == 0 with e4m3), I % 8 == 0, H and I < 2^20;
+ * 16-byte aligned arrays.  Three launches; N = 0 launches nothing.
+ */
+#define MOE_LAYER_MAX_TOKENS 64
+MOE_API size_t moe_layer_workspace_size(int N, int K, int I);
+MOE_API int moe_layer(const void* x, const float* x_scale, const float* logits, const float* bias,
+                      const void* w_gate_up, const float* w_scale, const uint16_t* w_down, int N, int E, int H, int I,
+                      int K, int x_dtype, int scoring, int renormalize, int n_group, int topk_group,
+                      float routed_scaling, int32_t* topk_idx, float* topk_w, uint16_t* out, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------- status */
 /*
