@@ -53,14 +53,15 @@ struct Chosen {
     unsigned long long* tokens;  // [E] sets of tokens
     int* expert;                 // [slots]
     int* begin;                  // [slots + 1]
-    int* sums;                   // [warps + 1] of the scan
+    int* sums;                   // [warps] of the scan
     float* weight;               // [N*K]
+    uint16_t* place;             // [E] a chosen expert's place
     uint8_t* token;              // [N*K]
     int count;
 
     static __host__ __device__ int slots(int N, int K, int E) { return N * K < E ? N * K : E; }
     static __host__ __device__ size_t bytes(int N, int K, int E) {
-        const size_t s = 8 * static_cast<size_t>(E) + 4 * (2 * slots(N, K, E) + 1) + 4 * (kLayerWarps + 1) + 5 * N * K;
+        const size_t s = 8 * static_cast<size_t>(E) + 4 * (2 * slots(N, K, E) + 1) + 4 * kLayerWarps + 4 * N * K + 2 * E + N * K;
         return (s + 15) / 16 * 16;
     }
     __device__ Chosen(uint8_t* smem, const LayerArgs& a) {
@@ -69,21 +70,37 @@ struct Chosen {
         expert = reinterpret_cast<int*>(tokens + a.E);
         begin = expert + n;
         sums = begin + n + 1;
-        weight = reinterpret_cast<float*>(sums + kLayerWarps + 1);
-        token = reinterpret_cast<uint8_t*>(weight + a.N * a.K);
+        weight = reinterpret_cast<float*>(sums + kLayerWarps);
+        place = reinterpret_cast<uint16_t*>(weight + a.N * a.K);
+        token = reinterpret_cast<uint8_t*>(place + a.E);
     }
     __device__ int size(int i) const { return begin[i + 1] - begin[i]; }
 
+    // Reads topk_idx and topk_w once; `clear` comes before.
+    __device__ void clear(const LayerArgs& a) {
+        for (int e = threadIdx.x; e < a.E; e += kLayerThreads) tokens[e] = 0;
+        __syncthreads();
+    }
     __device__ void find(const LayerArgs& a) {
+        constexpr int kMost = MOE_LAYER_MAX_TOKENS * 32 / kLayerThreads;  // pairs a thread
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pairs = a.N * a.K;
-        for (int e = tid; e < a.E; e += kLayerThreads) tokens[e] = 0;
-        __syncthreads();
-        for (int f = tid; f < pairs; f += kLayerThreads) {
-            const int e = a.topk_idx[f];
-            if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicOr(&tokens[e], 1ull << (f / a.K));
+        int e_of[kMost];
+        float w_of[kMost];
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            const int f = tid + i * kLayerThreads;
+            e_of[i] = -1;
+            if (f < pairs) {
+                e_of[i] = a.topk_idx[f];
+                w_of[i] = a.topk_w[f];
+            }
         }
+#pragma unroll
+        for (int i = 0; i < kMost; ++i)
+            if (static_cast<unsigned>(e_of[i]) < static_cast<unsigned>(a.E))
+                atomicOr(&tokens[e_of[i]], 1ull << ((tid + i * kLayerThreads) / a.K));
         __syncthreads();
-        // a thread has a run of experts: counts of chosen ones and of pairs before it, in one word
+        // a thread has a run of experts: chosen ones and pairs before it, in one word
         const int per = (a.E + kLayerThreads - 1) / kLayerThreads, e0 = tid * per;
         int mine = 0;
         for (int e = e0; e < e0 + per && e < a.E; ++e)
@@ -104,31 +121,25 @@ struct Chosen {
             all += sums[w];
         }
         count = all >> 16;
-        int place = before >> 16, at = before & 0xffff;
+        int i = before >> 16, at = before & 0xffff;
         for (int e = e0; e < e0 + per && e < a.E; ++e) {
             if (tokens[e] == 0) continue;
-            expert[place] = e;
-            begin[place] = at;
-            ++place;
+            expert[i] = e;
+            begin[i] = at;
+            place[e] = static_cast<uint16_t>(i);
+            ++i;
             at += __popcll(tokens[e]);
         }
         if (tid == 0) begin[count] = all & 0xffff;
         __syncthreads();
-        for (int i = warp; i < count; i += kLayerWarps) {  // a warp an expert, a lane a token (and its 32nd next)
-            const unsigned long long set = tokens[expert[i]];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int s = lane + 32 * half;
-                if (s < a.N && (set >> s & 1) != 0) {
-                    const int p = begin[i] + __popcll(set & ((1ull << s) - 1));
-                    token[p] = static_cast<uint8_t>(s);
-                    float w = 0.f;
-                    for (int k = 0; k < a.K; ++k)
-                        if (a.topk_idx[s * a.K + k] == expert[i]) w = a.topk_w[s * a.K + k];
-                    weight[p] = w;
-                }
+        for (int v = 0; v < kMost; ++v)
+            if (static_cast<unsigned>(e_of[v]) < static_cast<unsigned>(a.E)) {
+                const int s = (tid + v * kLayerThreads) / a.K;
+                const int p = begin[place[e_of[v]]] + __popcll(tokens[e_of[v]] & ((1ull << s) - 1));
+                token[p] = static_cast<uint8_t>(s);
+                weight[p] = w_of[v];
             }
-        }
         __syncthreads();
     }
 };
@@ -188,39 +199,124 @@ __device__ __forceinline__ uint4 load16(const uint8_t* p, bool inside) {
         asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ uint4 stream16(const uint8_t* p, bool inside) {
-    return inside ? ld_stream_v4(p) : make_uint4(0, 0, 0, 0);
-}
+// A warp's ring of weight steps in shared memory, filled by its own copies (cp.async): no
+// other warp waits for it, and it runs on over the ends of tiles and experts, so that memory
+// is kept busy while the warps join their sums.  A step is kStepBytes of each of the warp's MT
+// sixteens of rows.  Eight lanes copy a row's 128 bytes, a whole line (with the four lanes a
+// row that a fragment has, 64 bytes of eight rows, memory gave a third less).
+constexpr int kStepBytes = 128;
+constexpr int kPieces = 2;  // of 64 bytes: what a fragment has of a row
 
-// acc += rows times tokens over the lane's 16-byte blocks first .. last of k
-// (64 bytes of a row each).  lo, hi: the lane's two weight rows, null where there is
-// none; col[j]: its token's row in the j-th eight, null where there is none.
-// bytes: a row's length.
-template <bool Q, int NT>
-__device__ __forceinline__ void stream_rows(float (&acc)[NT][4], const uint8_t* lo, const uint8_t* hi,
-                                            const uint8_t* const (&col)[NT], int first, int last, int bytes, int t) {
-    constexpr int U = 4;  // blocks asked for at a time
-    for (int b = first; b < last; b += U) {
-        uint4 wl[U], wh[U];
+// Rows of one tile: MT times two eights; eight h of sixteen m begins at first + m * tile + h * half.
+struct WeightRows {
+    const uint8_t* first;
+    int64_t row, half, tile;  // bytes from one to the next
+    int n;                    // rows that are there: of each half (gate and up), or of all
+};
+
+template <int MT, bool HALVES, int DEPTH>  // HALVES: n counts the rows of each half
+struct WeightRing {
+    static constexpr int kStep = MT * 16 * kStepBytes;
+    static constexpr int kDepth = DEPTH;
+    static constexpr int kWarpBytes = DEPTH * kStep;
+    const uint32_t mine;
+    int slot = 0;  // the step's that is read next
+    __device__ explicit WeightRing(const uint8_t* smem) : mine(smem_addr(smem) + (threadIdx.x >> 5) * kWarpBytes) {}
+    // 16-byte chunk `chunk` of row `row` of eight `e`: odd rows are turned by half a row, so that
+    // the eight lanes of a read, two rows' four chunks, are in different banks.
+    static __device__ __forceinline__ int place(int e, int row, int chunk) {
+        return (e * 8 + row) * kStepBytes + (chunk ^ (row & 1) << 2) * 16;
+    }
+    // The step at byte `at` of the rows; zeros behind a row's end (`bytes`) and for rows that are not there.
+    __device__ __forceinline__ void fetch(int ahead, const WeightRows& w, int at, int bytes) const {
+        const int s = slot + ahead, r = (threadIdx.x & 31) >> 3, chunk = threadIdx.x & 7, k = at + chunk * 16;
+        const uint32_t to = mine + (s >= DEPTH ? s - DEPTH : s) * kStep;
+        __syncwarp();  // all lanes have read what was there
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int at = (b + i) * 64 + t * 16;
-            const bool in = b + i < last && at < bytes;
-            wl[i] = stream16(lo + at, in && lo != nullptr);
-            wh[i] = stream16(hi + at, in && hi != nullptr);
-        }
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int at = (b + i) * 64 + t * 16;
-            const bool in = b + i < last && at < bytes;
-            uint4 xs[NT];
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) xs[j] = load16(col[j] + at, in && col[j] != nullptr);
-            const Fragment<Q> fl(wl[i]), fh(wh[i]);
+                for (int i = 0; i < 2; ++i) {
+                    const int row = 4 * i + r;
+                    const bool in = (HALVES ? 8 * m : 16 * m + 8 * half) + row < w.n && k < bytes;
+                    const uint8_t* from = w.first + m * w.tile + half * w.half + row * w.row + k;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + place(2 * m + half, row, chunk)),
+                                 "l"(in ? from : w.first), "r"(in ? 16 : 0)
+                                 : "memory");
+                }
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    static __device__ __forceinline__ void wait() {
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+        __syncwarp();
+    }
+    // The lane's piece p of its row (g) of an eight.
+    __device__ __forceinline__ uint4 read(int m, int half, int p) const {
+        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(mine + slot * kStep + place(2 * m + half, g, 4 * p + t))
+                     : "memory");
+        return v;
+    }
+    __device__ __forceinline__ void next() { slot = slot + 1 == DEPTH ? 0 : slot + 1; }
+};
+
+constexpr int kEights = 2;             // of tokens that a pass over a tile's weights takes
+constexpr int kPass = 8 * kEights;
+
+// The lane's token rows for the steps of a pass: both pieces of its token in each eight, asked
+// for a step ahead.  A row that is not there is null and gives zeros.
+struct Tokens {
+    const uint8_t* row[kEights];
+    uint4 v[kPieces][kEights];
+    bool more;  // a second eight
+    __device__ __forceinline__ void rows(const Chosen& c, int expert, int pass, const uint8_t* base, bool by_place,
+                                         int64_t bytes) {
+        const int first = c.begin[expert] + pass * kPass, cols = c.begin[expert + 1] - first;
+        more = cols > 8;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) product<Q>(acc[j], fl, fh, Fragment<Q>(xs[j]));
+        for (int j = 0; j < kEights; ++j) {
+            const int p = 8 * j + ((threadIdx.x & 31) >> 2);
+            row[j] = nullptr;
+            if (p < cols) row[j] = base + (by_place ? first + p : c.token[first + p]) * bytes + (threadIdx.x & 3) * 16;
         }
     }
+    __device__ __forceinline__ void load(int step, int bytes) {
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            const int at = step * kStepBytes + 64 * p;
+            const bool in = at + static_cast<int>(threadIdx.x & 3) * 16 < bytes;
+            v[p][0] = load16(row[0] + at, in && row[0] != nullptr);
+            if (more) v[p][1] = load16(row[1] + at, in && row[1] != nullptr);
+        }
+    }
+};
+
+// One step: acc += the step's weight rows times tokens.
+template <bool Q, int MT, typename Ring>
+__device__ __forceinline__ void multiply(float (&acc)[MT][kEights][4], const Ring& ring, const uint4 (&v)[kPieces][kEights],
+                                         bool more) {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+        const Fragment<Q> b0(v[p][0]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const Fragment<Q> lo(ring.read(m, 0, p)), hi(ring.read(m, 1, p));
+            product<Q>(acc[m][0], lo, hi, b0);
+            if (more) product<Q>(acc[m][1], lo, hi, Fragment<Q>(v[p][1]));
+        }
+    }
+}
+
+template <int MT>
+__device__ __forceinline__ void zero(float (&acc)[MT][kEights][4]) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < kEights; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
 }
 
 // ---------------------------------------------------------------- gate and up
@@ -229,167 +325,335 @@ __device__ __forceinline__ float silu(float g) {
     return g * __fdiv_rn(g >= 0.f ? 1.f : e, 1.f + e);
 }
 
-// Up to eight channels of one expert: gate rows as the instruction's first
-// eight rows, up rows as its others, so that a lane ends with both; the block's warps
-// share k.  `sum`: [warps][NT][32] float4.
-template <bool Q, int NT>
-__device__ __forceinline__ void gate_up_tile(const LayerArgs& a, const Chosen& c, float4* sum, int i, int channel,
-                                             int channels) {
-    constexpr int kSize = Q ? 1 : 2;
+constexpr int kGateUpTiles = 2;  // eights of channels in a tile
+constexpr int kGateUpChannels = 8 * kGateUpTiles;
+using GateUpRing = WeightRing<kGateUpTiles, true, 3>;
+
+// A walk over a block's run of the chosen experts' channels: tile by tile (channels of one
+// expert), pass by pass (sixteen of its tokens; the passes after the first find the tile's
+// weights in L2), and over the warp's steps of k.
+struct GateUpWalk {
+    int64_t at, end;
+    int expert, channel, n;  // the tile at hand: its place among the chosen, first channel, channels
+    int pass, passes, step;
+    __device__ void tile(const Chosen& c, int I) {
+        pass = 0;
+        passes = 0;
+        if (at >= end) return;
+        expert = static_cast<int>(at / I);
+        channel = static_cast<int>(at - static_cast<int64_t>(expert) * I);
+        n = I - channel < kGateUpChannels ? I - channel : kGateUpChannels;
+        if (end - at < n) n = static_cast<int>(end - at);
+        passes = (c.size(expert) + kPass - 1) / kPass;
+    }
+    // To the next pass or tile; whether there is one.
+    __device__ bool next(const Chosen& c, int I) {
+        if (++pass < passes) return true;
+        at += n;
+        tile(c, I);
+        return at < end;
+    }
+};
+
+// The warp's steps are kLayerWarps apart: what the block's warps ask for at one time is contiguous.
+template <bool Q>
+struct GateUpWeights {
+    GateUpWalk walk;
+    WeightRows w;
+    __device__ void rows(const LayerArgs& a, const Chosen& c) {
+        if (walk.at >= walk.end) return;
+        w.row = static_cast<int64_t>(a.H) * (Q ? 1 : 2);
+        w.half = a.I * w.row;
+        w.tile = 8 * w.row;
+        w.n = walk.n;
+        w.first = static_cast<const uint8_t*>(a.w_gate_up) +
+                  (static_cast<int64_t>(c.expert[walk.expert]) * 2 * a.I + walk.channel) * w.row;
+    }
+    __device__ __forceinline__ void fetch(const LayerArgs& a, const Chosen& c, const GateUpRing& ring, int ahead, int warp,
+                                          int steps) {
+        if (walk.at < walk.end && warp < steps) {
+            ring.fetch(ahead, w, walk.step * kStepBytes, a.H * (Q ? 1 : 2));
+            if ((walk.step += kLayerWarps) >= steps) {
+                walk.step = warp;
+                walk.next(c, a.I);
+                rows(a, c);
+            }
+        }
+        GateUpRing::commit();
+    }
+};
+
+// The parts of a tile's pass are joined over the block's warps in `sum` ([warps][kGateUpTiles][32]),
+// one eight of tokens after the other; warp m joins eight m of the channels.
+template <bool Q>
+__device__ __forceinline__ void gate_up_join(const LayerArgs& a, const Chosen& c, float4* sum, const GateUpWalk& walk,
+                                             const float (&acc)[kGateUpTiles][kEights][4]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int e = c.expert[i], first_pair = c.begin[i], cols = c.begin[i + 1] - first_pair;
-    const int64_t row_bytes = static_cast<int64_t>(a.H) * kSize;
-    const uint8_t* w = static_cast<const uint8_t*>(a.w_gate_up);
-    const uint8_t *lo = nullptr, *hi = nullptr;
-    if (g < channels) {
-        const int64_t r = (static_cast<int64_t>(e) * 2 * a.I + channel + g) * row_bytes;
-        lo = w + r;
-        hi = w + r + a.I * row_bytes;
-    }
-    const uint8_t* col[NT];
-    float acc[NT][4];
+    const int e = c.expert[walk.expert], first = c.begin[walk.expert] + walk.pass * kPass,
+              cols = c.begin[walk.expert + 1] - first;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int p = 8 * j + g;
-        col[j] = p < cols ? static_cast<const uint8_t*>(a.x) + c.token[first_pair + p] * row_bytes : nullptr;
-        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-    }
-    const int bytes = static_cast<int>(row_bytes), blocks = (bytes + 63) / 64;
-    stream_rows<Q, NT>(acc, lo, hi, col, warp * blocks / kLayerWarps, (warp + 1) * blocks / kLayerWarps, bytes, t);
+    for (int j = 0; j < kEights; ++j) {
+        if (8 * j >= cols) break;
+        __syncthreads();  // the sums before are taken
 #pragma unroll
-    for (int j = 0; j < NT; ++j) sum[(warp * NT + j) * 32 + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-    __syncthreads();
-    for (int v = threadIdx.x; v < NT * 32; v += kLayerThreads) {
-        float4 s = sum[v];
+        for (int m = 0; m < kGateUpTiles; ++m)
+            sum[(warp * kGateUpTiles + m) * 32 + lane] = make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
+        __syncthreads();
+        if (warp >= kGateUpTiles) continue;
+        float4 s = sum[warp * 32 + lane];
 #pragma unroll
         for (int k = 1; k < kLayerWarps; ++k) {
-            const float4 o = sum[k * NT * 32 + v];
+            const float4 o = sum[(k * kGateUpTiles + warp) * 32 + lane];
             s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
         }
-        const int row = (v & 31) >> 2, p = 8 * (v >> 5) + 2 * (v & 3);
-        if (row < channels) {
-            const int ch = channel + row;
-            float wg = 1.f, wu = 1.f;
-            if constexpr (Q) {
-                wg = __ldg(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + ch);
-                wu = __ldg(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + a.I + ch);
-            }
+        const int row = 8 * warp + g, ch = walk.channel + row;
+        if (row >= walk.n) continue;
+        float wg = 1.f, wu = 1.f;
+        if constexpr (Q) {
+            wg = __ldg(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + ch);
+            wu = __ldg(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + a.I + ch);
+        }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (p + j >= cols) continue;
-                float gate = j == 0 ? s.x : s.y, up = j == 0 ? s.z : s.w;
-                if constexpr (Q) {
-                    const float xs = __ldg(a.x_scale + c.token[first_pair + p + j]);
-                    gate = gate * wg * xs;
-                    up = up * wu * xs;
-                }
-                const __nv_bfloat16 h = __float2bfloat16_rn(silu(gate) * up);
-                a.h[static_cast<int64_t>(first_pair + p + j) * a.I + ch] = __bfloat16_as_ushort(h);
+        for (int v = 0; v < 2; ++v) {
+            const int p = 8 * j + 2 * t + v;
+            if (p >= cols) continue;
+            float gate = v == 0 ? s.x : s.y, up = v == 0 ? s.z : s.w;
+            if constexpr (Q) {
+                const float xs = __ldg(a.x_scale + c.token[first + p]);
+                gate = gate * wg * xs;
+                up = up * wu * xs;
             }
+            const __nv_bfloat16 h = __float2bfloat16_rn(silu(gate) * up);
+            a.h[static_cast<int64_t>(first + p) * a.I + ch] = __bfloat16_as_ushort(h);
         }
     }
-    __syncthreads();
 }
 
-// MAXT: eights of tokens an expert can have.
-template <bool Q, int MAXT>
-__global__ void __launch_bounds__(kLayerThreads) layer_gate_up_kernel(const LayerArgs a) {
+template <bool Q>
+__global__ void __launch_bounds__(kLayerThreads, 2) layer_gate_up_kernel(const LayerArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
-    float4* sum = reinterpret_cast<float4*>(smem);
-    Chosen c(smem + sizeof(float4) * kLayerWarps * MAXT * 32, a);
+    GateUpRing ring(smem);
+    float4* sum = reinterpret_cast<float4*>(smem + kLayerWarps * GateUpRing::kWarpBytes);
+    Chosen c(reinterpret_cast<uint8_t*>(sum + kLayerWarps * kGateUpTiles * 32), a);
+    c.clear(a);
     pdl_wait();
     pdl_trigger();
     c.find(a);
+    const int warp = threadIdx.x >> 5, bytes = a.H * (Q ? 1 : 2), steps = (bytes + kStepBytes - 1) / kStepBytes;
+    const uint8_t* x = static_cast<const uint8_t*>(a.x);
     // every block takes an equal run of the chosen experts' channels
     const int64_t all = static_cast<int64_t>(c.count) * a.I;
-    int64_t at = blockIdx.x * all / gridDim.x;
-    const int64_t end = (blockIdx.x + 1) * all / gridDim.x;
-    while (at < end) {
-        const int i = static_cast<int>(at / a.I), channel = static_cast<int>(at - static_cast<int64_t>(i) * a.I);
-        int n = a.I - channel < 8 ? a.I - channel : 8;
-        if (end - at < n) n = static_cast<int>(end - at);
-        const int eights = (c.size(i) + 7) / 8;
-        if (MAXT >= 8 && eights > 4) gate_up_tile<Q, MAXT >= 8 ? 8 : 1>(a, c, sum, i, channel, n);
-        else if (MAXT >= 4 && eights > 2) gate_up_tile<Q, MAXT >= 4 ? 4 : 1>(a, c, sum, i, channel, n);
-        else if (MAXT >= 2 && eights > 1) gate_up_tile<Q, MAXT >= 2 ? 2 : 1>(a, c, sum, i, channel, n);
-        else gate_up_tile<Q, 1>(a, c, sum, i, channel, n);
-        at += n;
-    }
+    GateUpWalk walk;
+    walk.at = blockIdx.x * all / gridDim.x;
+    walk.end = (blockIdx.x + 1) * all / gridDim.x;
+    walk.step = warp;
+    walk.tile(c, a.I);
+    if (walk.at >= walk.end) return;
+    GateUpWeights<Q> weights;
+    weights.walk = walk;
+    weights.rows(a, c);
+    for (int i = 0; i < GateUpRing::kDepth - 1; ++i) weights.fetch(a, c, ring, i, warp, steps);
+    GateUpWalk ahead = walk;  // the tokens', a step ahead
+    Tokens tokens;
+    tokens.rows(c, walk.expert, 0, x, false, bytes);
+    if (warp < steps) tokens.load(warp, bytes);
+    do {
+        float acc[kGateUpTiles][kEights][4];
+        zero(acc);
+        for (int s = warp; s < steps; s += kLayerWarps) {
+            weights.fetch(a, c, ring, GateUpRing::kDepth - 1, warp, steps);
+            uint4 now[kPieces][kEights];
+            const bool more = tokens.more;
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+                for (int j = 0; j < kEights; ++j) now[p][j] = tokens.v[p][j];
+            if (s + kLayerWarps < steps) {
+                tokens.load(s + kLayerWarps, bytes);
+            } else if (ahead.next(c, a.I)) {
+                tokens.rows(c, ahead.expert, ahead.pass, x, false, bytes);
+                tokens.load(warp, bytes);
+            }
+            GateUpRing::wait();
+            multiply<Q>(acc, ring, now, more);
+            ring.next();
+        }
+        gate_up_join<Q>(a, c, sum, walk, acc);
+    } while (walk.next(c, a.I));
 }
 
 // ---------------------------------------------------------------- down
-// Rows `first_row` .. of out for one expert's tokens, over blocks first .. last of k: added,
-// weighted, to the warp's sums [ROWS][N].
-template <int ROWS, int NT>
-__device__ __forceinline__ void down_part(const LayerArgs& a, const Chosen& c, float* sum, int i, int first_row, int rows,
-                                          int first, int last) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int first_pair = c.begin[i], cols = c.begin[i + 1] - first_pair;
-    const int64_t row_bytes = static_cast<int64_t>(a.I) * 2;
-    const uint8_t* w = reinterpret_cast<const uint8_t*>(a.w_down) +
-                       (static_cast<int64_t>(c.expert[i]) * a.H + first_row) * row_bytes;
-    const uint8_t* lo = g < rows ? w + g * row_bytes : nullptr;
-    const uint8_t* hi = ROWS == 16 && g + 8 < rows ? w + (g + 8) * row_bytes : nullptr;
-    const uint8_t* col[NT];
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int p = 8 * j + g;
-        col[j] = p < cols ? reinterpret_cast<const uint8_t*>(a.h) + (first_pair + p) * row_bytes : nullptr;
-        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+// A walk over a warp's run of the chosen experts' steps of k: one expert's (its part) after the
+// other, pass by pass.
+struct DownWalk {
+    int at, end, steps;
+    int expert, first, last;  // the part at hand: the expert's place among the chosen, its steps
+    int pass, passes, step;
+    __device__ void part(const Chosen& c) {
+        pass = 0;
+        passes = 0;
+        if (at >= end) return;
+        expert = at / steps;
+        step = first = at - expert * steps;
+        last = end - at < steps - first ? first + end - at : steps;
+        passes = (c.size(expert) + kPass - 1) / kPass;
     }
-    stream_rows<false, NT>(acc, lo, hi, col, first, last, static_cast<int>(row_bytes), t);
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int p = 8 * j + 2 * t + (v & 1), row = g + (v >> 1) * 8;
-            if (p < cols && row < ROWS) {
-                float* s = sum + row * a.N + c.token[first_pair + p];
-                *s = fmaf(c.weight[first_pair + p], acc[j][v], *s);
+    __device__ bool next(const Chosen& c) {
+        step = first;
+        if (++pass < passes) return true;
+        at += last - first;
+        part(c);
+        return at < end;
+    }
+};
+
+// Sixteens of rows that a cluster has.  The sums of more than eight tokens leave room for one.
+template <bool MANY>
+struct Down {
+    static constexpr int kTiles = MANY ? 1 : 2;
+    static constexpr int kRows = 16 * kTiles;
+    using Ring = WeightRing<kTiles, false, MANY ? 4 : 3>;
+};
+
+template <bool MANY>
+struct DownWeights {
+    using D = Down<MANY>;
+    DownWalk walk;
+    WeightRows w;
+    int first_row;
+    __device__ void rows(const LayerArgs& a, const Chosen& c) {
+        if (walk.at >= walk.end) return;
+        w.row = static_cast<int64_t>(a.I) * 2;
+        w.half = 8 * w.row;
+        w.tile = 16 * w.row;
+        w.n = a.H - first_row;
+        w.first = reinterpret_cast<const uint8_t*>(a.w_down) +
+                  (static_cast<int64_t>(c.expert[walk.expert]) * a.H + first_row) * w.row;
+    }
+    __device__ __forceinline__ void fetch(const LayerArgs& a, const Chosen& c, const typename D::Ring& ring, int ahead) {
+        if (walk.at < walk.end) {
+            ring.fetch(ahead, w, walk.step * kStepBytes, 2 * a.I);
+            if (++walk.step >= walk.last) {
+                walk.next(c);
+                rows(a, c);
             }
+        }
+        D::Ring::commit();
+    }
+};
+
+// A part's products, weighted, are added to the warp's sums [rows][N].
+template <int MT>
+__device__ __forceinline__ void down_add(const LayerArgs& a, const Chosen& c, float* sum, const DownWalk& walk,
+                                         const float (&acc)[MT][kEights][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int first = c.begin[walk.expert] + walk.pass * kPass, cols = c.begin[walk.expert + 1] - first;
+#pragma unroll
+    for (int j = 0; j < kEights; ++j)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const int p = 8 * j + 2 * t + v;
+            if (p >= cols) continue;
+            const float w = c.weight[first + p];
+            float* s = sum + c.token[first + p];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float* o = s + (16 * m + 8 * half + g) * a.N;
+                    *o = fmaf(w, acc[m][j][2 * half + v], *o);
+                }
         }
     __syncwarp();  // the next expert's tokens are other lanes'
 }
 
-// A block has ROWS rows of the output, its warps share the chosen experts' k.
-template <int ROWS, int MAXT>
-__global__ void __launch_bounds__(kLayerThreads) layer_down_kernel(const LayerArgs a) {
+__device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// A cluster has Down::kRows rows of the output; all warps of its blocks share the chosen experts' k.
+template <bool MANY>
+__global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const LayerArgs a) {
+    using D = Down<MANY>;
     extern __shared__ __align__(16) uint8_t smem[];
-    float* sums = reinterpret_cast<float*>(smem);  // [warps][ROWS][N]
-    Chosen c(smem + sizeof(float) * kLayerWarps * ROWS * a.N, a);
+    typename D::Ring ring(smem);
+    float* sums = reinterpret_cast<float*>(smem + kLayerWarps * D::Ring::kWarpBytes);  // [warps][rows][N]
+    Chosen c(reinterpret_cast<uint8_t*>(sums) + sizeof(float) * kLayerWarps * D::kRows * a.N, a);
     const int tid = threadIdx.x, warp = tid >> 5;
-    for (int v = tid; v < kLayerWarps * ROWS * a.N; v += kLayerThreads) sums[v] = 0.f;
+    uint32_t rank, blocks;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(blocks));
+    for (int v = tid; v < kLayerWarps * D::kRows * a.N; v += kLayerThreads) sums[v] = 0.f;
+    // topk_idx and the weights come from before the launch that this one may overlap
+    c.clear(a);
     c.find(a);
+    const uint8_t* h = reinterpret_cast<const uint8_t*>(a.h);
+    const int bytes = 2 * a.I;
+    DownWalk walk;
+    walk.steps = (bytes + kStepBytes - 1) / kStepBytes;
+    const int64_t all = static_cast<int64_t>(c.count) * walk.steps, me = rank * kLayerWarps + warp, of = blocks * kLayerWarps;
+    walk.at = static_cast<int>(me * all / of);
+    walk.end = static_cast<int>((me + 1) * all / of);
+    walk.part(c);
+    DownWeights<MANY> weights;
+    weights.walk = walk;
+    weights.first_row = blockIdx.x / blocks * D::kRows;
+    weights.rows(a, c);
+    for (int i = 0; i < D::Ring::kDepth - 1; ++i) weights.fetch(a, c, ring, i);
     pdl_wait();
     pdl_trigger();
-    const int first_row = blockIdx.x * ROWS;
-    const int rows = a.H - first_row < ROWS ? a.H - first_row : ROWS;
-    const int blocks = (2 * a.I + 63) / 64;
-    const int all = c.count * blocks;
-    int at = static_cast<int>(static_cast<int64_t>(warp) * all / kLayerWarps);
-    const int end = static_cast<int>(static_cast<int64_t>(warp + 1) * all / kLayerWarps);
-    float* sum = sums + warp * ROWS * a.N;
-    while (at < end) {
-        const int i = at / blocks, first = at - i * blocks;
-        const int last = end - at < blocks - first ? first + end - at : blocks;
-        const int eights = (c.size(i) + 7) / 8;
-        if (MAXT >= 8 && eights > 4) down_part<ROWS, MAXT >= 8 ? 8 : 1>(a, c, sum, i, first_row, rows, first, last);
-        else if (MAXT >= 4 && eights > 2) down_part<ROWS, MAXT >= 4 ? 4 : 1>(a, c, sum, i, first_row, rows, first, last);
-        else if (MAXT >= 2 && eights > 1) down_part<ROWS, MAXT >= 2 ? 2 : 1>(a, c, sum, i, first_row, rows, first, last);
-        else down_part<ROWS, 1>(a, c, sum, i, first_row, rows, first, last);
-        at += last - first;
+    if (walk.at < walk.end) {
+        float* sum = sums + warp * D::kRows * a.N;
+        DownWalk ahead = walk;  // the tokens', a step ahead
+        Tokens tokens;
+        tokens.rows(c, walk.expert, 0, h, true, bytes);
+        tokens.load(walk.first, bytes);
+        do {
+            float acc[D::kTiles][kEights][4];
+            zero(acc);
+            for (int s = walk.first; s < walk.last; ++s) {
+                weights.fetch(a, c, ring, D::Ring::kDepth - 1);
+                uint4 now[kPieces][kEights];
+                const bool more = tokens.more;
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+                    for (int j = 0; j < kEights; ++j) now[p][j] = tokens.v[p][j];
+                if (s + 1 < walk.last) {
+                    tokens.load(s + 1, bytes);
+                } else if (ahead.next(c)) {
+                    tokens.rows(c, ahead.expert, ahead.pass, h, true, bytes);
+                    tokens.load(ahead.first, bytes);
+                }
+                D::Ring::wait();
+                multiply<false>(acc, ring, now, more);
+                ring.next();
+            }
+            down_add(a, c, sum, walk, acc);
+        } while (walk.next(c));
     }
     __syncthreads();
-    for (int v = tid; v < ROWS * a.N; v += kLayerThreads) {
-        const int row = v % ROWS, s = v / ROWS;  // neighbouring threads write neighbouring elements
-        if (row < rows) {
-            float o = 0.f;
+    for (int v = tid; v < D::kRows * a.N; v += kLayerThreads) {
+        float o = sums[v];
 #pragma unroll
-            for (int w = 0; w < kLayerWarps; ++w) o += sums[(w * ROWS + row) * a.N + s];
-            a.out[static_cast<int64_t>(s) * a.H + first_row + row] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-        }
+        for (int w = 1; w < kLayerWarps; ++w) o += sums[w * D::kRows * a.N + v];
+        sums[v] = o;
     }
+    // the blocks' sums are joined in their order, each block an equal part of them
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int v = rank * kLayerThreads + tid; v < D::kRows * a.N; v += blocks * kLayerThreads) {
+        const int row = v % D::kRows, s = v / D::kRows;  // neighbouring threads write neighbouring elements
+        if (weights.first_row + row >= a.H) continue;
+        float o = 0.f;
+        for (uint32_t r = 0; r < blocks; ++r) o += load_cluster(sums + row * a.N + s, r);
+        a.out[static_cast<int64_t>(s) * a.H + weights.first_row + row] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+    }
+    // a block's sums stay until the others have read them
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace moe
@@ -400,31 +664,42 @@ namespace {
 using namespace moe_host;
 using moe::LayerArgs;
 
-template <bool Q, int MAXT>
+template <bool Q>
 int launch_gate_up(const LayerArgs& a, cudaStream_t stream) {
-    const size_t smem = sizeof(float4) * moe::kLayerWarps * MAXT * 32 + moe::Chosen::bytes(a.N, a.K, a.E);
-    if (cudaFuncSetAttribute(moe::layer_gate_up_kernel<Q, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) !=
+    const size_t smem = moe::kLayerWarps * (moe::GateUpRing::kWarpBytes + sizeof(float4) * moe::kGateUpTiles * 32) +
+                        moe::Chosen::bytes(a.N, a.K, a.E);
+    if (cudaFuncSetAttribute(moe::layer_gate_up_kernel<Q>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
-    return launch(moe::layer_gate_up_kernel<Q, MAXT>, dim3(static_cast<unsigned>(3 * num_sms())), dim3(moe::kLayerThreads),
+    return launch(moe::layer_gate_up_kernel<Q>, dim3(static_cast<unsigned>(2 * num_sms())), dim3(moe::kLayerThreads),
                   smem, stream, a);
 }
 
-template <int ROWS, int MAXT>
+template <bool MANY>
 int launch_down(const LayerArgs& a, cudaStream_t stream) {
-    const size_t smem = sizeof(float) * moe::kLayerWarps * ROWS * a.N + moe::Chosen::bytes(a.N, a.K, a.E);
-    if (cudaFuncSetAttribute(moe::layer_down_kernel<ROWS, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) !=
+    using D = moe::Down<MANY>;
+    const size_t smem = moe::kLayerWarps * (D::Ring::kWarpBytes + sizeof(float) * D::kRows * a.N) +
+                        moe::Chosen::bytes(a.N, a.K, a.E);
+    if (cudaFuncSetAttribute(moe::layer_down_kernel<MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
-    return launch(moe::layer_down_kernel<ROWS, MAXT>, dim3(static_cast<unsigned>((a.H + ROWS - 1) / ROWS)),
-                  dim3(moe::kLayerThreads), smem, stream, a);
-}
-
-template <int MAXT>
-int launch_layer(const LayerArgs& a, bool q, cudaStream_t stream) {
-    const int rc = q ? launch_gate_up<true, MAXT>(a, stream) : launch_gate_up<false, MAXT>(a, stream);
-    if (rc != MOE_OK) return rc;
-    return a.H / 16 >= 2 * num_sms() ? launch_down<16, MAXT>(a, stream) : launch_down<8, MAXT>(a, stream);
+    const int groups = (a.H + D::kRows - 1) / D::kRows;
+    int blocks = 1;  // of a cluster: as many as keep all resident
+    while (blocks < 8 && 2 * blocks * groups <= 2 * num_sms()) blocks *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(groups * blocks));
+    cfg.blockDim = dim3(moe::kLayerThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(blocks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, moe::layer_down_kernel<MANY>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
@@ -467,8 +742,7 @@ extern "C" MOE_API int moe_layer(const void* x, const float* x_scale, const floa
     if (rc != MOE_OK || N == 0) return rc;
     const LayerArgs a = {x, x_scale, w_gate_up, w_scale, w_down, topk_idx, topk_w, static_cast<uint16_t*>(workspace), out,
                          N, K, E, H, I};
-    if (N <= 8) return launch_layer<1>(a, q, stream);
-    if (N <= 16) return launch_layer<2>(a, q, stream);
-    if (N <= 32) return launch_layer<4>(a, q, stream);
-    return launch_layer<8>(a, q, stream);
+    const int up = q ? launch_gate_up<true>(a, stream) : launch_gate_up<false>(a, stream);
+    if (up != MOE_OK) return up;
+    return N > 8 ? launch_down<true>(a, stream) : launch_down<false>(a, stream);
 }
