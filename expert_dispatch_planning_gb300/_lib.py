@@ -81,7 +81,7 @@ SIGNATURES = [
     ("moe_block_norm_backward_workspace_size", _size, [_i32, _i32]),
     ("moe_block_norm_backward", _i32, [_P, _P, _P, _i32, _P, _P, _i32, _P, _i32, _P, _i32, _P, _P, _i32, _i32, _f32, _P, _P,
                                        _P, _P, _P, _P, _size, _P]),
-    ("moe_layer_workspace_size", _size, [_i32, _i32, _i32]),
+    ("moe_layer_workspace_size", _size, [_i32, _i32, _i32, _i32]),
     ("moe_layer", _i32, [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _P,
                          _P, _P, _P, _size, _P]),
     ("moe_get_status", _i32, [ctypes.POINTER(MoePlanOut), ctypes.POINTER(ctypes.c_int32), _P]),

@@ -21,9 +21,6 @@
 // of its row (and of its token's) instead: four lanes read 64 bytes of a row,
 // without shared memory or shuffles.  8-bit operands become fp16 in registers
 // (exact), their products are exact in the fp32 accumulator.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
 #include <cmath>
 
 #include "vec8.cuh"
@@ -42,13 +39,14 @@ struct LayerArgs {
     const int32_t* topk_idx;
     const float* topk_w;
     uint16_t* h;  // [N*K][I], rows in the order of experts, then tokens
+    float* y;     // [N*K][H], for many tokens
     uint16_t* out;
     int N, K, E, H, I;
 };
 
 // ---------------------------------------------------------------- the chosen experts
 // In shared memory: expert[a] and begin[a] of the a-th chosen expert (begin[count]
-// = pairs), and for every place its token and weight.  All threads of the block call.
+// = pairs), and for every place its pair, token and weight.  All threads of the block call.
 struct Chosen {
     unsigned long long* tokens;  // [E] sets of tokens
     int* expert;                 // [slots]
@@ -56,12 +54,13 @@ struct Chosen {
     int* sums;                   // [warps] of the scan
     float* weight;               // [N*K]
     uint16_t* place;             // [E] a chosen expert's place
+    uint16_t* pair;              // [N*K] flat indices s * K + k
     uint8_t* token;              // [N*K]
     int count;
 
     static __host__ __device__ int slots(int N, int K, int E) { return N * K < E ? N * K : E; }
     static __host__ __device__ size_t bytes(int N, int K, int E) {
-        const size_t s = 8 * static_cast<size_t>(E) + 4 * (2 * slots(N, K, E) + 1) + 4 * kLayerWarps + 4 * N * K + 2 * E + N * K;
+        const size_t s = 8 * static_cast<size_t>(E) + 4 * (2 * slots(N, K, E) + 1) + 4 * kLayerWarps + 7 * N * K + 2 * E;
         return (s + 15) / 16 * 16;
     }
     __device__ Chosen(uint8_t* smem, const LayerArgs& a) {
@@ -72,7 +71,8 @@ struct Chosen {
         sums = begin + n + 1;
         weight = reinterpret_cast<float*>(sums + kLayerWarps);
         place = reinterpret_cast<uint16_t*>(weight + a.N * a.K);
-        token = reinterpret_cast<uint8_t*>(place + a.E);
+        pair = place + a.E;
+        token = reinterpret_cast<uint8_t*>(pair + a.N * a.K);
     }
     __device__ int size(int i) const { return begin[i + 1] - begin[i]; }
 
@@ -138,6 +138,7 @@ struct Chosen {
                 const int s = (tid + v * kLayerThreads) / a.K;
                 const int p = begin[place[e_of[v]]] + __popcll(tokens[e_of[v]] & ((1ull << s) - 1));
                 token[p] = static_cast<uint8_t>(s);
+                pair[p] = static_cast<uint16_t>(tid + v * kLayerThreads);
                 weight[p] = w_of[v];
             }
         __syncthreads();
@@ -154,16 +155,13 @@ struct Fragment {
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if constexpr (Q) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                        static_cast<__nv_fp8x2_storage_t>(j == 0 ? u[i] & 0xffffu : u[i] >> 16), __NV_E4M3);
-                    w[2 * i + j] = h.x | static_cast<uint32_t>(h.y) << 16;
-                }
-            } else {
+            if constexpr (Q)
+                asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+                    "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+                    : "=r"(w[2 * i]), "=r"(w[2 * i + 1])
+                    : "r"(u[i]));
+            else
                 w[i] = u[i];
-            }
         }
     }
 };
@@ -207,11 +205,17 @@ __device__ __forceinline__ uint4 load16(const uint8_t* p, bool inside) {
 constexpr int kStepBytes = 128;
 constexpr int kPieces = 2;  // of 64 bytes: what a fragment has of a row
 
-// Rows of one tile: MT times two eights; eight h of sixteen m begins at first + m * tile + h * half.
+// Rows of one tile: MT times two eights of them.
 struct WeightRows {
-    const uint8_t* first;
-    int64_t row, half, tile;  // bytes from one to the next
-    int n;                    // rows that are there: of each half (gate and up), or of all
+    const uint8_t* any;        // an address to give where nothing is read
+    const uint8_t* lane;       // chunk lane % 8 of row lane / 8 of the first eight
+    int64_t four, half, tile;  // bytes from a row to its fourth next, an eight to the other, a sixteen to the next
+    int n;                     // rows that are there: of each half (gate and up), or of all
+    __device__ __forceinline__ void set(const void* base, int64_t first_row, int64_t row, int there) {
+        n = there;
+        any = static_cast<const uint8_t*>(base);
+        lane = any + (first_row + ((threadIdx.x & 31) >> 3)) * row + (threadIdx.x & 7) * 16;
+    }
 };
 
 template <int MT, bool HALVES, int DEPTH>  // HALVES: n counts the rows of each half
@@ -219,66 +223,70 @@ struct WeightRing {
     static constexpr int kStep = MT * 16 * kStepBytes;
     static constexpr int kDepth = DEPTH;
     static constexpr int kWarpBytes = DEPTH * kStep;
-    const uint32_t mine;
-    int slot = 0;  // the step's that is read next
-    __device__ explicit WeightRing(const uint8_t* smem) : mine(smem_addr(smem) + (threadIdx.x >> 5) * kWarpBytes) {}
-    // 16-byte chunk `chunk` of row `row` of eight `e`: odd rows are turned by half a row, so that
-    // the eight lanes of a read, two rows' four chunks, are in different banks.
-    static __device__ __forceinline__ int place(int e, int row, int chunk) {
-        return (e * 8 + row) * kStepBytes + (chunk ^ (row & 1) << 2) * 16;
+    // A row's 16-byte chunks lie one after the other, an odd row's turned by half a row: so the
+    // eight lanes of a read, two rows' four chunks, are in different banks.
+    uint32_t to;       // where the lane's copies go: row r = lane / 8 of each four rows, chunk lane % 8
+    uint32_t from;     // where its pieces are: row g = lane / 4 of each eight, chunk lane % 4 (the other piece: ^ 64)
+    uint32_t at = 0;   // the step's that is read next, and the one that is filled next
+    uint32_t fill = 0;
+    __device__ explicit WeightRing(const uint8_t* smem) {
+        const uint32_t lane = threadIdx.x & 31, mine = smem_addr(smem) + (threadIdx.x >> 5) * kWarpBytes;
+        const uint32_t r = lane >> 3, chunk = lane & 7, g = lane >> 2, t = lane & 3;
+        to = mine + r * kStepBytes + (chunk ^ (r & 1) << 2) * 16;
+        from = mine + g * kStepBytes + (t ^ (g & 1) << 2) * 16;
     }
-    // The step at byte `at` of the rows; zeros behind a row's end (`bytes`) and for rows that are not there.
-    __device__ __forceinline__ void fetch(int ahead, const WeightRows& w, int at, int bytes) const {
-        const int s = slot + ahead, r = (threadIdx.x & 31) >> 3, chunk = threadIdx.x & 7, k = at + chunk * 16;
-        const uint32_t to = mine + (s >= DEPTH ? s - DEPTH : s) * kStep;
+    // The step at byte `k` of the rows; zeros behind a row's end (`bytes`) and for rows that are not there.
+    __device__ __forceinline__ void fetch(const WeightRows& w, int k, int bytes) {
+        const int r = (threadIdx.x & 31) >> 3, mine = k + static_cast<int>(threadIdx.x & 7) * 16;
+        const uint8_t* first = w.lane + k;
+        const uint32_t slot = to + fill;
+        fill = fill == (DEPTH - 1) * kStep ? 0 : fill + kStep;
         __syncwarp();  // all lanes have read what was there
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int half = 0; half < 2; ++half) {
+                const uint8_t* eight = first + m * w.tile + half * w.half;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int row = 4 * i + r;
-                    const bool in = (HALVES ? 8 * m : 16 * m + 8 * half) + row < w.n && k < bytes;
-                    const uint8_t* from = w.first + m * w.tile + half * w.half + row * w.row + k;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + place(2 * m + half, row, chunk)),
-                                 "l"(in ? from : w.first), "r"(in ? 16 : 0)
+                    const bool in = (HALVES ? 8 * m : 16 * m + 8 * half) + 4 * i + r < w.n && mine < bytes;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + (4 * (2 * m + half) + 2 * i) * 256),
+                                 "l"(in ? eight + i * w.four : w.any), "r"(in ? 16 : 0)
                                  : "memory");
                 }
+            }
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
     static __device__ __forceinline__ void wait() {
         asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
         __syncwarp();
     }
-    // The lane's piece p of its row (g) of an eight.
+    // The lane's piece p of its row of an eight.
     __device__ __forceinline__ uint4 read(int m, int half, int p) const {
-        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
         uint4 v;
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(mine + slot * kStep + place(2 * m + half, g, 4 * p + t))
+                     : "r"((from ^ p << 6) + at + (2 * m + half) * 1024)
                      : "memory");
         return v;
     }
-    __device__ __forceinline__ void next() { slot = slot + 1 == DEPTH ? 0 : slot + 1; }
+    __device__ __forceinline__ void next() { at = at == (DEPTH - 1) * kStep ? 0 : at + kStep; }
 };
 
-constexpr int kEights = 2;             // of tokens that a pass over a tile's weights takes
-constexpr int kPass = 8 * kEights;
-
-// The lane's token rows for the steps of a pass: both pieces of its token in each eight, asked
-// for a step ahead.  A row that is not there is null and gives zeros.
+// The lane's token rows for the steps of a pass over a tile's weights, which takes up to EIGHTS eights
+// of an expert's tokens: both pieces of its token in each eight, asked for a step ahead.  A row that is
+// not there is null and gives zeros.
+template <int EIGHTS>
 struct Tokens {
-    const uint8_t* row[kEights];
-    uint4 v[kPieces][kEights];
-    bool more;  // a second eight
+    const uint8_t* row[EIGHTS];
+    uint4 v[kPieces][EIGHTS];
+    bool more;  // than one eight
     __device__ __forceinline__ void rows(const Chosen& c, int expert, int pass, const uint8_t* base, bool by_place,
                                          int64_t bytes) {
-        const int first = c.begin[expert] + pass * kPass, cols = c.begin[expert + 1] - first;
+        const int first = c.begin[expert] + pass * 8 * EIGHTS, cols = c.begin[expert + 1] - first;
         more = cols > 8;
 #pragma unroll
-        for (int j = 0; j < kEights; ++j) {
+        for (int j = 0; j < EIGHTS; ++j) {
             const int p = 8 * j + ((threadIdx.x & 31) >> 2);
             row[j] = nullptr;
             if (p < cols) row[j] = base + (by_place ? first + p : c.token[first + p]) * bytes + (threadIdx.x & 3) * 16;
@@ -289,15 +297,16 @@ struct Tokens {
         for (int p = 0; p < kPieces; ++p) {
             const int at = step * kStepBytes + 64 * p;
             const bool in = at + static_cast<int>(threadIdx.x & 3) * 16 < bytes;
-            v[p][0] = load16(row[0] + at, in && row[0] != nullptr);
-            if (more) v[p][1] = load16(row[1] + at, in && row[1] != nullptr);
+#pragma unroll
+            for (int j = 0; j < EIGHTS; ++j)
+                if (j == 0 || more) v[p][j] = load16(row[j] + at, in && row[j] != nullptr);
         }
     }
 };
 
 // One step: acc += the step's weight rows times tokens.
-template <bool Q, int MT, typename Ring>
-__device__ __forceinline__ void multiply(float (&acc)[MT][kEights][4], const Ring& ring, const uint4 (&v)[kPieces][kEights],
+template <bool Q, int MT, int EIGHTS, typename Ring>
+__device__ __forceinline__ void multiply(float (&acc)[MT][EIGHTS][4], const Ring& ring, const uint4 (&v)[kPieces][EIGHTS],
                                          bool more) {
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
@@ -306,264 +315,295 @@ __device__ __forceinline__ void multiply(float (&acc)[MT][kEights][4], const Rin
         for (int m = 0; m < MT; ++m) {
             const Fragment<Q> lo(ring.read(m, 0, p)), hi(ring.read(m, 1, p));
             product<Q>(acc[m][0], lo, hi, b0);
-            if (more) product<Q>(acc[m][1], lo, hi, Fragment<Q>(v[p][1]));
+            if constexpr (EIGHTS > 1)
+                if (more) product<Q>(acc[m][1], lo, hi, Fragment<Q>(v[p][1]));
         }
     }
 }
 
-template <int MT>
-__device__ __forceinline__ void zero(float (&acc)[MT][kEights][4]) {
+template <int MT, int EIGHTS>
+__device__ __forceinline__ void zero(float (&acc)[MT][EIGHTS][4]) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int j = 0; j < kEights; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
+        for (int j = 0; j < EIGHTS; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
 }
 
-// ---------------------------------------------------------------- gate and up
 __device__ __forceinline__ float silu(float g) {
     const float e = expf(-fabsf(g));
     return g * __fdiv_rn(g >= 0.f ? 1.f : e, 1.f + e);
 }
 
-constexpr int kGateUpTiles = 2;  // eights of channels in a tile
-constexpr int kGateUpChannels = 8 * kGateUpTiles;
-using GateUpRing = WeightRing<kGateUpTiles, true, 3>;
+// ---------------------------------------------------------------- rows by rows
+// Gate and up, and the down product of many tokens: every block takes an equal run of the chosen
+// experts' rows (channels of gate and up: a row of each), its warps share k.
+constexpr int kTiles = 2;  // sixteens of rows in a tile
+template <bool DOWN>
+using TileRing = WeightRing<kTiles, !DOWN, 3>;
 
-// A walk over a block's run of the chosen experts' channels: tile by tile (channels of one
-// expert), pass by pass (sixteen of its tokens; the passes after the first find the tile's
-// weights in L2), and over the warp's steps of k.
-struct GateUpWalk {
+// A walk over a block's run: tile by tile (32 rows of one expert, or 16 channels with two rows
+// each), pass by pass (those after the first find the tile's weights in L2),
+// and over the warp's steps of k.
+template <bool DOWN, int EIGHTS>
+struct TileWalk {
+    static constexpr int kUnits = DOWN ? 16 * kTiles : 8 * kTiles;
     int64_t at, end;
-    int expert, channel, n;  // the tile at hand: its place among the chosen, first channel, channels
+    int expert, unit, n;  // the tile at hand: its expert's place among the chosen, first row or channel, their number
     int pass, passes, step;
-    __device__ void tile(const Chosen& c, int I) {
+    __device__ void tile(const Chosen& c, int units) {
         pass = 0;
         passes = 0;
         if (at >= end) return;
-        expert = static_cast<int>(at / I);
-        channel = static_cast<int>(at - static_cast<int64_t>(expert) * I);
-        n = I - channel < kGateUpChannels ? I - channel : kGateUpChannels;
+        expert = static_cast<int>(at / units);
+        unit = static_cast<int>(at - static_cast<int64_t>(expert) * units);
+        n = units - unit < kUnits ? units - unit : kUnits;
         if (end - at < n) n = static_cast<int>(end - at);
-        passes = (c.size(expert) + kPass - 1) / kPass;
+        passes = (c.size(expert) + 8 * EIGHTS - 1) / (8 * EIGHTS);
     }
     // To the next pass or tile; whether there is one.
-    __device__ bool next(const Chosen& c, int I) {
+    __device__ bool next(const Chosen& c, int units) {
         if (++pass < passes) return true;
         at += n;
-        tile(c, I);
+        tile(c, units);
         return at < end;
     }
 };
 
-// The warp's steps are kLayerWarps apart: what the block's warps ask for at one time is contiguous.
-template <bool Q>
-struct GateUpWeights {
-    GateUpWalk walk;
+// Where the ring asks for weights.  The warp's steps are kLayerWarps apart: what the block's warps
+// ask for at one time is contiguous.
+template <bool Q, bool DOWN, int EIGHTS>
+struct TileWeights {
+    TileWalk<DOWN, EIGHTS> walk;
     WeightRows w;
     __device__ void rows(const LayerArgs& a, const Chosen& c) {
         if (walk.at >= walk.end) return;
-        w.row = static_cast<int64_t>(a.H) * (Q ? 1 : 2);
-        w.half = a.I * w.row;
-        w.tile = 8 * w.row;
-        w.n = walk.n;
-        w.first = static_cast<const uint8_t*>(a.w_gate_up) +
-                  (static_cast<int64_t>(c.expert[walk.expert]) * 2 * a.I + walk.channel) * w.row;
+        const int64_t row = DOWN ? 2 * static_cast<int64_t>(a.I) : static_cast<int64_t>(a.H) * (Q ? 1 : 2);
+        w.four = 4 * row;
+        w.half = DOWN ? 8 * row : a.I * row;
+        w.tile = DOWN ? 16 * row : 8 * row;
+        if constexpr (DOWN) w.set(a.w_down, static_cast<int64_t>(c.expert[walk.expert]) * a.H + walk.unit, row, walk.n);
+        else w.set(a.w_gate_up, static_cast<int64_t>(c.expert[walk.expert]) * 2 * a.I + walk.unit, row, walk.n);
     }
-    __device__ __forceinline__ void fetch(const LayerArgs& a, const Chosen& c, const GateUpRing& ring, int ahead, int warp,
-                                          int steps) {
+    __device__ __forceinline__ void fetch(const LayerArgs& a, const Chosen& c, TileRing<DOWN>& ring, int warp, int steps,
+                                          int bytes) {
         if (walk.at < walk.end && warp < steps) {
-            ring.fetch(ahead, w, walk.step * kStepBytes, a.H * (Q ? 1 : 2));
+            ring.fetch(w, walk.step * kStepBytes, bytes);
             if ((walk.step += kLayerWarps) >= steps) {
                 walk.step = warp;
-                walk.next(c, a.I);
+                walk.next(c, DOWN ? a.H : a.I);
                 rows(a, c);
             }
         }
-        GateUpRing::commit();
+        TileRing<DOWN>::commit();
     }
 };
 
-// The parts of a tile's pass are joined over the block's warps in `sum` ([warps][kGateUpTiles][32]),
-// one eight of tokens after the other; warp m joins eight m of the channels.
-template <bool Q>
-__device__ __forceinline__ void gate_up_join(const LayerArgs& a, const Chosen& c, float4* sum, const GateUpWalk& walk,
-                                             const float (&acc)[kGateUpTiles][kEights][4]) {
+// The parts of a tile's pass are joined over the block's warps in `sum` ([warps][kTiles][32]), one
+// eight of tokens after the other; warp m joins sixteen m of the rows.  A lane has two tokens of rows
+// g and g + 8, which for gate and up are the two rows of a channel.
+template <bool Q, bool DOWN, int EIGHTS>
+__device__ __forceinline__ void join(const LayerArgs& a, const Chosen& c, float4* sum, const TileWalk<DOWN, EIGHTS>& walk,
+                                     const float (&acc)[kTiles][EIGHTS][4]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int e = c.expert[walk.expert], first = c.begin[walk.expert] + walk.pass * kPass,
+    const int e = c.expert[walk.expert], first = c.begin[walk.expert] + walk.pass * 8 * EIGHTS,
               cols = c.begin[walk.expert + 1] - first;
 #pragma unroll
-    for (int j = 0; j < kEights; ++j) {
+    for (int j = 0; j < EIGHTS; ++j) {
         if (8 * j >= cols) break;
         __syncthreads();  // the sums before are taken
 #pragma unroll
-        for (int m = 0; m < kGateUpTiles; ++m)
-            sum[(warp * kGateUpTiles + m) * 32 + lane] = make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
+        for (int m = 0; m < kTiles; ++m)
+            sum[(warp * kTiles + m) * 32 + lane] = make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
         __syncthreads();
-        if (warp >= kGateUpTiles) continue;
+        if (warp >= kTiles) continue;
         float4 s = sum[warp * 32 + lane];
 #pragma unroll
         for (int k = 1; k < kLayerWarps; ++k) {
-            const float4 o = sum[(k * kGateUpTiles + warp) * 32 + lane];
+            const float4 o = sum[(k * kTiles + warp) * 32 + lane];
             s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
         }
-        const int row = 8 * warp + g, ch = walk.channel + row;
-        if (row >= walk.n) continue;
-        float wg = 1.f, wu = 1.f;
-        if constexpr (Q) {
-            wg = __ldg(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + ch);
-            wu = __ldg(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + a.I + ch);
-        }
+        if constexpr (DOWN) {
+            const int row = 16 * warp + g;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const int p = 8 * j + 2 * t + v;
-            if (p >= cols) continue;
-            float gate = v == 0 ? s.x : s.y, up = v == 0 ? s.z : s.w;
-            if constexpr (Q) {
-                const float xs = __ldg(a.x_scale + c.token[first + p]);
-                gate = gate * wg * xs;
-                up = up * wu * xs;
+            for (int v = 0; v < 2; ++v) {
+                const int p = 8 * j + 2 * t + v;
+                if (p >= cols) continue;
+                const float w = c.weight[first + p];
+                float* y = a.y + static_cast<int64_t>(c.pair[first + p]) * a.H + walk.unit;
+                if (row < walk.n) y[row] = w * (v == 0 ? s.x : s.y);
+                if (row + 8 < walk.n) y[row + 8] = w * (v == 0 ? s.z : s.w);
             }
-            const __nv_bfloat16 h = __float2bfloat16_rn(silu(gate) * up);
-            a.h[static_cast<int64_t>(first + p) * a.I + ch] = __bfloat16_as_ushort(h);
+        } else {
+            const int row = 8 * warp + g, ch = walk.unit + row;
+            if (row >= walk.n) continue;
+            float wg = 1.f, wu = 1.f;
+            if constexpr (Q) {
+                wg = __ldg(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + ch);
+                wu = __ldg(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + a.I + ch);
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const int p = 8 * j + 2 * t + v;
+                if (p >= cols) continue;
+                float gate = v == 0 ? s.x : s.y, up = v == 0 ? s.z : s.w;
+                if constexpr (Q) {
+                    const float xs = __ldg(a.x_scale + c.token[first + p]);
+                    gate = gate * wg * xs;
+                    up = up * wu * xs;
+                }
+                const __nv_bfloat16 h = __float2bfloat16_rn(silu(gate) * up);
+                a.h[static_cast<int64_t>(first + p) * a.I + ch] = __bfloat16_as_ushort(h);
+            }
         }
     }
 }
 
-template <bool Q>
-__global__ void __launch_bounds__(kLayerThreads, 2) layer_gate_up_kernel(const LayerArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    GateUpRing ring(smem);
-    float4* sum = reinterpret_cast<float4*>(smem + kLayerWarps * GateUpRing::kWarpBytes);
-    Chosen c(reinterpret_cast<uint8_t*>(sum + kLayerWarps * kGateUpTiles * 32), a);
+// DOWN: y[s*K + k] = w[s][k] * (h . w_down^T) in fp32.  Else h.  EIGHTS: of tokens, in a pass.
+template <bool Q, bool DOWN, int EIGHTS>
+__global__ void __launch_bounds__(kLayerThreads, 2) layer_rows_kernel(const LayerArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    using Ring = TileRing<DOWN>;
+    Ring ring(smem);
+    float4* sum = reinterpret_cast<float4*>(smem + kLayerWarps * Ring::kWarpBytes);
+    Chosen c(reinterpret_cast<uint8_t*>(sum + kLayerWarps * kTiles * 32), a);
     c.clear(a);
-    pdl_wait();
-    pdl_trigger();
-    c.find(a);
-    const int warp = threadIdx.x >> 5, bytes = a.H * (Q ? 1 : 2), steps = (bytes + kStepBytes - 1) / kStepBytes;
-    const uint8_t* x = static_cast<const uint8_t*>(a.x);
-    // every block takes an equal run of the chosen experts' channels
-    const int64_t all = static_cast<int64_t>(c.count) * a.I;
-    GateUpWalk walk;
+    if constexpr (!DOWN) {
+        pdl_wait();
+        pdl_trigger();
+    }
+    c.find(a);  // (of the down product topk_idx and the weights come from before the launch that this one may overlap)
+    const int warp = threadIdx.x >> 5, units = DOWN ? a.H : a.I;
+    const int bytes = DOWN ? 2 * a.I : a.H * (Q ? 1 : 2), steps = (bytes + kStepBytes - 1) / kStepBytes;
+    const uint8_t* x = static_cast<const uint8_t*>(DOWN ? a.h : a.x);
+    const int64_t all = static_cast<int64_t>(c.count) * units;
+    TileWalk<DOWN, EIGHTS> walk;
     walk.at = blockIdx.x * all / gridDim.x;
     walk.end = (blockIdx.x + 1) * all / gridDim.x;
     walk.step = warp;
-    walk.tile(c, a.I);
-    if (walk.at >= walk.end) return;
-    GateUpWeights<Q> weights;
+    walk.tile(c, units);
+    TileWeights<Q, DOWN, EIGHTS> weights;
     weights.walk = walk;
     weights.rows(a, c);
-    for (int i = 0; i < GateUpRing::kDepth - 1; ++i) weights.fetch(a, c, ring, i, warp, steps);
-    GateUpWalk ahead = walk;  // the tokens', a step ahead
-    Tokens tokens;
-    tokens.rows(c, walk.expert, 0, x, false, bytes);
+    for (int i = 0; i < Ring::kDepth - 1; ++i) weights.fetch(a, c, ring, warp, steps, bytes);
+    if constexpr (DOWN) {
+        pdl_wait();
+        pdl_trigger();
+    }
+    if (walk.at >= walk.end) return;
+    TileWalk<DOWN, EIGHTS> ahead = walk;  // the tokens', a step ahead
+    Tokens<EIGHTS> tokens;
+    tokens.rows(c, walk.expert, 0, x, DOWN, bytes);
     if (warp < steps) tokens.load(warp, bytes);
     do {
-        float acc[kGateUpTiles][kEights][4];
+        float acc[kTiles][EIGHTS][4];
         zero(acc);
         for (int s = warp; s < steps; s += kLayerWarps) {
-            weights.fetch(a, c, ring, GateUpRing::kDepth - 1, warp, steps);
-            uint4 now[kPieces][kEights];
+            weights.fetch(a, c, ring, warp, steps, bytes);
+            uint4 now[kPieces][EIGHTS];
             const bool more = tokens.more;
 #pragma unroll
             for (int p = 0; p < kPieces; ++p)
 #pragma unroll
-                for (int j = 0; j < kEights; ++j) now[p][j] = tokens.v[p][j];
+                for (int j = 0; j < EIGHTS; ++j) now[p][j] = tokens.v[p][j];
             if (s + kLayerWarps < steps) {
                 tokens.load(s + kLayerWarps, bytes);
-            } else if (ahead.next(c, a.I)) {
-                tokens.rows(c, ahead.expert, ahead.pass, x, false, bytes);
+            } else if (ahead.next(c, units)) {
+                tokens.rows(c, ahead.expert, ahead.pass, x, DOWN, bytes);
                 tokens.load(warp, bytes);
             }
-            GateUpRing::wait();
+            Ring::wait();
             multiply<Q>(acc, ring, now, more);
             ring.next();
         }
-        gate_up_join<Q>(a, c, sum, walk, acc);
-    } while (walk.next(c, a.I));
+        join<Q, DOWN>(a, c, sum, walk, acc);
+    } while (walk.next(c, units));
 }
 
-// ---------------------------------------------------------------- down
-// A walk over a warp's run of the chosen experts' steps of k: one expert's (its part) after the
-// other, pass by pass.
+// out[s] = bf16 of the sum of its pairs' y, in the order of k: a thread eight elements.
+__global__ void __launch_bounds__(256) layer_sum_kernel(const LayerArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int nvec = a.H / 8;
+    const int v = blockIdx.x * 256 + threadIdx.x;
+    if (v >= a.N * nvec) return;
+    const int s = v / nvec, c = v - s * nvec;
+    const float4* y = reinterpret_cast<const float4*>(a.y + static_cast<int64_t>(s) * a.K * a.H) + 2 * c;
+    float f[8] = {};
+#pragma unroll 4
+    for (int k = 0; k < a.K; ++k) {
+        const float4 p = y[static_cast<int64_t>(k) * (a.H / 4)], q = y[static_cast<int64_t>(k) * (a.H / 4) + 1];
+        f[0] += p.x, f[1] += p.y, f[2] += p.z, f[3] += p.w;
+        f[4] += q.x, f[5] += q.y, f[6] += q.z, f[7] += q.w;
+    }
+    store8(a.out + static_cast<int64_t>(s) * a.H, c, f);
+}
+
+// ---------------------------------------------------------------- down, few tokens
+// A walk over a warp's run of the chosen experts' steps of k: one expert's (its part) after the other.
 struct DownWalk {
     int at, end, steps;
     int expert, first, last;  // the part at hand: the expert's place among the chosen, its steps
-    int pass, passes, step;
-    __device__ void part(const Chosen& c) {
-        pass = 0;
-        passes = 0;
+    int step;
+    __device__ void part() {
         if (at >= end) return;
         expert = at / steps;
         step = first = at - expert * steps;
         last = end - at < steps - first ? first + end - at : steps;
-        passes = (c.size(expert) + kPass - 1) / kPass;
     }
-    __device__ bool next(const Chosen& c) {
-        step = first;
-        if (++pass < passes) return true;
+    __device__ bool next() {
         at += last - first;
-        part(c);
+        part();
         return at < end;
     }
 };
 
-// Sixteens of rows that a cluster has.  The sums of more than eight tokens leave room for one.
-template <bool MANY>
-struct Down {
-    static constexpr int kTiles = MANY ? 1 : 2;
-    static constexpr int kRows = 16 * kTiles;
-    using Ring = WeightRing<kTiles, false, MANY ? 4 : 3>;
-};
+constexpr int kDownTokens = 8;  // at most: the block's sums are [warps][rows][N]
+constexpr int kDownRows = 16 * kTiles;
+using DownRing = WeightRing<kTiles, false, 3>;
 
-template <bool MANY>
 struct DownWeights {
-    using D = Down<MANY>;
     DownWalk walk;
     WeightRows w;
-    int first_row;
+    int first_row, n;  // the cluster's rows
     __device__ void rows(const LayerArgs& a, const Chosen& c) {
         if (walk.at >= walk.end) return;
-        w.row = static_cast<int64_t>(a.I) * 2;
-        w.half = 8 * w.row;
-        w.tile = 16 * w.row;
-        w.n = a.H - first_row;
-        w.first = reinterpret_cast<const uint8_t*>(a.w_down) +
-                  (static_cast<int64_t>(c.expert[walk.expert]) * a.H + first_row) * w.row;
+        const int64_t row = static_cast<int64_t>(a.I) * 2;
+        w.four = 4 * row;
+        w.half = 8 * row;
+        w.tile = 16 * row;
+        w.set(a.w_down, static_cast<int64_t>(c.expert[walk.expert]) * a.H + first_row, row, n);
     }
-    __device__ __forceinline__ void fetch(const LayerArgs& a, const Chosen& c, const typename D::Ring& ring, int ahead) {
+    __device__ __forceinline__ void fetch(const LayerArgs& a, const Chosen& c, DownRing& ring) {
         if (walk.at < walk.end) {
-            ring.fetch(ahead, w, walk.step * kStepBytes, 2 * a.I);
+            ring.fetch(w, walk.step * kStepBytes, 2 * a.I);
             if (++walk.step >= walk.last) {
-                walk.next(c);
+                walk.next();
                 rows(a, c);
             }
         }
-        D::Ring::commit();
+        DownRing::commit();
     }
 };
 
 // A part's products, weighted, are added to the warp's sums [rows][N].
-template <int MT>
 __device__ __forceinline__ void down_add(const LayerArgs& a, const Chosen& c, float* sum, const DownWalk& walk,
-                                         const float (&acc)[MT][kEights][4]) {
+                                         const float (&acc)[kTiles][1][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int first = c.begin[walk.expert] + walk.pass * kPass, cols = c.begin[walk.expert + 1] - first;
+    const int first = c.begin[walk.expert], cols = c.size(walk.expert);
 #pragma unroll
-    for (int j = 0; j < kEights; ++j)
+    for (int v = 0; v < 2; ++v) {
+        const int p = 2 * t + v;
+        if (p >= cols) continue;
+        const float w = c.weight[first + p];
+        float* s = sum + c.token[first + p];
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const int p = 8 * j + 2 * t + v;
-            if (p >= cols) continue;
-            const float w = c.weight[first + p];
-            float* s = sum + c.token[first + p];
+        for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float* o = s + (16 * m + 8 * half + g) * a.N;
-                    *o = fmaf(w, acc[m][j][2 * half + v], *o);
-                }
-        }
+            for (int half = 0; half < 2; ++half) {
+                float* o = s + (16 * m + 8 * half + g) * a.N;
+                *o = fmaf(w, acc[m][0][2 * half + v], *o);
+            }
+    }
     __syncwarp();  // the next expert's tokens are other lanes'
 }
 
@@ -575,19 +615,18 @@ __device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
     return v;
 }
 
-// A cluster has Down::kRows rows of the output; all warps of its blocks share the chosen experts' k.
-template <bool MANY>
-__global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const LayerArgs a) {
-    using D = Down<MANY>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    typename D::Ring ring(smem);
-    float* sums = reinterpret_cast<float*>(smem + kLayerWarps * D::Ring::kWarpBytes);  // [warps][rows][N]
-    Chosen c(reinterpret_cast<uint8_t*>(sums) + sizeof(float) * kLayerWarps * D::kRows * a.N, a);
+// A cluster has `rows` rows of the output, at most kDownRows; all warps of its blocks share the
+// chosen experts' k.
+__global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const LayerArgs a, int rows) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    DownRing ring(smem);
+    float* sums = reinterpret_cast<float*>(smem + kLayerWarps * DownRing::kWarpBytes);  // [warps][rows][N]
+    Chosen c(reinterpret_cast<uint8_t*>(sums) + sizeof(float) * kLayerWarps * kDownRows * a.N, a);
     const int tid = threadIdx.x, warp = tid >> 5;
     uint32_t rank, blocks;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(blocks));
-    for (int v = tid; v < kLayerWarps * D::kRows * a.N; v += kLayerThreads) sums[v] = 0.f;
+    for (int v = tid; v < kLayerWarps * kDownRows * a.N; v += kLayerThreads) sums[v] = 0.f;
     // topk_idx and the weights come from before the launch that this one may overlap
     c.clear(a);
     c.find(a);
@@ -598,56 +637,52 @@ __global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const Laye
     const int64_t all = static_cast<int64_t>(c.count) * walk.steps, me = rank * kLayerWarps + warp, of = blocks * kLayerWarps;
     walk.at = static_cast<int>(me * all / of);
     walk.end = static_cast<int>((me + 1) * all / of);
-    walk.part(c);
-    DownWeights<MANY> weights;
+    walk.part();
+    DownWeights weights;
     weights.walk = walk;
-    weights.first_row = blockIdx.x / blocks * D::kRows;
+    weights.first_row = static_cast<int>(blockIdx.x / blocks) * rows;
+    weights.n = a.H - weights.first_row < rows ? a.H - weights.first_row : rows;
     weights.rows(a, c);
-    for (int i = 0; i < D::Ring::kDepth - 1; ++i) weights.fetch(a, c, ring, i);
+    for (int i = 0; i < DownRing::kDepth - 1; ++i) weights.fetch(a, c, ring);
     pdl_wait();
     pdl_trigger();
     if (walk.at < walk.end) {
-        float* sum = sums + warp * D::kRows * a.N;
+        float* sum = sums + warp * kDownRows * a.N;
         DownWalk ahead = walk;  // the tokens', a step ahead
-        Tokens tokens;
+        Tokens<1> tokens;
         tokens.rows(c, walk.expert, 0, h, true, bytes);
         tokens.load(walk.first, bytes);
         do {
-            float acc[D::kTiles][kEights][4];
+            float acc[kTiles][1][4];
             zero(acc);
             for (int s = walk.first; s < walk.last; ++s) {
-                weights.fetch(a, c, ring, D::Ring::kDepth - 1);
-                uint4 now[kPieces][kEights];
-                const bool more = tokens.more;
-#pragma unroll
-                for (int p = 0; p < kPieces; ++p)
-#pragma unroll
-                    for (int j = 0; j < kEights; ++j) now[p][j] = tokens.v[p][j];
+                weights.fetch(a, c, ring);
+                const uint4 now[kPieces][1] = {{tokens.v[0][0]}, {tokens.v[1][0]}};
                 if (s + 1 < walk.last) {
                     tokens.load(s + 1, bytes);
-                } else if (ahead.next(c)) {
-                    tokens.rows(c, ahead.expert, ahead.pass, h, true, bytes);
+                } else if (ahead.next()) {
+                    tokens.rows(c, ahead.expert, 0, h, true, bytes);
                     tokens.load(ahead.first, bytes);
                 }
-                D::Ring::wait();
-                multiply<false>(acc, ring, now, more);
+                DownRing::wait();
+                multiply<false>(acc, ring, now, false);
                 ring.next();
             }
             down_add(a, c, sum, walk, acc);
-        } while (walk.next(c));
+        } while (walk.next());
     }
     __syncthreads();
-    for (int v = tid; v < D::kRows * a.N; v += kLayerThreads) {
+    for (int v = tid; v < kDownRows * a.N; v += kLayerThreads) {
         float o = sums[v];
 #pragma unroll
-        for (int w = 1; w < kLayerWarps; ++w) o += sums[w * D::kRows * a.N + v];
+        for (int w = 1; w < kLayerWarps; ++w) o += sums[w * kDownRows * a.N + v];
         sums[v] = o;
     }
     // the blocks' sums are joined in their order, each block an equal part of them
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    for (int v = rank * kLayerThreads + tid; v < D::kRows * a.N; v += blocks * kLayerThreads) {
-        const int row = v % D::kRows, s = v / D::kRows;  // neighbouring threads write neighbouring elements
-        if (weights.first_row + row >= a.H) continue;
+    for (int v = rank * kLayerThreads + tid; v < kDownRows * a.N; v += blocks * kLayerThreads) {
+        const int row = v % kDownRows, s = v / kDownRows;  // neighbouring threads write neighbouring elements
+        if (row >= weights.n) continue;
         float o = 0.f;
         for (uint32_t r = 0; r < blocks; ++r) o += load_cluster(sums + row * a.N + s, r);
         a.out[static_cast<int64_t>(s) * a.H + weights.first_row + row] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
@@ -664,28 +699,33 @@ namespace {
 using namespace moe_host;
 using moe::LayerArgs;
 
-template <bool Q>
-int launch_gate_up(const LayerArgs& a, cudaStream_t stream) {
-    const size_t smem = moe::kLayerWarps * (moe::GateUpRing::kWarpBytes + sizeof(float4) * moe::kGateUpTiles * 32) +
+template <bool Q, bool DOWN, int EIGHTS>
+int launch_rows(const LayerArgs& a, cudaStream_t stream) {
+    const size_t smem = moe::kLayerWarps * (moe::TileRing<DOWN>::kWarpBytes + sizeof(float4) * moe::kTiles * 32) +
                         moe::Chosen::bytes(a.N, a.K, a.E);
-    if (cudaFuncSetAttribute(moe::layer_gate_up_kernel<Q>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) !=
+    if (cudaFuncSetAttribute(moe::layer_rows_kernel<Q, DOWN, EIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
-    return launch(moe::layer_gate_up_kernel<Q>, dim3(static_cast<unsigned>(2 * num_sms())), dim3(moe::kLayerThreads),
-                  smem, stream, a);
+    return launch(moe::layer_rows_kernel<Q, DOWN, EIGHTS>, dim3(static_cast<unsigned>(2 * num_sms())), dim3(moe::kLayerThreads), smem,
+                  stream, a);
 }
 
-template <bool MANY>
 int launch_down(const LayerArgs& a, cudaStream_t stream) {
-    using D = moe::Down<MANY>;
-    const size_t smem = moe::kLayerWarps * (D::Ring::kWarpBytes + sizeof(float) * D::kRows * a.N) +
+    const size_t smem = moe::kLayerWarps * (moe::DownRing::kWarpBytes + sizeof(float) * moe::kDownRows * a.N) +
                         moe::Chosen::bytes(a.N, a.K, a.E);
-    if (cudaFuncSetAttribute(moe::layer_down_kernel<MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(moe::layer_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess)
         return MOE_ERR_CUDA;
-    const int groups = (a.H + D::kRows - 1) / D::kRows;
-    int blocks = 1;  // of a cluster: as many as keep all resident
-    while (blocks < 8 && 2 * blocks * groups <= 2 * num_sms()) blocks *= 2;
+    // Two blocks an SM, all resident: with so many rows that blocks alone fill the GPU, equal parts
+    // of them; with fewer, as many blocks to a cluster as fit (a GPC's SMs are not all filled by clusters,
+    // and one left for a second wave costs more than SMs with one block).
+    const int slots = 2 * num_sms();
+    int rows = (a.H + slots - 1) / slots, blocks = 1;
+    if (2 * rows <= moe::kDownRows) {
+        rows = moe::kDownRows;
+        while (blocks < 4 && (a.H + rows - 1) / rows * blocks * 2 <= slots) blocks *= 2;
+    }
+    if (rows > moe::kDownRows) rows = moe::kDownRows;
+    const int groups = (a.H + rows - 1) / rows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(groups * blocks));
     cfg.blockDim = dim3(moe::kLayerThreads);
@@ -699,7 +739,7 @@ int launch_down(const LayerArgs& a, cudaStream_t stream) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, moe::layer_down_kernel<MANY>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, moe::layer_down_kernel, a, rows) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
@@ -707,10 +747,12 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 }  // namespace
 
-extern "C" MOE_API size_t moe_layer_workspace_size(int N, int K, int I) {
-    if (N < 0 || N > MOE_LAYER_MAX_TOKENS || K < 1 || K > 32 || I < 8 || I % 8 != 0 || I >= 1 << 20) return 0;
+extern "C" MOE_API size_t moe_layer_workspace_size(int N, int K, int H, int I) {
+    if (N < 0 || N > MOE_LAYER_MAX_TOKENS || K < 1 || K > 32 || H < 8 || H % 8 != 0 || H >= 1 << 20 || I < 8 || I % 8 != 0 ||
+        I >= 1 << 20)
+        return 0;
     const size_t pairs = static_cast<size_t>(N > 0 ? N : 1) * K;
-    return pairs * I * 2 + 2 * round16(pairs * 4);
+    return pairs * I * 2 + (N > moe::kDownTokens ? pairs * H * 4 : 0) + 2 * round16(pairs * 4);
 }
 
 extern "C" MOE_API int moe_layer(const void* x, const float* x_scale, const float* logits, const float* bias,
@@ -730,9 +772,12 @@ extern "C" MOE_API int moe_layer(const void* x, const float* x_scale, const floa
     if (!aligned(x, 16) || !aligned(w_gate_up, 16) || !aligned(w_down, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
         !aligned(x_scale, 4) || !aligned(w_scale, 4))
         return MOE_ERR_INVALID_ARG;
+    float* y = nullptr;
     if (N > 0 && K >= 1 && K <= 32) {
-        if (workspace_bytes < moe_layer_workspace_size(N, K, I)) return MOE_ERR_CAPACITY;
+        if (workspace_bytes < moe_layer_workspace_size(N, K, H, I)) return MOE_ERR_CAPACITY;
         uint8_t* rest = static_cast<uint8_t*>(workspace) + static_cast<size_t>(N) * K * I * 2;
+        y = reinterpret_cast<float*>(rest);
+        if (N > moe::kDownTokens) rest += static_cast<size_t>(N) * K * H * 4;
         if (topk_idx == nullptr) topk_idx = reinterpret_cast<int32_t*>(rest);
         if (topk_w == nullptr) topk_w = reinterpret_cast<float*>(rest + round16(static_cast<size_t>(N) * K * 4));
     }
@@ -740,9 +785,16 @@ extern "C" MOE_API int moe_layer(const void* x, const float* x_scale, const floa
     const int rc = moe_route_topk(logits, bias, N, E, K, scoring, renormalize, n_group, topk_group, routed_scaling, topk_idx,
                                   topk_w, stream);
     if (rc != MOE_OK || N == 0) return rc;
-    const LayerArgs a = {x, x_scale, w_gate_up, w_scale, w_down, topk_idx, topk_w, static_cast<uint16_t*>(workspace), out,
-                         N, K, E, H, I};
-    const int up = q ? launch_gate_up<true>(a, stream) : launch_gate_up<false>(a, stream);
+    const LayerArgs a = {x, x_scale, w_gate_up, w_scale, w_down, topk_idx, topk_w, static_cast<uint16_t*>(workspace), y,
+                         out, N, K, E, H, I};
+    if (N <= moe::kDownTokens) {
+        const int up = q ? launch_rows<true, false, 1>(a, stream) : launch_rows<false, false, 1>(a, stream);
+        return up != MOE_OK ? up : launch_down(a, stream);
+    }
+    const int up = q ? launch_rows<true, false, 2>(a, stream) : launch_rows<false, false, 2>(a, stream);
     if (up != MOE_OK) return up;
-    return N > 8 ? launch_down<true>(a, stream) : launch_down<false>(a, stream);
+    const int down = launch_rows<false, true, 2>(a, stream);
+    if (down != MOE_OK) return down;
+    const int64_t vecs = static_cast<int64_t>(N) * (H / 8);
+    return launch(moe::layer_sum_kernel, dim3(static_cast<unsigned>((vecs + 255) / 256)), dim3(256), 0, stream, a);
 }

@@ -551,11 +551,11 @@ PyObject* layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
             refuse("at most " + std::to_string(MOE_LAYER_MAX_TOKENS) + " tokens (got " + std::to_string(N) +
                    "): plan, permute, expert_ffn and combine serve more");
         const Tensor y = output(tensor(a[13], "out"), {N, H}, kBf16, x, "out");
-        const int64_t bytes = static_cast<int64_t>(moe_layer_workspace_size(static_cast<int>(N), K, as_int(I, "I")));
+        const int64_t bytes = static_cast<int64_t>(moe_layer_workspace_size(static_cast<int>(N), K, as_int(H, "H"), as_int(I, "I")));
         const Tensor ws = empty({bytes}, at::kByte, x);
         const int rc = moe_layer(ptr<>(x), ptr<float>(x_scale), ptr<float>(logits), ptr<float>(bias), ptr<>(wgu),
                                  ptr<float>(w_scale), ptr<uint16_t>(wd), static_cast<int>(N), as_int(E, "E"),
-                                 as_int(H, "H"), static_cast<int>(I), K, dtype_of(x), scoring, renormalize, n_group,
+                                 static_cast<int>(H), static_cast<int>(I), K, dtype_of(x), scoring, renormalize, n_group,
                                  topk_group, static_cast<float>(scaling), ptr<int32_t>(idx), ptr<float>(w),
                                  ptr<uint16_t>(y), ptr<>(ws), static_cast<size_t>(bytes), stream.handle());
         stream.hand_over(y, a[13]);

@@ -609,14 +609,15 @@ MOE_API int moe_combine_backward(const uint16_t* dout, const uint16_t* y, const 
  *   topk_idx   (device) int32[N][K] and
  *   topk_w     float32[N][K]: the router's outputs, or NULL if not wanted.
  *   out        (device) bf16[N][H] out; must not alias x.
- *   workspace  (device) moe_layer_workspace_size(N, K, I) bytes, 16-byte aligned, no
+ *   workspace  (device) moe_layer_workspace_size(N, K, H, I) bytes, 16-byte aligned, no
  *              initialisation; one call at a time.
  * N <= MOE_LAYER_MAX_TOKENS (more: MOE_ERR_UNSUPPORTED; plan, permute, expert_ffn and
  * combine serve those).  H % 8 == 0 (H % 16 == 0 with e4m3), I % 8 == 0, H and I < 2^20;
- * 16-byte aligned arrays.  Three launches; N = 0 launches nothing.
+ * 16-byte aligned arrays.  Three launches, four for more than eight tokens; N = 0
+ * launches nothing.
  */
 #define MOE_LAYER_MAX_TOKENS 64
-MOE_API size_t moe_layer_workspace_size(int N, int K, int I);
+MOE_API size_t moe_layer_workspace_size(int N, int K, int H, int I);
 MOE_API int moe_layer(const void* x, const float* x_scale, const float* logits, const float* bias,
                       const void* w_gate_up, const float* w_scale, const uint16_t* w_down, int N, int E, int H, int I,
                       int K, int x_dtype, int scoring, int renormalize, int n_group, int topk_group,

@@ -75,9 +75,10 @@ LAYER = ("x", "xs", "lg", "b", "wgu", "ws", "wd", "N", "E", "H", "I", "K", "t", 
 
 def test_layer(lib):
     size = lib.moe_layer_workspace_size
-    assert size(-1, 2, 64) == 0 and size(65, 2, 64) == 0 and size(4, 0, 64) == 0 and size(4, 33, 64) == 0
-    assert size(4, 2, 60) == 0 and size(4, 2, 0) == 0 and size(4, 2, 1 << 20) == 0
-    assert size(0, 2, 64) > 0 and size(64, 32, 4096) >= 64 * 32 * (4096 * 2 + 8)
+    for bad in (dict(N=-1), dict(N=65), dict(K=0), dict(K=33), dict(H=60), dict(H=0), dict(H=1 << 20), dict(I=60), dict(I=0),
+                dict(I=1 << 20)):
+        assert size(*dict(N=4, K=2, H=64, I=64).values()) > 0 and size(*{**dict(N=4, K=2, H=64, I=64), **bad}.values()) == 0
+    assert size(0, 2, 64, 64) > 0 and size(64, 32, 64, 4096) >= 64 * 32 * (4096 * 2 + 64 * 4 + 8)
     ok = dict(x=FAKE, xs=None, lg=FAKE, b=None, wgu=FAKE, ws=None, wd=FAKE, N=4, E=8, H=64, I=40, K=2, t=0, sc=0, rn=1, ng=1,
               tg=1, rsc=1.0, idx=FAKE, w=FAKE, out=FAKE, wk=FAKE, n=1 << 30)
 
