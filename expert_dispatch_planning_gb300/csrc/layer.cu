@@ -9,9 +9,9 @@
 // weights stream from memory once, straight into the registers that the matrix
 // instruction takes them from, and everything else hides behind them.
 //
-// Three launches: moe_route_topk, gate/up, down.  Each block of the second and
-// third finds the chosen experts and their tokens by itself from topk_idx (a
-// 64-bit set of tokens for every expert).
+// Up to eight tokens: two launches, gate/up and down, each block of which routes for itself; more: the
+// router's, gate/up, down, and the sum over k.  Each block finds the chosen experts and their
+// tokens by itself (a 64-bit set of tokens for every expert).
 //
 // Products.  mma.m16n8k16 with 16 weight rows as its M side and up to 8 tokens
 // as its N side: an expert has a few tokens, and a tcgen05 tile of 64 or 128
@@ -23,12 +23,14 @@
 // (exact), their products are exact in the fp32 accumulator.
 #include <cmath>
 
+#include "route_core.cuh"
 #include "vec8.cuh"
 
 namespace moe {
 
 constexpr int kLayerThreads = 256;
 constexpr int kLayerWarps = kLayerThreads / 32;
+constexpr int kDownTokens = 8;  // at most in layer_down_kernel, whose sums are [warps][rows][N]
 
 struct LayerArgs {
     const void* x;
@@ -42,11 +44,18 @@ struct LayerArgs {
     float* y;     // [N*K][H], for many tokens
     uint16_t* out;
     int N, K, E, H, I;
+    RouteArgs route;  // of calls that choose for themselves (kRouteExperts)
 };
 
+// Code.  While weights stream through L2 they push the kernels' own instructions out of it,
+// and then every 128 bytes of code that run for the first time cost some 45 ns, on all SMs at
+// once.  So what runs before the first weights are asked for is short: loops are not unrolled,
+// steps that happen in two places are one place in the code, and what both kernels do is one
+// function, which the second finds where the first has left it (layer_token: figures).
+
 // ---------------------------------------------------------------- the chosen experts
-// In shared memory: expert[a] and begin[a] of the a-th chosen expert (begin[count]
-// = pairs), and for every place its pair, token and weight.  All threads of the block call.
+// In shared memory: expert[i] and begin[i] of the i-th chosen expert (begin[count] = pairs),
+// and for every place its pair, token and weight.
 struct Chosen {
     unsigned long long* tokens;  // [E] sets of tokens
     int* expert;                 // [slots]
@@ -56,94 +65,217 @@ struct Chosen {
     uint16_t* place;             // [E] a chosen expert's place
     uint16_t* pair;              // [N*K] flat indices s * K + k
     uint8_t* token;              // [N*K]
-    int count;
 
     static __host__ __device__ int slots(int N, int K, int E) { return N * K < E ? N * K : E; }
     static __host__ __device__ size_t bytes(int N, int K, int E) {
         const size_t s = 8 * static_cast<size_t>(E) + 4 * (2 * slots(N, K, E) + 1) + 4 * kLayerWarps + 7 * N * K + 2 * E;
         return (s + 15) / 16 * 16;
     }
-    __device__ Chosen(uint8_t* smem, const LayerArgs& a) {
-        const int n = slots(a.N, a.K, a.E);
+    __device__ Chosen(uint8_t* smem, int N, int K, int E) {
+        const int n = slots(N, K, E);
         tokens = reinterpret_cast<unsigned long long*>(smem);
-        expert = reinterpret_cast<int*>(tokens + a.E);
+        expert = reinterpret_cast<int*>(tokens + E);
         begin = expert + n;
         sums = begin + n + 1;
         weight = reinterpret_cast<float*>(sums + kLayerWarps);
-        place = reinterpret_cast<uint16_t*>(weight + a.N * a.K);
-        pair = place + a.E;
-        token = reinterpret_cast<uint8_t*>(pair + a.N * a.K);
+        place = reinterpret_cast<uint16_t*>(weight + N * K);
+        pair = place + E;
+        token = reinterpret_cast<uint8_t*>(pair + N * K);
     }
     __device__ int size(int i) const { return begin[i + 1] - begin[i]; }
-
-    // Reads topk_idx and topk_w once; `clear` comes before.
-    __device__ void clear(const LayerArgs& a) {
-        for (int e = threadIdx.x; e < a.E; e += kLayerThreads) tokens[e] = 0;
-        __syncthreads();
-    }
-    __device__ void find(const LayerArgs& a) {
-        constexpr int kMost = MOE_LAYER_MAX_TOKENS * 32 / kLayerThreads;  // pairs a thread
-        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pairs = a.N * a.K;
-        int e_of[kMost];
-        float w_of[kMost];
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int f = tid + i * kLayerThreads;
-            e_of[i] = -1;
-            if (f < pairs) {
-                e_of[i] = a.topk_idx[f];
-                w_of[i] = a.topk_w[f];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kMost; ++i)
-            if (static_cast<unsigned>(e_of[i]) < static_cast<unsigned>(a.E))
-                atomicOr(&tokens[e_of[i]], 1ull << ((tid + i * kLayerThreads) / a.K));
-        __syncthreads();
-        // a thread has a run of experts: chosen ones and pairs before it, in one word
-        const int per = (a.E + kLayerThreads - 1) / kLayerThreads, e0 = tid * per;
-        int mine = 0;
-        for (int e = e0; e < e0 + per && e < a.E; ++e)
-            if (tokens[e] != 0) mine += 0x10000 + __popcll(tokens[e]);
-        int before = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(FULL_MASK, before, o);
-            if (lane >= o) before += t;
-        }
-        if (lane == 31) sums[warp] = before;
-        __syncthreads();
-        int all = 0;
-        before -= mine;
-#pragma unroll
-        for (int w = 0; w < kLayerWarps; ++w) {
-            if (w < warp) before += sums[w];
-            all += sums[w];
-        }
-        count = all >> 16;
-        int i = before >> 16, at = before & 0xffff;
-        for (int e = e0; e < e0 + per && e < a.E; ++e) {
-            if (tokens[e] == 0) continue;
-            expert[i] = e;
-            begin[i] = at;
-            place[e] = static_cast<uint16_t>(i);
-            ++i;
-            at += __popcll(tokens[e]);
-        }
-        if (tid == 0) begin[count] = all & 0xffff;
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < kMost; ++v)
-            if (static_cast<unsigned>(e_of[v]) < static_cast<unsigned>(a.E)) {
-                const int s = (tid + v * kLayerThreads) / a.K;
-                const int p = begin[place[e_of[v]]] + __popcll(tokens[e_of[v]] & ((1ull << s) - 1));
-                token[p] = static_cast<uint8_t>(s);
-                pair[p] = static_cast<uint16_t>(tid + v * kLayerThreads);
-                weight[p] = w_of[v];
-            }
-        __syncthreads();
-    }
 };
+
+// ---- few tokens choose within the blocks that need the choice, each block for itself, a warp a
+// token: the router's rules (route_core.cuh) in a short loop over keys in shared memory.
+constexpr int kRouteExperts = 256, kRouteK = 8;
+constexpr int kRouteTokens = kLayerWarps;
+constexpr int kRouteBytes = kRouteTokens * (kRouteExperts + kRouteK) * 8;  // logits and keys, indices and weights
+
+// A winner's weights are the router's: the same sums of the same terms, 32 lanes wide.
+__device__ __noinline__ float route_weight(const RouteArgs& r, const float* raw, float val, float top) {
+    const int lane = threadIdx.x & 31;
+    const bool sigmoid = r.scoring == MOE_SCORING_SIGMOID, won = lane < r.K;
+    float num = !won ? 0.f : sigmoid ? sigmoid_weight(val) : exp_diff(val, top);
+    float hi = 0.f, lo = 0.f;
+    if (!sigmoid && !r.renormalize) {
+#pragma unroll 1
+        for (int e = lane; e < r.E; e += 32) ff_add(hi, lo, exp_diff(raw[e], top), 0.f);
+    } else if (won && r.renormalize && (!sigmoid || num >= 0x1p-100f)) {
+        ff_add(hi, lo, num, 0.f);
+    }
+    if (__any_sync(FULL_MASK, sigmoid && won && num < 0x1p-100f)) {  // rare: scores that need 64 bits
+        double score = 0.0;
+        if (won) {
+            const double ex = exp(-fabs(static_cast<double>(val)));
+            score = val >= 0.f ? 1.0 / (1.0 + ex) : ex / (1.0 + ex);
+        }
+        double den = score;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) den += __shfl_xor_sync(FULL_MASK, den, o);
+        return static_cast<float>(score * (r.renormalize ? static_cast<double>(r.scaling) / den : r.scaling));
+    }
+    if (sigmoid && !r.renormalize) return __fmul_rn(num, r.scaling);
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const float oh = __shfl_xor_sync(FULL_MASK, hi, o), ol = __shfl_xor_sync(FULL_MASK, lo, o);
+        ff_add(hi, lo, oh, ol);
+    }
+    const float q = __fdiv_rn(r.scaling, hi);
+    return __fmul_rn(num, __fmaf_rn(-q, __fdiv_rn(lo, hi), q));
+}
+
+// Token s's choice by its warp.  raw, keys: [E] of scratch.
+__device__ __forceinline__ void route_warp(const RouteArgs& r, int s, float* raw, uint32_t* keys, int32_t* idx, float* w) {
+    const int lane = threadIdx.x & 31;
+    const bool sigmoid = r.scoring == MOE_SCORING_SIGMOID;
+    // all logits are asked for at once (E is a multiple of four, at most 256)
+    const float* row = r.logits + static_cast<int64_t>(s) * r.E;
+    float4 v[2] = {};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (4 * (lane + 32 * i) < r.E) v[i] = ld_stream_f4(row + 4 * (lane + 32 * i));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (4 * (lane + 32 * i) < r.E) *reinterpret_cast<float4*>(raw + 4 * (lane + 32 * i)) = v[i];
+    __syncwarp();
+#pragma unroll 1
+    for (int e = lane; e < r.E; e += 32) {
+        float key = raw[e];
+        if (sigmoid) {
+            key = sigmoid_f32(key);
+            if (r.bias != nullptr) key = __fadd_rn(key, __ldg(r.bias + e));
+        }
+        keys[e] = order_key(key);
+    }
+    __syncwarp();
+    if (r.n_group > 1) {  // a lane a group: its two largest keys' sum; then the best groups, ties to the lower
+        const int gs = r.E / r.n_group;
+        uint32_t mine = 0u, kept = 0u;
+        if (lane < r.n_group) {
+            uint32_t k1 = 0u, k2 = 0u;  // 0 is below every key
+#pragma unroll 1
+            for (int j = 0; j < gs; ++j) {
+                const uint32_t k = keys[lane * gs + j];
+                if (k > k1) k2 = k1, k1 = k;
+                else if (k > k2) k2 = k;
+            }
+            auto value = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) != 0 ? k ^ 0x80000000u : ~k); };
+            mine = order_key(gs == 1 ? value(k1) : __fadd_rn(value(k1), value(k2)));
+        }
+#pragma unroll 1
+        for (int i = 0; i < r.topk_group; ++i) {
+            const uint32_t m = __reduce_max_sync(FULL_MASK, mine);
+            const uint32_t win = __reduce_min_sync(FULL_MASK, mine == m ? static_cast<uint32_t>(lane) : 32u);
+            kept |= 1u << win;
+            if (static_cast<uint32_t>(lane) == win) mine = 0u;
+        }
+#pragma unroll 1
+        for (int e = lane; e < r.E; e += 32)
+            if (((kept >> (e / gs)) & 1u) == 0) keys[e] = 0u;
+        __syncwarp();
+    }
+    float val = 0.f, top = 0.f;
+    int mine = 0;
+#pragma unroll 1
+    for (int k = 0; k < r.K; ++k) {
+        uint32_t best = 0u, at = 0xffffffffu;
+#pragma unroll 1
+        for (int e = lane; e < r.E; e += 32) {
+            const uint32_t key = keys[e];
+            if (key > best) best = key, at = e;  // ascending: equal keys keep the lower expert
+        }
+        const uint32_t m = __reduce_max_sync(FULL_MASK, best);
+        const uint32_t win = __reduce_min_sync(FULL_MASK, best == m ? at : 0xffffffffu);
+        const float x = raw[win < static_cast<uint32_t>(r.E) ? win : 0];
+        if (at == win) keys[win] = 0u;
+        if (k == 0) top = x;
+        if (lane == k) val = x, mine = static_cast<int>(win);
+        __syncwarp();
+    }
+    const float weight = route_weight(r, raw, val, top);
+    if (lane < r.K) {
+        idx[s * r.K + lane] = mine;
+        w[s * r.K + lane] = weight;
+    }
+}
+
+// Fills `smem` as Chosen's arrays; returns the number of chosen experts.  From the logits with
+// `scratch` (kRouteBytes), else from topk_idx and topk_w.  All threads call.
+__device__ __noinline__ int choose(uint8_t* smem, int N, int K, int E, const int32_t* topk_idx, const float* topk_w,
+                                   const RouteArgs& r, uint8_t* scratch, bool report) {
+    const Chosen c(smem, N, K, E);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pairs = N * K;
+#pragma unroll 1
+    for (int e = tid; e < E; e += kLayerThreads) c.tokens[e] = 0;
+    if (scratch != nullptr) {
+        int32_t* idx = reinterpret_cast<int32_t*>(scratch);
+        float* w = reinterpret_cast<float*>(idx + kRouteTokens * kRouteK);
+        float* raw = w + kRouteTokens * kRouteK + warp * 2 * kRouteExperts;
+        if (warp < N) route_warp(r, warp, raw, reinterpret_cast<uint32_t*>(raw + kRouteExperts), idx, w);
+        topk_idx = idx;
+        topk_w = w;
+    }
+    __syncthreads();
+    if (report && tid < pairs) {
+        if (r.topk_idx != nullptr) r.topk_idx[tid] = topk_idx[tid];
+        if (r.topk_w != nullptr) r.topk_w[tid] = topk_w[tid];
+    }
+    auto chosen = [&](int f) {  // the pair's expert; -1 for an index that the router does not give
+        const int e = topk_idx[f];
+        return static_cast<unsigned>(e) < static_cast<unsigned>(E) ? e : -1;
+    };
+#pragma unroll 1
+    for (int f = tid; f < pairs; f += kLayerThreads) {
+        const int e = chosen(f);
+        if (e >= 0) atomicOr(&c.tokens[e], 1ull << (f / K));
+    }
+    __syncthreads();
+    // a thread has a run of experts: chosen ones and pairs before it, in one word
+    const int per = (E + kLayerThreads - 1) / kLayerThreads, e0 = tid * per, e1 = e0 + per < E ? e0 + per : E;
+    int mine = 0;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e)
+        if (c.tokens[e] != 0) mine += 0x10000 + __popcll(c.tokens[e]);
+    int before = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(FULL_MASK, before, o);
+        if (lane >= o) before += t;
+    }
+    if (lane == 31) c.sums[warp] = before;
+    __syncthreads();
+    int all = 0;
+    before -= mine;
+#pragma unroll 1
+    for (int w = 0; w < kLayerWarps; ++w) {
+        if (w < warp) before += c.sums[w];
+        all += c.sums[w];
+    }
+    const int count = all >> 16;
+    int i = before >> 16, at = before & 0xffff;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+        if (c.tokens[e] == 0) continue;
+        c.expert[i] = e;
+        c.begin[i] = at;
+        c.place[e] = static_cast<uint16_t>(i);
+        ++i;
+        at += __popcll(c.tokens[e]);
+    }
+    if (tid == 0) c.begin[count] = all & 0xffff;
+    __syncthreads();
+#pragma unroll 1
+    for (int f = tid; f < pairs; f += kLayerThreads) {
+        const int e = chosen(f);
+        if (e < 0) continue;
+        const int s = f / K, p = c.begin[c.place[e]] + __popcll(c.tokens[e] & ((1ull << s) - 1));
+        c.token[p] = static_cast<uint8_t>(s);
+        c.pair[p] = static_cast<uint16_t>(f);
+        c.weight[p] = topk_w[f];
+    }
+    __syncthreads();
+    return count;
+}
 
 // ---------------------------------------------------------------- products
 // Sixteen bytes of a row as the matrix instruction's words: eight bf16, or
@@ -250,7 +382,7 @@ struct WeightRing {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const bool in = (HALVES ? 8 * m : 16 * m + 8 * half) + 4 * i + r < w.n && mine < bytes;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + (4 * (2 * m + half) + 2 * i) * 256),
+                    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(slot + (4 * (2 * m + half) + 2 * i) * 256),
                                  "l"(in ? eight + i * w.four : w.any), "r"(in ? 16 : 0)
                                  : "memory");
                 }
@@ -342,59 +474,40 @@ template <bool DOWN>
 using TileRing = WeightRing<kTiles, !DOWN, 3>;
 
 // A walk over a block's run: tile by tile (32 rows of one expert, or 16 channels with two rows
-// each), pass by pass (those after the first find the tile's weights in L2),
-// and over the warp's steps of k.
+// each), pass by pass (those after the first find the tile's weights in L2), and over the warp's
+// steps of k, which are kLayerWarps apart: what the block's warps ask for at one time is contiguous.
 template <bool DOWN, int EIGHTS>
 struct TileWalk {
     static constexpr int kUnits = DOWN ? 16 * kTiles : 8 * kTiles;
-    int64_t at, end;
-    int expert, unit, n;  // the tile at hand: its expert's place among the chosen, first row or channel, their number
+    int left;             // units (rows or channels) of the run from this tile on; 0: the walk has ended
+    int expert, unit, n;  // the tile at hand: its expert's place among the chosen, first unit, their number
     int pass, passes, step;
-    __device__ void tile(const Chosen& c, int units) {
-        pass = 0;
-        passes = 0;
-        if (at >= end) return;
-        expert = static_cast<int>(at / units);
-        unit = static_cast<int>(at - static_cast<int64_t>(expert) * units);
+    bool fresh;           // nothing has been derived from the tile or pass yet
+    __device__ __forceinline__ void tile(const Chosen& c, int units) {
         n = units - unit < kUnits ? units - unit : kUnits;
-        if (end - at < n) n = static_cast<int>(end - at);
+        if (left < n) n = left;
+        pass = 0;
         passes = (c.size(expert) + 8 * EIGHTS - 1) / (8 * EIGHTS);
     }
     // To the next pass or tile; whether there is one.
-    __device__ bool next(const Chosen& c, int units) {
+    __device__ __forceinline__ bool next(const Chosen& c, int units) {
+        fresh = true;
         if (++pass < passes) return true;
-        at += n;
-        tile(c, units);
-        return at < end;
-    }
-};
-
-// Where the ring asks for weights.  The warp's steps are kLayerWarps apart: what the block's warps
-// ask for at one time is contiguous.
-template <bool Q, bool DOWN, int EIGHTS>
-struct TileWeights {
-    TileWalk<DOWN, EIGHTS> walk;
-    WeightRows w;
-    __device__ void rows(const LayerArgs& a, const Chosen& c) {
-        if (walk.at >= walk.end) return;
-        const int64_t row = DOWN ? 2 * static_cast<int64_t>(a.I) : static_cast<int64_t>(a.H) * (Q ? 1 : 2);
-        w.four = 4 * row;
-        w.half = DOWN ? 8 * row : a.I * row;
-        w.tile = DOWN ? 16 * row : 8 * row;
-        if constexpr (DOWN) w.set(a.w_down, static_cast<int64_t>(c.expert[walk.expert]) * a.H + walk.unit, row, walk.n);
-        else w.set(a.w_gate_up, static_cast<int64_t>(c.expert[walk.expert]) * 2 * a.I + walk.unit, row, walk.n);
-    }
-    __device__ __forceinline__ void fetch(const LayerArgs& a, const Chosen& c, TileRing<DOWN>& ring, int warp, int steps,
-                                          int bytes) {
-        if (walk.at < walk.end && warp < steps) {
-            ring.fetch(w, walk.step * kStepBytes, bytes);
-            if ((walk.step += kLayerWarps) >= steps) {
-                walk.step = warp;
-                walk.next(c, DOWN ? a.H : a.I);
-                rows(a, c);
-            }
+        left -= n;
+        if (left == 0) return false;
+        unit += n;
+        if (unit == units) {
+            unit = 0;
+            ++expert;
         }
-        TileRing<DOWN>::commit();
+        tile(c, units);
+        return true;
+    }
+    // To the warp's next step.
+    __device__ __forceinline__ void advance(const Chosen& c, int units, int warp, int steps) {
+        if ((step += kLayerWarps) < steps) return;
+        step = warp;
+        next(c, units);
     }
 };
 
@@ -463,60 +576,94 @@ template <bool Q, bool DOWN, int EIGHTS>
 __global__ void __launch_bounds__(kLayerThreads, 2) layer_rows_kernel(const LayerArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     using Ring = TileRing<DOWN>;
+    static_assert(kRouteBytes <= kLayerWarps * Ring::kWarpBytes, "the ring's place is the router's scratch");
     Ring ring(smem);
     float4* sum = reinterpret_cast<float4*>(smem + kLayerWarps * Ring::kWarpBytes);
-    Chosen c(reinterpret_cast<uint8_t*>(sum + kLayerWarps * kTiles * 32), a);
-    c.clear(a);
+    uint8_t* lists = reinterpret_cast<uint8_t*>(sum + kLayerWarps * kTiles * 32);
+    const Chosen c(lists, a.N, a.K, a.E);
     if constexpr (!DOWN) {
         pdl_wait();
         pdl_trigger();
     }
-    c.find(a);  // (of the down product topk_idx and the weights come from before the launch that this one may overlap)
+    // (of the down product topk_idx and the weights come from before the launch that this one may overlap)
+    const int count = choose(lists, a.N, a.K, a.E, a.topk_idx, a.topk_w, a.route, a.topk_idx == nullptr ? smem : nullptr,
+                             !DOWN && a.topk_idx == nullptr && blockIdx.x == 0);
     const int warp = threadIdx.x >> 5, units = DOWN ? a.H : a.I;
     const int bytes = DOWN ? 2 * a.I : a.H * (Q ? 1 : 2), steps = (bytes + kStepBytes - 1) / kStepBytes;
     const uint8_t* x = static_cast<const uint8_t*>(DOWN ? a.h : a.x);
-    const int64_t all = static_cast<int64_t>(c.count) * units;
+    const unsigned all = static_cast<unsigned>(count) * units, per = all / gridDim.x, rest = all - per * gridDim.x;
+    const unsigned begin = blockIdx.x * per + (blockIdx.x < rest ? blockIdx.x : rest);
     TileWalk<DOWN, EIGHTS> walk;
-    walk.at = blockIdx.x * all / gridDim.x;
-    walk.end = (blockIdx.x + 1) * all / gridDim.x;
-    walk.step = warp;
-    walk.tile(c, units);
-    TileWeights<Q, DOWN, EIGHTS> weights;
-    weights.walk = walk;
-    weights.rows(a, c);
-    for (int i = 0; i < Ring::kDepth - 1; ++i) weights.fetch(a, c, ring, warp, steps, bytes);
-    if constexpr (DOWN) {
+    walk.left = static_cast<int>(per + (blockIdx.x < rest ? 1 : 0));
+    if (DOWN && (walk.left == 0 || warp >= steps)) {
         pdl_wait();
         pdl_trigger();
     }
-    if (walk.at >= walk.end) return;
-    TileWalk<DOWN, EIGHTS> ahead = walk;  // the tokens', a step ahead
+    if (walk.left == 0) return;
+    walk.expert = static_cast<int>(begin / units);
+    walk.unit = static_cast<int>(begin) - walk.expert * units;
+    walk.step = warp;
+    walk.fresh = true;
+    walk.tile(c, units);
+    TileWalk<DOWN, EIGHTS> weights = walk, ahead = walk;  // the ring's, and the tokens', a step ahead
+    WeightRows w;
     Tokens<EIGHTS> tokens;
-    tokens.rows(c, walk.expert, 0, x, DOWN, bytes);
-    if (warp < steps) tokens.load(warp, bytes);
-    do {
-        float acc[kTiles][EIGHTS][4];
-        zero(acc);
-        for (int s = warp; s < steps; s += kLayerWarps) {
-            weights.fetch(a, c, ring, warp, steps, bytes);
+    float acc[kTiles][EIGHTS][4];
+    zero(acc);
+    int lead = warp < steps ? Ring::kDepth - 1 : 0;  // steps to ask for before the first product
+    while (true) {
+        if (warp < steps) {
+            if (weights.left != 0) {
+                if (weights.fresh) {
+                    const int64_t row = DOWN ? 2 * static_cast<int64_t>(a.I) : static_cast<int64_t>(a.H) * (Q ? 1 : 2);
+                    w.four = 4 * row;
+                    w.half = DOWN ? 8 * row : a.I * row;
+                    w.tile = DOWN ? 16 * row : 8 * row;
+                    const int64_t first = static_cast<int64_t>(c.expert[weights.expert]) * (DOWN ? a.H : 2 * a.I) + weights.unit;
+                    w.set(DOWN ? static_cast<const void*>(a.w_down) : a.w_gate_up, first, row, weights.n);
+                    weights.fresh = false;
+                }
+                ring.fetch(w, weights.step * kStepBytes, bytes);
+                weights.advance(c, units, warp, steps);
+            }
+            Ring::commit();
+            if (lead > 1) {
+                --lead;
+                continue;
+            }
+            if (DOWN && lead == 1) {
+                pdl_wait();
+                pdl_trigger();
+            }
             uint4 now[kPieces][EIGHTS];
             const bool more = tokens.more;
 #pragma unroll
             for (int p = 0; p < kPieces; ++p)
 #pragma unroll
                 for (int j = 0; j < EIGHTS; ++j) now[p][j] = tokens.v[p][j];
-            if (s + kLayerWarps < steps) {
-                tokens.load(s + kLayerWarps, bytes);
-            } else if (ahead.next(c, units)) {
-                tokens.rows(c, ahead.expert, ahead.pass, x, DOWN, bytes);
-                tokens.load(warp, bytes);
+            if (ahead.left != 0) {
+                if (ahead.fresh) {
+                    tokens.rows(c, ahead.expert, ahead.pass, x, DOWN, bytes);
+                    ahead.fresh = false;
+                }
+                tokens.load(ahead.step, bytes);
+                ahead.advance(c, units, warp, steps);
+            }
+            if (lead == 1) {
+                lead = 0;
+                continue;
             }
             Ring::wait();
             multiply<Q>(acc, ring, now, more);
             ring.next();
         }
-        join<Q, DOWN>(a, c, sum, walk, acc);
-    } while (walk.next(c, units));
+        if ((walk.step += kLayerWarps) >= steps) {
+            join<Q, DOWN>(a, c, sum, walk, acc);
+            if (!walk.next(c, units)) break;
+            zero(acc);
+            walk.step = warp;
+        }
+    }
 }
 
 // out[s] = bf16 of the sum of its pairs' y, in the order of k: a thread eight elements.
@@ -541,55 +688,28 @@ __global__ void __launch_bounds__(256) layer_sum_kernel(const LayerArgs a) {
 // ---------------------------------------------------------------- down, few tokens
 // A walk over a warp's run of the chosen experts' steps of k: one expert's (its part) after the other.
 struct DownWalk {
-    int at, end, steps;
-    int expert, first, last;  // the part at hand: the expert's place among the chosen, its steps
-    int step;
-    __device__ void part() {
-        if (at >= end) return;
-        expert = at / steps;
-        step = first = at - expert * steps;
-        last = end - at < steps - first ? first + end - at : steps;
-    }
-    __device__ bool next() {
-        at += last - first;
-        part();
-        return at < end;
+    int left, steps;   // steps of the run from this one on; an expert's
+    int expert, step;  // the expert's place among the chosen, the step of it
+    bool fresh;        // nothing has been derived from the expert yet
+    // To the next step; whether it begins another expert or the run has ended.
+    __device__ __forceinline__ bool advance() {
+        if (++step == steps) {
+            step = 0;
+            ++expert;
+            fresh = true;
+        }
+        return --left == 0 || step == 0;
     }
 };
 
-constexpr int kDownTokens = 8;  // at most: the block's sums are [warps][rows][N]
 constexpr int kDownRows = 16 * kTiles;
 using DownRing = WeightRing<kTiles, false, 3>;
 
-struct DownWeights {
-    DownWalk walk;
-    WeightRows w;
-    int first_row, n;  // the cluster's rows
-    __device__ void rows(const LayerArgs& a, const Chosen& c) {
-        if (walk.at >= walk.end) return;
-        const int64_t row = static_cast<int64_t>(a.I) * 2;
-        w.four = 4 * row;
-        w.half = 8 * row;
-        w.tile = 16 * row;
-        w.set(a.w_down, static_cast<int64_t>(c.expert[walk.expert]) * a.H + first_row, row, n);
-    }
-    __device__ __forceinline__ void fetch(const LayerArgs& a, const Chosen& c, DownRing& ring) {
-        if (walk.at < walk.end) {
-            ring.fetch(w, walk.step * kStepBytes, 2 * a.I);
-            if (++walk.step >= walk.last) {
-                walk.next();
-                rows(a, c);
-            }
-        }
-        DownRing::commit();
-    }
-};
-
 // A part's products, weighted, are added to the warp's sums [rows][N].
-__device__ __forceinline__ void down_add(const LayerArgs& a, const Chosen& c, float* sum, const DownWalk& walk,
+__device__ __forceinline__ void down_add(const LayerArgs& a, const Chosen& c, float* sum, int expert,
                                          const float (&acc)[kTiles][1][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int first = c.begin[walk.expert], cols = c.size(walk.expert);
+    const int first = c.begin[expert], cols = c.size(expert);
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
         const int p = 2 * t + v;
@@ -621,60 +741,84 @@ __global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const Laye
     extern __shared__ __align__(128) uint8_t smem[];
     DownRing ring(smem);
     float* sums = reinterpret_cast<float*>(smem + kLayerWarps * DownRing::kWarpBytes);  // [warps][rows][N]
-    Chosen c(reinterpret_cast<uint8_t*>(sums) + sizeof(float) * kLayerWarps * kDownRows * a.N, a);
+    uint8_t* lists = reinterpret_cast<uint8_t*>(sums) + sizeof(float) * kLayerWarps * kDownRows * a.N;
+    const Chosen c(lists, a.N, a.K, a.E);
     const int tid = threadIdx.x, warp = tid >> 5;
     uint32_t rank, blocks;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(blocks));
+#pragma unroll 1
     for (int v = tid; v < kLayerWarps * kDownRows * a.N; v += kLayerThreads) sums[v] = 0.f;
-    // topk_idx and the weights come from before the launch that this one may overlap
-    c.clear(a);
-    c.find(a);
+    // topk_idx or the logits, and the weights, come from before the launch that this one may overlap
+    const int count =
+        choose(lists, a.N, a.K, a.E, a.topk_idx, a.topk_w, a.route, a.topk_idx == nullptr ? smem : nullptr, false);
     const uint8_t* h = reinterpret_cast<const uint8_t*>(a.h);
-    const int bytes = 2 * a.I;
+    const int bytes = 2 * a.I, first_row = static_cast<int>(blockIdx.x / blocks) * rows;
+    const int there = a.H - first_row < rows ? a.H - first_row : rows;
+    // equal parts of the steps, to a step, for the cluster's warps
     DownWalk walk;
     walk.steps = (bytes + kStepBytes - 1) / kStepBytes;
-    const int64_t all = static_cast<int64_t>(c.count) * walk.steps, me = rank * kLayerWarps + warp, of = blocks * kLayerWarps;
-    walk.at = static_cast<int>(me * all / of);
-    walk.end = static_cast<int>((me + 1) * all / of);
-    walk.part();
-    DownWeights weights;
-    weights.walk = walk;
-    weights.first_row = static_cast<int>(blockIdx.x / blocks) * rows;
-    weights.n = a.H - weights.first_row < rows ? a.H - weights.first_row : rows;
-    weights.rows(a, c);
-    for (int i = 0; i < DownRing::kDepth - 1; ++i) weights.fetch(a, c, ring);
-    pdl_wait();
-    pdl_trigger();
-    if (walk.at < walk.end) {
-        float* sum = sums + warp * kDownRows * a.N;
-        DownWalk ahead = walk;  // the tokens', a step ahead
-        Tokens<1> tokens;
-        tokens.rows(c, walk.expert, 0, h, true, bytes);
-        tokens.load(walk.first, bytes);
-        do {
-            float acc[kTiles][1][4];
-            zero(acc);
-            for (int s = walk.first; s < walk.last; ++s) {
-                weights.fetch(a, c, ring);
-                const uint4 now[kPieces][1] = {{tokens.v[0][0]}, {tokens.v[1][0]}};
-                if (s + 1 < walk.last) {
-                    tokens.load(s + 1, bytes);
-                } else if (ahead.next()) {
-                    tokens.rows(c, ahead.expert, 0, h, true, bytes);
-                    tokens.load(ahead.first, bytes);
-                }
-                DownRing::wait();
-                multiply<false>(acc, ring, now, false);
-                ring.next();
+    const unsigned all = static_cast<unsigned>(count) * walk.steps, me = rank * kLayerWarps + warp, of = blocks * kLayerWarps;
+    const unsigned per = all / of, rest = all - per * of, begin = me * per + (me < rest ? me : rest);
+    walk.left = static_cast<int>(per + (me < rest ? 1 : 0));
+    walk.expert = static_cast<int>(begin / walk.steps);
+    walk.step = static_cast<int>(begin) - walk.expert * walk.steps;
+    walk.fresh = true;
+    DownWalk weights = walk, ahead = walk;  // the ring's, and the tokens', a step ahead
+    WeightRows w;
+    Tokens<1> tokens;
+    float* sum = sums + warp * kDownRows * a.N;
+    float acc[kTiles][1][4];
+    zero(acc);
+    int lead = DownRing::kDepth - 1;  // steps to ask for before the first product
+    while (walk.left != 0 || lead != 0) {
+        if (weights.left != 0) {
+            if (weights.fresh) {
+                const int64_t row = bytes;
+                w.four = 4 * row;
+                w.half = 8 * row;
+                w.tile = 16 * row;
+                w.set(a.w_down, static_cast<int64_t>(c.expert[weights.expert]) * a.H + first_row, row, there);
+                weights.fresh = false;
             }
-            down_add(a, c, sum, walk, acc);
-        } while (walk.next());
+            ring.fetch(w, weights.step * kStepBytes, bytes);
+            weights.advance();
+        }
+        DownRing::commit();
+        if (lead > 1) {
+            --lead;
+            continue;
+        }
+        if (lead == 1) {
+            pdl_wait();
+            pdl_trigger();
+        }
+        const uint4 now[kPieces][1] = {{tokens.v[0][0]}, {tokens.v[1][0]}};
+        if (ahead.left != 0) {
+            if (ahead.fresh) {
+                tokens.rows(c, ahead.expert, 0, h, true, bytes);
+                ahead.fresh = false;
+            }
+            tokens.load(ahead.step, bytes);
+            ahead.advance();
+        }
+        if (lead == 1) {
+            lead = 0;
+            continue;
+        }
+        DownRing::wait();
+        multiply<false>(acc, ring, now, false);
+        ring.next();
+        const int expert = walk.expert;
+        if (walk.advance()) {
+            down_add(a, c, sum, expert, acc);
+            zero(acc);
+        }
     }
     __syncthreads();
     for (int v = tid; v < kDownRows * a.N; v += kLayerThreads) {
         float o = sums[v];
-#pragma unroll
+#pragma unroll 1
         for (int w = 1; w < kLayerWarps; ++w) o += sums[w * kDownRows * a.N + v];
         sums[v] = o;
     }
@@ -682,10 +826,10 @@ __global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const Laye
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     for (int v = rank * kLayerThreads + tid; v < kDownRows * a.N; v += blocks * kLayerThreads) {
         const int row = v % kDownRows, s = v / kDownRows;  // neighbouring threads write neighbouring elements
-        if (row >= weights.n) continue;
+        if (row >= there) continue;
         float o = 0.f;
         for (uint32_t r = 0; r < blocks; ++r) o += load_cluster(sums + row * a.N + s, r);
-        a.out[static_cast<int64_t>(s) * a.H + weights.first_row + row] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+        a.out[static_cast<int64_t>(s) * a.H + first_row + row] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
     }
     // a block's sums stay until the others have read them
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -773,6 +917,8 @@ extern "C" MOE_API int moe_layer(const void* x, const float* x_scale, const floa
         !aligned(x_scale, 4) || !aligned(w_scale, 4))
         return MOE_ERR_INVALID_ARG;
     float* y = nullptr;
+    int32_t* const wanted_idx = topk_idx;
+    float* const wanted_w = topk_w;
     if (N > 0 && K >= 1 && K <= 32) {
         if (workspace_bytes < moe_layer_workspace_size(N, K, H, I)) return MOE_ERR_CAPACITY;
         uint8_t* rest = static_cast<uint8_t*>(workspace) + static_cast<size_t>(N) * K * I * 2;
@@ -781,13 +927,23 @@ extern "C" MOE_API int moe_layer(const void* x, const float* x_scale, const floa
         if (topk_idx == nullptr) topk_idx = reinterpret_cast<int32_t*>(rest);
         if (topk_w == nullptr) topk_w = reinterpret_cast<float*>(rest + round16(static_cast<size_t>(N) * K * 4));
     }
-    // the router's own checks of logits, bias, E, K and its options come with its call
-    const int rc = moe_route_topk(logits, bias, N, E, K, scoring, renormalize, n_group, topk_group, routed_scaling, topk_idx,
-                                  topk_w, stream);
-    if (rc != MOE_OK || N == 0) return rc;
-    const LayerArgs a = {x, x_scale, w_gate_up, w_scale, w_down, topk_idx, topk_w, static_cast<uint16_t*>(workspace), y,
-                         out, N, K, E, H, I};
-    if (N <= moe::kDownTokens) {
+    LayerArgs a = {x, x_scale, w_gate_up, w_scale, w_down, topk_idx, topk_w, static_cast<uint16_t*>(workspace), y,
+                   out, N, K, E, H, I, {}};
+    const bool few = N <= moe::kDownTokens;
+    if (few && E <= moe::kRouteExperts && E % 4 == 0 && K <= moe::kRouteK) {
+        const int rc = route_args(logits, bias, N, E, K, scoring, renormalize, n_group, topk_group, routed_scaling, topk_idx,
+                                  topk_w, &a.route);
+        if (rc != MOE_OK || N == 0) return rc;
+        a.route.topk_idx = wanted_idx;
+        a.route.topk_w = wanted_w;
+        a.topk_idx = nullptr;  // the blocks route
+    } else {
+        // the router's own checks of logits, bias, E, K and its options come with its call
+        const int rc = moe_route_topk(logits, bias, N, E, K, scoring, renormalize, n_group, topk_group, routed_scaling,
+                                      topk_idx, topk_w, stream);
+        if (rc != MOE_OK || N == 0) return rc;
+    }
+    if (few) {
         const int up = q ? launch_rows<true, false, 1>(a, stream) : launch_rows<false, false, 1>(a, stream);
         return up != MOE_OK ? up : launch_down(a, stream);
     }
