@@ -159,6 +159,123 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) block_norm_kernel(cons
     }
 }
 
+// ---------------------------------------------------------------- ring
+// R: the residual's element type.
+template <int SLOTS, typename R, int GATE>
+__global__ void __launch_bounds__(kRingThreads) block_norm_ring_kernel(const BlockNormArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];  // [SLOTS][x row, gate row, residual row]
+    __shared__ float buf[2][3][32];
+    pdl_wait();
+    pdl_trigger();
+    const int T = blockDim.x, H = a.H;
+    constexpr int kGateBytes = GATE == kFullGate ? 2 : 0;
+    const uint32_t slot_bytes = static_cast<uint32_t>(H) * (2 + kGateBytes + sizeof(R));
+    const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.N / gridDim.x;
+    const int64_t end = (static_cast<int64_t>(blockIdx.x) + 1) * a.N / gridDim.x;
+    auto fetch = [&](int64_t row, uint32_t slot) {
+        if (row < end) {
+            uint16_t* x = reinterpret_cast<uint16_t*>(smem + slot * slot_bytes);
+            R* r = reinterpret_cast<R*>(x + H + H * kGateBytes / 2);
+#pragma unroll
+            for (int i = 0; i < kRingGroups; ++i) {
+                const int h = 4 * (threadIdx.x + i * T);
+                if (h < H) {
+                    cp_async_group(x + h, a.x + row * H + h);
+                    cp_async_group(r + h, static_cast<const R*>(a.residual) + row * H + h);
+                    if constexpr (GATE == kFullGate)
+                        cp_async_group(x + H + h, static_cast<const uint16_t*>(a.gate) + row * H + h);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float wp[kRingGroups][4], w[kRingGroups][4];
+#pragma unroll
+    for (int i = 0; i < kRingGroups; ++i) {
+        const int h = 4 * (threadIdx.x + i * T);
+        if (h < H) {
+            load_weight4(a.post_weight, a.post_f32, h, wp[i]);
+            load_weight4(a.weight, a.weight_f32, h, w[i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < SLOTS - 1; ++j) fetch(begin + j, j);
+    float next_gate = GATE == kTokenGate && begin < end ? __ldg(static_cast<const float*>(a.gate) + begin) : 1.f;
+    uint32_t slot = 0;  // the row's
+    for (int64_t row = begin; row < end; ++row, slot = (slot + 1) % SLOTS) {
+        fetch(row + SLOTS - 1, (slot + SLOTS - 1) % SLOTS);
+        const float token_gate = next_gate;
+        if (GATE == kTokenGate && row + 1 < end) next_gate = __ldg(static_cast<const float*>(a.gate) + row + 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+        const uint16_t* x = reinterpret_cast<const uint16_t*>(smem + slot * slot_bytes);
+        const R* r = reinterpret_cast<const R*>(x + H + H * kGateBytes / 2);
+        const int64_t at = row * H;
+        float(*sums)[32] = buf[row & 1];
+        float s[kRingGroups][4];
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) {
+                load4(x + h, s[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float t = s[i][j] * a.down;
+                    ss = fmaf(t, t, ss);
+                }
+            }
+        }
+        ss = block_reduce<false>(ss, sums[0]);
+        const float post = rsqrtf(fmaf(ss, a.mean, a.eps));  // within 2^-22
+        if (threadIdx.x == 0) a.post_rstd[row] = post;
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) {
+                float q[4], g[4];
+                load4(r + h, q);
+                if constexpr (GATE == kFullGate) load4(x + H + h, g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float n = s[i][j] * post * wp[i][j];
+                    if constexpr (GATE == kTokenGate) n *= token_gate;
+                    if constexpr (GATE == kFullGate) n *= g[j];
+                    s[i][j] = fmaf(a.alpha, q[j], n);
+                    const float t = s[i][j] * a.down;
+                    ss = fmaf(t, t, ss);
+                }
+                store4(static_cast<R*>(a.residual_out) + at + h, s[i]);
+            }
+        }
+        ss = block_reduce<false>(ss, sums[1]);
+        const float rstd = rsqrtf(fmaf(ss, a.mean, a.eps));
+        if (threadIdx.x == 0) a.rstd[row] = rstd;
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = s[i][j] * rstd * w[i][j];
+                    amax = fmaxf(amax, fabsf(s[i][j]));
+                }
+                store4(a.y + at + h, s[i]);
+            }
+        }
+        if (a.q == nullptr) continue;
+        amax = block_reduce<true>(amax, sums[2]);
+        const Quantum q = quantum_of(amax);
+        if (threadIdx.x == 0) a.q_scale[row] = q.scale;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) *reinterpret_cast<uint32_t*>(a.q + at + h) = q.round4(s[i]);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- backward
 struct BlockNormBackwardArgs {
     const uint16_t* dy;
@@ -313,6 +430,154 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) block_norm_backward_ke
     }
 }
 
+// A thread reads its columns' values from the ring anew in each of the row's three parts: in
+// registers there is only room for what has no other place (the weights' sums and d).
+template <int SLOTS, typename S, int GATE, bool DS>
+__global__ void __launch_bounds__(kRingThreads) block_norm_backward_ring_kernel(const BlockNormBackwardArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];  // [SLOTS][dy row, x row, gate row, s row, ds row]
+    __shared__ float buf[2][2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int T = blockDim.x, H = a.H;
+    constexpr int kNarrow = GATE == kFullGate ? 3 : 2;  // rows of two bytes an element
+    const uint32_t slot_bytes = static_cast<uint32_t>(H) * (2 * kNarrow + (DS ? 2 : 1) * sizeof(S));
+    const float over_h = 1.f / static_cast<float>(H);
+    const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.N / gridDim.x;
+    const int64_t end = (static_cast<int64_t>(blockIdx.x) + 1) * a.N / gridDim.x;
+    auto fetch = [&](int64_t row, uint32_t slot) {
+        if (row < end) {
+            uint16_t* dy = reinterpret_cast<uint16_t*>(smem + slot * slot_bytes);
+            S* s = reinterpret_cast<S*>(dy + kNarrow * H);
+#pragma unroll
+            for (int i = 0; i < kRingGroups; ++i) {
+                const int h = 4 * (threadIdx.x + i * T);
+                if (h < H) {
+                    cp_async_group(dy + h, a.dy + row * H + h);
+                    cp_async_group(s + h, static_cast<const S*>(a.s) + row * H + h);
+                    cp_async_group(dy + H + h, a.x + row * H + h);
+                    if constexpr (DS) cp_async_group(s + H + h, static_cast<const S*>(a.ds) + row * H + h);
+                    if constexpr (GATE == kFullGate)
+                        cp_async_group(dy + 2 * H + h, static_cast<const uint16_t*>(a.gate) + row * H + h);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float w[kRingGroups][4], wp[kRingGroups][4], acc[kRingGroups][4], post_acc[kRingGroups][4];
+#pragma unroll
+    for (int i = 0; i < kRingGroups; ++i) {
+        const int h = 4 * (threadIdx.x + i * T);
+        if (h < H) {
+            load_weight4(a.weight, a.weight_f32, h, w[i]);
+            load_weight4(a.post_weight, a.post_f32, h, wp[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = post_acc[i][j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < SLOTS - 1; ++j) fetch(begin + j, j);
+    uint32_t slot = 0;  // the row's
+    float next_rstd = 0.f, next_post = 0.f, next_gate = 1.f;
+    auto scalars = [&](int64_t row) {
+        if (row >= end) return;
+        next_rstd = __ldg(a.rstd + row);
+        next_post = __ldg(a.post_rstd + row);
+        if constexpr (GATE == kTokenGate) next_gate = __ldg(static_cast<const float*>(a.gate) + row);
+    };
+    scalars(begin);
+    for (int64_t row = begin; row < end; ++row, slot = (slot + 1) % SLOTS) {
+        fetch(row + SLOTS - 1, (slot + SLOTS - 1) % SLOTS);
+        const float rstd = next_rstd, post = next_post, token_gate = next_gate;
+        scalars(row + 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+        const uint16_t* dy = reinterpret_cast<const uint16_t*>(smem + slot * slot_bytes);
+        const S* s = reinterpret_cast<const S*>(dy + kNarrow * H);
+        const int64_t at = row * H;
+        float(*sums)[32] = buf[row & 1];
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) {
+                float t[4], hat[4];
+                load4(dy + h, t);
+                load4(s + h, hat);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    hat[j] *= rstd;
+                    acc[i][j] = fmaf(t[j], hat[j], acc[i][j]);
+                    dot = fmaf(t[j] * w[i][j], hat[j], dot);
+                }
+            }
+        }
+        const float mean = block_reduce<false>(dot, sums[0]) * over_h;
+        float d[kRingGroups][4];
+        dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) {
+                float t[4], v[4], o[4];
+                load4(dy + h, t);
+                load4(s + h, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
+                if constexpr (DS) load4(s + H + h, d[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    d[i][j] += rstd * (t[j] * w[i][j] - v[j] * rstd * mean);
+                    o[j] = a.alpha * d[i][j];
+                }
+                store4(static_cast<S*>(a.dres) + at + h, o);
+                load4(dy + H + h, v);
+                if constexpr (GATE == kFullGate) load4(dy + 2 * H + h, t);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] *= post;
+                    const float n = v[j] * wp[i][j];
+                    if constexpr (GATE == kFullGate) {
+                        o[j] = d[i][j] * n;
+                        d[i][j] *= t[j];
+                        dot = fmaf(d[i][j], n, dot);
+                    } else {
+                        dot = fmaf(d[i][j], n, dot);
+                        d[i][j] *= token_gate;
+                    }
+                    post_acc[i][j] = fmaf(d[i][j], v[j], post_acc[i][j]);
+                    d[i][j] *= wp[i][j];
+                }
+                if constexpr (GATE == kFullGate) store4(static_cast<uint16_t*>(a.dgate) + at + h, o);
+            }
+        }
+        dot = block_reduce<false>(dot, sums[1]);
+        if constexpr (GATE == kTokenGate) {
+            if (threadIdx.x == 0) static_cast<float*>(a.dgate)[row] = dot;
+            dot *= token_gate;
+        }
+        const float post_mean = dot * over_h;
+#pragma unroll
+        for (int i = 0; i < kRingGroups; ++i) {
+            const int h = 4 * (threadIdx.x + i * T);
+            if (h < H) {
+                float v[4];
+                load4(dy + H + h, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[i][j] = post * (d[i][j] - v[j] * post * post_mean);
+                store4(a.dx + at + h, d[i]);
+            }
+        }
+    }
+    float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * H;
+#pragma unroll
+    for (int i = 0; i < kRingGroups; ++i) {
+        const int h = 4 * (threadIdx.x + i * T);
+        if (h < H) {
+            store4(out + h, acc[i]);
+            store4(out + H + h, post_acc[i]);
+        }
+    }
+}
+
 // The weights' gradients from the blocks' partials: 32 columns a block; each
 // of its 32 warps adds every 32nd partial, and the warps' sums are joined in order.
 __global__ void __launch_bounds__(1024) block_norm_weights_kernel(const float* partial, int blocks, int H, float* dweight,
@@ -374,7 +639,52 @@ int launch_backward(const moe::BlockNormBackwardArgs& a, bool f32, int gate, dim
                : launch_backward_gate<VPT, WARP, uint16_t>(a, gate, grid, block, smem, stream);
 }
 
-// Blocks of the backward kernel: four an SM, no more than there are rows.
+// Four slots of 8192 columns fit in up to six bytes a column; rings of two are for wider rows.
+constexpr bool may_need_two(int bytes) { return bytes > 6; }
+
+template <int SLOTS, typename R>
+int launch_ring_gate(const Ring& r, const moe::BlockNormArgs& a, int gate, cudaStream_t stream) {
+    switch (gate) {
+        case moe::kNoGate: return launch_ring(moe::block_norm_ring_kernel<SLOTS, R, moe::kNoGate>, r, a, stream);
+        case moe::kTokenGate: return launch_ring(moe::block_norm_ring_kernel<SLOTS, R, moe::kTokenGate>, r, a, stream);
+        default: return launch_ring(moe::block_norm_ring_kernel<SLOTS, R, moe::kFullGate>, r, a, stream);
+    }
+}
+
+template <typename R>
+int launch_forward_ring(const Ring& r, const moe::BlockNormArgs& a, int gate, cudaStream_t stream) {
+    if constexpr (may_need_two(sizeof(R) + 4))  // only with a gate an element
+        if (r.slots == 2) return launch_ring(moe::block_norm_ring_kernel<2, R, moe::kFullGate>, r, a, stream);
+    return r.slots == 8 ? launch_ring_gate<8, R>(r, a, gate, stream) : launch_ring_gate<4, R>(r, a, gate, stream);
+}
+
+template <int SLOTS, typename S, bool DS>
+int launch_backward_ring_gate(const Ring& r, const moe::BlockNormBackwardArgs& a, int gate, cudaStream_t stream) {
+    switch (gate) {
+        case moe::kNoGate:
+            if constexpr (SLOTS > 2 || may_need_two(4 + (DS ? 2 : 1) * sizeof(S)))
+                return launch_ring(moe::block_norm_backward_ring_kernel<SLOTS, S, moe::kNoGate, DS>, r, a, stream);
+            [[fallthrough]];
+        case moe::kTokenGate:
+            if constexpr (SLOTS > 2 || may_need_two(4 + (DS ? 2 : 1) * sizeof(S)))
+                return launch_ring(moe::block_norm_backward_ring_kernel<SLOTS, S, moe::kTokenGate, DS>, r, a, stream);
+            [[fallthrough]];
+        default: return launch_ring(moe::block_norm_backward_ring_kernel<SLOTS, S, moe::kFullGate, DS>, r, a, stream);
+    }
+}
+
+template <typename S>
+int launch_backward_ring(const Ring& r, const moe::BlockNormBackwardArgs& a, int gate, cudaStream_t stream) {
+    if (a.ds != nullptr)
+        return r.slots == 8   ? launch_backward_ring_gate<8, S, true>(r, a, gate, stream)
+               : r.slots == 4 ? launch_backward_ring_gate<4, S, true>(r, a, gate, stream)
+                              : launch_backward_ring_gate<2, S, true>(r, a, gate, stream);
+    return r.slots == 8   ? launch_backward_ring_gate<8, S, false>(r, a, gate, stream)
+           : r.slots == 4 ? launch_backward_ring_gate<4, S, false>(r, a, gate, stream)
+                          : launch_backward_ring_gate<2, S, false>(r, a, gate, stream);
+}
+
+// Blocks of the backward kernel's other forms: four an SM, no more than there are rows.
 int backward_blocks(int N, int H) {
     const int64_t units = H <= 512 ? (static_cast<int64_t>(N) + 3) / 4 : N;
     const int64_t cap = static_cast<int64_t>(num_sms()) * 4;
@@ -419,6 +729,12 @@ extern "C" MOE_API int moe_block_norm(const uint16_t* x, const void* residual, i
     const moe::BlockNormArgs a = {x, residual, gate, post_weight, weight, post_weight_dtype == MOE_DTYPE_F32,
                                   weight_dtype == MOE_DTYPE_F32, N, H, residual_scale, eps, down, mean, y,
                                   residual_out, post_rstd, rstd, q, q_scale};
+    // (the ring has no second sum for squares that vanish: only with an eps that covers them)
+    const Ring ring = eps >= moe::kLeastEps
+                          ? ring_for(N, H, static_cast<size_t>(H) * (2 + (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0)))
+                          : Ring();
+    if (ring.slots > 0)
+        return f32 ? launch_forward_ring<float>(ring, a, kind, stream) : launch_forward_ring<uint16_t>(ring, a, kind, stream);
     if (H <= 512) {
         const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(N) + 3) / 4)), block(128);
         return H <= 256 ? launch_forward<1, true>(a, f32, kind, grid, block, stream)
@@ -434,7 +750,8 @@ extern "C" MOE_API int moe_block_norm(const uint16_t* x, const void* residual, i
 
 extern "C" MOE_API size_t moe_block_norm_backward_workspace_size(int N, int H) {
     if (N < 0 || H < 8 || H % 8 != 0 || H > kMaxH) return 0;
-    const int blocks = backward_blocks(N, H);
+    int blocks = backward_blocks(N, H);  // the ring form may have more, of the narrowest type
+    if (N > blocks) blocks = N < 6 * num_sms() ? N : 6 * num_sms();
     return static_cast<size_t>(blocks > 0 ? blocks : 1) * 2 * H * sizeof(float);
 }
 
@@ -468,14 +785,18 @@ extern "C" MOE_API int moe_block_norm_backward(const uint16_t* dy, const uint16_
     }
     if (workspace_bytes < moe_block_norm_backward_workspace_size(N, H)) return MOE_ERR_CAPACITY;
     const bool f32 = s_dtype == MOE_DTYPE_F32;
-    const int blocks = backward_blocks(N, H);
+    const size_t slot = static_cast<size_t>(H) * (4 + (ds != nullptr ? 2 : 1) * (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0));
+    const Ring ring = ring_for(N, H, slot);
+    const int blocks = ring.slots > 0 ? ring.blocks : backward_blocks(N, H);
     float* partial = static_cast<float*>(workspace);
     const moe::BlockNormBackwardArgs a = {dy, x, s, ds, gate, post_weight, weight, post_weight_dtype == MOE_DTYPE_F32,
                                           weight_dtype == MOE_DTYPE_F32, post_rstd, rstd, N, H, residual_scale, dx, dres,
                                           dgate, partial};
     const dim3 grid(static_cast<unsigned>(blocks));
     int rc;
-    if (H <= 512) {
+    if (ring.slots > 0) {
+        rc = f32 ? launch_backward_ring<float>(ring, a, kind, stream) : launch_backward_ring<uint16_t>(ring, a, kind, stream);
+    } else if (H <= 512) {
         const dim3 block(128);
         const size_t smem = 8 * sizeof(float) * H;
         rc = H <= 256 ? launch_backward<1, true>(a, f32, kind, grid, block, smem, stream)

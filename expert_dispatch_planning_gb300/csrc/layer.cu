@@ -9,9 +9,9 @@
 // weights stream from memory once, straight into the registers that the matrix
 // instruction takes them from, and everything else hides behind them.
 //
-// Up to eight tokens: two launches, gate/up and down, each block of which routes for itself; more: the
-// router's, gate/up, down, and the sum over k.  Each block finds the chosen experts and their
-// tokens by itself (a 64-bit set of tokens for every expert).
+// Launches: the router's, gate/up, down; for more than eight tokens the down product's
+// parts are summed by a fourth.  Each block finds the chosen experts and their tokens by
+// itself from topk_idx (a 64-bit set of tokens for every expert).
 //
 // Products.  mma.m16n8k16 with 16 weight rows as its M side and up to 8 tokens
 // as its N side: an expert has a few tokens, and a tcgen05 tile of 64 or 128
@@ -23,7 +23,6 @@
 // (exact), their products are exact in the fp32 accumulator.
 #include <cmath>
 
-#include "route_core.cuh"
 #include "vec8.cuh"
 
 namespace moe {
@@ -44,7 +43,6 @@ struct LayerArgs {
     float* y;     // [N*K][H], for many tokens
     uint16_t* out;
     int N, K, E, H, I;
-    RouteArgs route;  // of calls that choose for themselves (kRouteExperts)
 };
 
 // Code.  While weights stream through L2 they push the kernels' own instructions out of it,
@@ -85,141 +83,14 @@ struct Chosen {
     __device__ int size(int i) const { return begin[i + 1] - begin[i]; }
 };
 
-// ---- few tokens choose within the blocks that need the choice, each block for itself, a warp a
-// token: the router's rules (route_core.cuh) in a short loop over keys in shared memory.
-constexpr int kRouteExperts = 256, kRouteK = 8;
-constexpr int kRouteTokens = kLayerWarps;
-constexpr int kRouteBytes = kRouteTokens * (kRouteExperts + kRouteK) * 8;  // logits and keys, indices and weights
-
-// A winner's weights are the router's: the same sums of the same terms, 32 lanes wide.
-__device__ __noinline__ float route_weight(const RouteArgs& r, const float* raw, float val, float top) {
-    const int lane = threadIdx.x & 31;
-    const bool sigmoid = r.scoring == MOE_SCORING_SIGMOID, won = lane < r.K;
-    float num = !won ? 0.f : sigmoid ? sigmoid_weight(val) : exp_diff(val, top);
-    float hi = 0.f, lo = 0.f;
-    if (!sigmoid && !r.renormalize) {
-#pragma unroll 1
-        for (int e = lane; e < r.E; e += 32) ff_add(hi, lo, exp_diff(raw[e], top), 0.f);
-    } else if (won && r.renormalize && (!sigmoid || num >= 0x1p-100f)) {
-        ff_add(hi, lo, num, 0.f);
-    }
-    if (__any_sync(FULL_MASK, sigmoid && won && num < 0x1p-100f)) {  // rare: scores that need 64 bits
-        double score = 0.0;
-        if (won) {
-            const double ex = exp(-fabs(static_cast<double>(val)));
-            score = val >= 0.f ? 1.0 / (1.0 + ex) : ex / (1.0 + ex);
-        }
-        double den = score;
-#pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) den += __shfl_xor_sync(FULL_MASK, den, o);
-        return static_cast<float>(score * (r.renormalize ? static_cast<double>(r.scaling) / den : r.scaling));
-    }
-    if (sigmoid && !r.renormalize) return __fmul_rn(num, r.scaling);
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-        const float oh = __shfl_xor_sync(FULL_MASK, hi, o), ol = __shfl_xor_sync(FULL_MASK, lo, o);
-        ff_add(hi, lo, oh, ol);
-    }
-    const float q = __fdiv_rn(r.scaling, hi);
-    return __fmul_rn(num, __fmaf_rn(-q, __fdiv_rn(lo, hi), q));
-}
-
-// Token s's choice by its warp.  raw, keys: [E] of scratch.
-__device__ __forceinline__ void route_warp(const RouteArgs& r, int s, float* raw, uint32_t* keys, int32_t* idx, float* w) {
-    const int lane = threadIdx.x & 31;
-    const bool sigmoid = r.scoring == MOE_SCORING_SIGMOID;
-    // all logits are asked for at once (E is a multiple of four, at most 256)
-    const float* row = r.logits + static_cast<int64_t>(s) * r.E;
-    float4 v[2] = {};
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (4 * (lane + 32 * i) < r.E) v[i] = ld_stream_f4(row + 4 * (lane + 32 * i));
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (4 * (lane + 32 * i) < r.E) *reinterpret_cast<float4*>(raw + 4 * (lane + 32 * i)) = v[i];
-    __syncwarp();
-#pragma unroll 1
-    for (int e = lane; e < r.E; e += 32) {
-        float key = raw[e];
-        if (sigmoid) {
-            key = sigmoid_f32(key);
-            if (r.bias != nullptr) key = __fadd_rn(key, __ldg(r.bias + e));
-        }
-        keys[e] = order_key(key);
-    }
-    __syncwarp();
-    if (r.n_group > 1) {  // a lane a group: its two largest keys' sum; then the best groups, ties to the lower
-        const int gs = r.E / r.n_group;
-        uint32_t mine = 0u, kept = 0u;
-        if (lane < r.n_group) {
-            uint32_t k1 = 0u, k2 = 0u;  // 0 is below every key
-#pragma unroll 1
-            for (int j = 0; j < gs; ++j) {
-                const uint32_t k = keys[lane * gs + j];
-                if (k > k1) k2 = k1, k1 = k;
-                else if (k > k2) k2 = k;
-            }
-            auto value = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) != 0 ? k ^ 0x80000000u : ~k); };
-            mine = order_key(gs == 1 ? value(k1) : __fadd_rn(value(k1), value(k2)));
-        }
-#pragma unroll 1
-        for (int i = 0; i < r.topk_group; ++i) {
-            const uint32_t m = __reduce_max_sync(FULL_MASK, mine);
-            const uint32_t win = __reduce_min_sync(FULL_MASK, mine == m ? static_cast<uint32_t>(lane) : 32u);
-            kept |= 1u << win;
-            if (static_cast<uint32_t>(lane) == win) mine = 0u;
-        }
-#pragma unroll 1
-        for (int e = lane; e < r.E; e += 32)
-            if (((kept >> (e / gs)) & 1u) == 0) keys[e] = 0u;
-        __syncwarp();
-    }
-    float val = 0.f, top = 0.f;
-    int mine = 0;
-#pragma unroll 1
-    for (int k = 0; k < r.K; ++k) {
-        uint32_t best = 0u, at = 0xffffffffu;
-#pragma unroll 1
-        for (int e = lane; e < r.E; e += 32) {
-            const uint32_t key = keys[e];
-            if (key > best) best = key, at = e;  // ascending: equal keys keep the lower expert
-        }
-        const uint32_t m = __reduce_max_sync(FULL_MASK, best);
-        const uint32_t win = __reduce_min_sync(FULL_MASK, best == m ? at : 0xffffffffu);
-        const float x = raw[win < static_cast<uint32_t>(r.E) ? win : 0];
-        if (at == win) keys[win] = 0u;
-        if (k == 0) top = x;
-        if (lane == k) val = x, mine = static_cast<int>(win);
-        __syncwarp();
-    }
-    const float weight = route_weight(r, raw, val, top);
-    if (lane < r.K) {
-        idx[s * r.K + lane] = mine;
-        w[s * r.K + lane] = weight;
-    }
-}
-
-// Fills `smem` as Chosen's arrays; returns the number of chosen experts.  From the logits with
-// `scratch` (kRouteBytes), else from topk_idx and topk_w.  All threads call.
-__device__ __noinline__ int choose(uint8_t* smem, int N, int K, int E, const int32_t* topk_idx, const float* topk_w,
-                                   const RouteArgs& r, uint8_t* scratch, bool report) {
+// Fills `smem` as Chosen's arrays from the router's outputs; returns the number of chosen experts.
+// All threads call.
+__device__ __noinline__ int choose(uint8_t* smem, int N, int K, int E, const int32_t* topk_idx, const float* topk_w) {
     const Chosen c(smem, N, K, E);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pairs = N * K;
 #pragma unroll 1
     for (int e = tid; e < E; e += kLayerThreads) c.tokens[e] = 0;
-    if (scratch != nullptr) {
-        int32_t* idx = reinterpret_cast<int32_t*>(scratch);
-        float* w = reinterpret_cast<float*>(idx + kRouteTokens * kRouteK);
-        float* raw = w + kRouteTokens * kRouteK + warp * 2 * kRouteExperts;
-        if (warp < N) route_warp(r, warp, raw, reinterpret_cast<uint32_t*>(raw + kRouteExperts), idx, w);
-        topk_idx = idx;
-        topk_w = w;
-    }
     __syncthreads();
-    if (report && tid < pairs) {
-        if (r.topk_idx != nullptr) r.topk_idx[tid] = topk_idx[tid];
-        if (r.topk_w != nullptr) r.topk_w[tid] = topk_w[tid];
-    }
     auto chosen = [&](int f) {  // the pair's expert; -1 for an index that the router does not give
         const int e = topk_idx[f];
         return static_cast<unsigned>(e) < static_cast<unsigned>(E) ? e : -1;
@@ -576,7 +447,6 @@ template <bool Q, bool DOWN, int EIGHTS>
 __global__ void __launch_bounds__(kLayerThreads, 2) layer_rows_kernel(const LayerArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     using Ring = TileRing<DOWN>;
-    static_assert(kRouteBytes <= kLayerWarps * Ring::kWarpBytes, "the ring's place is the router's scratch");
     Ring ring(smem);
     float4* sum = reinterpret_cast<float4*>(smem + kLayerWarps * Ring::kWarpBytes);
     uint8_t* lists = reinterpret_cast<uint8_t*>(sum + kLayerWarps * kTiles * 32);
@@ -586,8 +456,7 @@ __global__ void __launch_bounds__(kLayerThreads, 2) layer_rows_kernel(const Laye
         pdl_trigger();
     }
     // (of the down product topk_idx and the weights come from before the launch that this one may overlap)
-    const int count = choose(lists, a.N, a.K, a.E, a.topk_idx, a.topk_w, a.route, a.topk_idx == nullptr ? smem : nullptr,
-                             !DOWN && a.topk_idx == nullptr && blockIdx.x == 0);
+    const int count = choose(lists, a.N, a.K, a.E, a.topk_idx, a.topk_w);
     const int warp = threadIdx.x >> 5, units = DOWN ? a.H : a.I;
     const int bytes = DOWN ? 2 * a.I : a.H * (Q ? 1 : 2), steps = (bytes + kStepBytes - 1) / kStepBytes;
     const uint8_t* x = static_cast<const uint8_t*>(DOWN ? a.h : a.x);
@@ -749,9 +618,8 @@ __global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const Laye
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(blocks));
 #pragma unroll 1
     for (int v = tid; v < kLayerWarps * kDownRows * a.N; v += kLayerThreads) sums[v] = 0.f;
-    // topk_idx or the logits, and the weights, come from before the launch that this one may overlap
-    const int count =
-        choose(lists, a.N, a.K, a.E, a.topk_idx, a.topk_w, a.route, a.topk_idx == nullptr ? smem : nullptr, false);
+    // topk_idx and the weights come from before the launch that this one may overlap
+    const int count = choose(lists, a.N, a.K, a.E, a.topk_idx, a.topk_w);
     const uint8_t* h = reinterpret_cast<const uint8_t*>(a.h);
     const int bytes = 2 * a.I, first_row = static_cast<int>(blockIdx.x / blocks) * rows;
     const int there = a.H - first_row < rows ? a.H - first_row : rows;
@@ -917,8 +785,6 @@ extern "C" MOE_API int moe_layer(const void* x, const float* x_scale, const floa
         !aligned(x_scale, 4) || !aligned(w_scale, 4))
         return MOE_ERR_INVALID_ARG;
     float* y = nullptr;
-    int32_t* const wanted_idx = topk_idx;
-    float* const wanted_w = topk_w;
     if (N > 0 && K >= 1 && K <= 32) {
         if (workspace_bytes < moe_layer_workspace_size(N, K, H, I)) return MOE_ERR_CAPACITY;
         uint8_t* rest = static_cast<uint8_t*>(workspace) + static_cast<size_t>(N) * K * I * 2;
@@ -927,23 +793,13 @@ extern "C" MOE_API int moe_layer(const void* x, const float* x_scale, const floa
         if (topk_idx == nullptr) topk_idx = reinterpret_cast<int32_t*>(rest);
         if (topk_w == nullptr) topk_w = reinterpret_cast<float*>(rest + round16(static_cast<size_t>(N) * K * 4));
     }
-    LayerArgs a = {x, x_scale, w_gate_up, w_scale, w_down, topk_idx, topk_w, static_cast<uint16_t*>(workspace), y,
-                   out, N, K, E, H, I, {}};
-    const bool few = N <= moe::kDownTokens;
-    if (few && E <= moe::kRouteExperts && E % 4 == 0 && K <= moe::kRouteK) {
-        const int rc = route_args(logits, bias, N, E, K, scoring, renormalize, n_group, topk_group, routed_scaling, topk_idx,
-                                  topk_w, &a.route);
-        if (rc != MOE_OK || N == 0) return rc;
-        a.route.topk_idx = wanted_idx;
-        a.route.topk_w = wanted_w;
-        a.topk_idx = nullptr;  // the blocks route
-    } else {
-        // the router's own checks of logits, bias, E, K and its options come with its call
-        const int rc = moe_route_topk(logits, bias, N, E, K, scoring, renormalize, n_group, topk_group, routed_scaling,
-                                      topk_idx, topk_w, stream);
-        if (rc != MOE_OK || N == 0) return rc;
-    }
-    if (few) {
+    // the router's own checks of logits, bias, E, K and its options come with its call
+    const int rc = moe_route_topk(logits, bias, N, E, K, scoring, renormalize, n_group, topk_group, routed_scaling, topk_idx,
+                                  topk_w, stream);
+    if (rc != MOE_OK || N == 0) return rc;
+    const LayerArgs a = {x, x_scale, w_gate_up, w_scale, w_down, topk_idx, topk_w, static_cast<uint16_t*>(workspace), y,
+                         out, N, K, E, H, I};
+    if (N <= moe::kDownTokens) {
         const int up = q ? launch_rows<true, false, 1>(a, stream) : launch_rows<false, false, 1>(a, stream);
         return up != MOE_OK ? up : launch_down(a, stream);
     }

@@ -607,15 +607,14 @@ MOE_API int moe_combine_backward(const uint16_t* dout, const uint16_t* y, const 
  *              as in moe_route_topk.
  *   w_gate_up, w_scale, w_down: as in moe_expert_ffn.
  *   topk_idx   (device) int32[N][K] and
- *   topk_w     float32[N][K]: the router's outputs, or NULL if not wanted (topk_w within
- *              moe_route_topk's bound of the exact value).
+ *   topk_w     float32[N][K]: the router's outputs, or NULL if not wanted.
  *   out        (device) bf16[N][H] out; must not alias x.
  *   workspace  (device) moe_layer_workspace_size(N, K, H, I) bytes, 16-byte aligned, no
  *              initialisation; one call at a time.
  * N <= MOE_LAYER_MAX_TOKENS (more: MOE_ERR_UNSUPPORTED; plan, permute, expert_ffn and
  * combine serve those).  H % 8 == 0 (H % 16 == 0 with e4m3), I % 8 == 0, H and I < 2^20;
- * 16-byte aligned arrays.  Up to eight tokens: two launches, with K <= 8 and E <= 256 a
- * multiple of 4, else three (the router's); more: four.  N = 0 launches nothing.
+ * 16-byte aligned arrays.  Three launches, four for more than eight tokens; N = 0
+ * launches nothing.
  */
 #define MOE_LAYER_MAX_TOKENS 64
 MOE_API size_t moe_layer_workspace_size(int N, int K, int H, int I);

@@ -36,7 +36,7 @@ def rand(*shape, seed=0):
 
 # a row in one warp (up to 512), in a block with 1, 2 or 4 chunks a thread, the bounds between them, and many rows
 SIZES = [(1, 8), (3, 128), (7, 256), (5, 264), (129, 512), (2, 520), (1, 2048), (33, 2056), (4, 4096), (9, 7168),
-         (3, 8200), (2, 16384), (1, 32768), (1000, 136), (4001, 520), (1300, 1000), (2500, 4104), (1111, 7168), (700, 8192)]
+         (3, 8200), (2, 16384), (1, 32768), (1000, 136), (4001, 520), (1300, 1000), (3700, 1000), (2500, 4104), (1111, 7168), (700, 8192)]
 KINDS = [(BF16, None, BF16, BF16), (F32, "token", F32, BF16), (BF16, "full", BF16, F32), (F32, "full", F32, F32),
          (F32, None, BF16, BF16), (BF16, "token", BF16, BF16)]
 
