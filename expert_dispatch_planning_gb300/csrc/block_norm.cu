@@ -160,119 +160,135 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) block_norm_kernel(cons
 }
 
 // ---------------------------------------------------------------- ring
-// R: the residual's element type.
-template <int SLOTS, typename R, int GATE>
-__global__ void __launch_bounds__(kRingThreads) block_norm_ring_kernel(const BlockNormArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];  // [SLOTS][x row, gate row, residual row]
+// A warp has 256 columns of the block's rows, a lane eight of them.  The warp's lanes copy its columns of
+// the next rows into shared memory (cp.async, 16 bytes a lane, side by side) while the block works on a
+// row; only the warp reads them, so that a slot needs no barrier of the block.  (Eight bytes a thread, the
+// columns it needs itself, go through L1, which the ring leaves little of: figures.)
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+// The warp's columns first .. of one row, to its place in shared memory: of 256 elements, or up to H.  Of fp32
+// rows the 16-byte chunks of every second eight are swapped in pairs, so that a read of eight lanes,
+// each 32 bytes from the next, is in different banks.
+__device__ __forceinline__ void copy_columns(uint16_t* to, const uint16_t* row, int first, int H) {
+    const int h = first + 8 * (threadIdx.x & 31);
+    if (h < H) copy16(to + h, row + h);
+}
+__device__ __forceinline__ void copy_columns(float* to, const float* row, int first, int H) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int chunk = (threadIdx.x & 31) + 32 * i, h = first + 4 * chunk;
+        if (h < H) copy16(to + first + 4 * (chunk ^ (chunk >> 3 & 1)), row + h);
+    }
+}
+// The lane's eight columns from there.
+__device__ __forceinline__ void read8(const uint16_t* from, int first, float (&f)[8]) {
+    unpack8(*reinterpret_cast<const uint4*>(from + first + 8 * (threadIdx.x & 31)), f);
+}
+__device__ __forceinline__ void read8(const float* from, int first, float (&f)[8]) {
+    const int chunk = 2 * (threadIdx.x & 31), swap = chunk >> 3 & 1;
+    const float4 a = *reinterpret_cast<const float4*>(from + first + 4 * (chunk ^ swap));
+    const float4 b = *reinterpret_cast<const float4*>(from + first + 4 * ((chunk + 1) ^ swap));
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+// Until at most slots - 1 of the thread's groups of copies are under way, and the warp's have landed.
+__device__ __forceinline__ void ring_wait(int slots) {
+    if (slots == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (slots == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (slots == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else asm volatile("cp.async.wait_group 7;" ::: "memory");
+    __syncwarp();
+}
+// A row's place holds its columns rounded up to whole warps'.
+__host__ __device__ __forceinline__ int ring_columns(int H) { return (H + 255) / 256 * 256; }
+
+// R: the residual's element type.  slots: 2, 3, 4 or 8.
+template <typename R, int GATE>
+__global__ void __launch_bounds__(kRingThreads) block_norm_ring_kernel(const BlockNormArgs a, const int slots) {
+    extern __shared__ __align__(16) uint8_t smem[];  // [slots][x row, gate row, residual row]
     __shared__ float buf[2][3][32];
     pdl_wait();
     pdl_trigger();
-    const int T = blockDim.x, H = a.H;
-    constexpr int kGateBytes = GATE == kFullGate ? 2 : 0;
-    const uint32_t slot_bytes = static_cast<uint32_t>(H) * (2 + kGateBytes + sizeof(R));
+    const int H = a.H, W = ring_columns(H), first = threadIdx.x / 32 * 256, h = 8 * threadIdx.x;
+    const bool mine = h < H;
+    constexpr int kNarrow = GATE == kFullGate ? 2 : 1;  // rows of two bytes an element
+    const uint32_t slot_bytes = static_cast<uint32_t>(W) * (2 * kNarrow + sizeof(R));
     const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.N / gridDim.x;
     const int64_t end = (static_cast<int64_t>(blockIdx.x) + 1) * a.N / gridDim.x;
-    auto fetch = [&](int64_t row, uint32_t slot) {
+    auto fetch = [&](int64_t row, int slot) {
+        __syncwarp();  // all lanes have read what was there
         if (row < end) {
             uint16_t* x = reinterpret_cast<uint16_t*>(smem + slot * slot_bytes);
-            R* r = reinterpret_cast<R*>(x + H + H * kGateBytes / 2);
-#pragma unroll
-            for (int i = 0; i < kRingGroups; ++i) {
-                const int h = 4 * (threadIdx.x + i * T);
-                if (h < H) {
-                    cp_async_group(x + h, a.x + row * H + h);
-                    cp_async_group(r + h, static_cast<const R*>(a.residual) + row * H + h);
-                    if constexpr (GATE == kFullGate)
-                        cp_async_group(x + H + h, static_cast<const uint16_t*>(a.gate) + row * H + h);
-                }
-            }
+            copy_columns(x, a.x + row * H, first, H);
+            if constexpr (GATE == kFullGate) copy_columns(x + W, static_cast<const uint16_t*>(a.gate) + row * H, first, H);
+            copy_columns(reinterpret_cast<R*>(x + kNarrow * W), static_cast<const R*>(a.residual) + row * H, first, H);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float wp[kRingGroups][4], w[kRingGroups][4];
-#pragma unroll
-    for (int i = 0; i < kRingGroups; ++i) {
-        const int h = 4 * (threadIdx.x + i * T);
-        if (h < H) {
-            load_weight4(a.post_weight, a.post_f32, h, wp[i]);
-            load_weight4(a.weight, a.weight_f32, h, w[i]);
-        }
+    float wp[8], w[8];
+    if (mine) {
+        load_weight8(a.post_weight, a.post_f32, threadIdx.x, wp);
+        load_weight8(a.weight, a.weight_f32, threadIdx.x, w);
     }
-#pragma unroll
-    for (int j = 0; j < SLOTS - 1; ++j) fetch(begin + j, j);
+    for (int j = 0; j < slots - 1; ++j) fetch(begin + j, j);
     float next_gate = GATE == kTokenGate && begin < end ? __ldg(static_cast<const float*>(a.gate) + begin) : 1.f;
-    uint32_t slot = 0;  // the row's
-    for (int64_t row = begin; row < end; ++row, slot = (slot + 1) % SLOTS) {
-        fetch(row + SLOTS - 1, (slot + SLOTS - 1) % SLOTS);
+    int slot = 0;  // the row's
+    for (int64_t row = begin; row < end; ++row) {
+        fetch(row + slots - 1, slot == 0 ? slots - 1 : slot - 1);
         const float token_gate = next_gate;
         if (GATE == kTokenGate && row + 1 < end) next_gate = __ldg(static_cast<const float*>(a.gate) + row + 1);
-        asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+        ring_wait(slots);
         const uint16_t* x = reinterpret_cast<const uint16_t*>(smem + slot * slot_bytes);
-        const R* r = reinterpret_cast<const R*>(x + H + H * kGateBytes / 2);
+        slot = slot + 1 == slots ? 0 : slot + 1;
         const int64_t at = row * H;
         float(*sums)[32] = buf[row & 1];
-        float s[kRingGroups][4];
+        float s[8];
         float ss = 0.f;
+        if (mine) {
+            read8(x, first, s);
 #pragma unroll
-        for (int i = 0; i < kRingGroups; ++i) {
-            const int h = 4 * (threadIdx.x + i * T);
-            if (h < H) {
-                load4(x + h, s[i]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float t = s[i][j] * a.down;
-                    ss = fmaf(t, t, ss);
-                }
+            for (int j = 0; j < 8; ++j) {
+                const float t = s[j] * a.down;
+                ss = fmaf(t, t, ss);
             }
         }
         ss = block_reduce<false>(ss, sums[0]);
         const float post = rsqrtf(fmaf(ss, a.mean, a.eps));  // within 2^-22
         if (threadIdx.x == 0) a.post_rstd[row] = post;
         ss = 0.f;
+        if (mine) {
+            float q[8], g[8];
+            read8(reinterpret_cast<const R*>(x + kNarrow * W), first, q);
+            if constexpr (GATE == kFullGate) read8(x + W, first, g);
 #pragma unroll
-        for (int i = 0; i < kRingGroups; ++i) {
-            const int h = 4 * (threadIdx.x + i * T);
-            if (h < H) {
-                float q[4], g[4];
-                load4(r + h, q);
-                if constexpr (GATE == kFullGate) load4(x + H + h, g);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float n = s[i][j] * post * wp[i][j];
-                    if constexpr (GATE == kTokenGate) n *= token_gate;
-                    if constexpr (GATE == kFullGate) n *= g[j];
-                    s[i][j] = fmaf(a.alpha, q[j], n);
-                    const float t = s[i][j] * a.down;
-                    ss = fmaf(t, t, ss);
-                }
-                store4(static_cast<R*>(a.residual_out) + at + h, s[i]);
+            for (int j = 0; j < 8; ++j) {
+                float n = s[j] * post * wp[j];
+                if constexpr (GATE == kTokenGate) n *= token_gate;
+                if constexpr (GATE == kFullGate) n *= g[j];
+                s[j] = fmaf(a.alpha, q[j], n);
+                const float t = s[j] * a.down;
+                ss = fmaf(t, t, ss);
             }
+            store8(static_cast<R*>(a.residual_out) + at, threadIdx.x, s);
         }
         ss = block_reduce<false>(ss, sums[1]);
         const float rstd = rsqrtf(fmaf(ss, a.mean, a.eps));
         if (threadIdx.x == 0) a.rstd[row] = rstd;
         float amax = 0.f;
+        if (mine) {
 #pragma unroll
-        for (int i = 0; i < kRingGroups; ++i) {
-            const int h = 4 * (threadIdx.x + i * T);
-            if (h < H) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[i][j] = s[i][j] * rstd * w[i][j];
-                    amax = fmaxf(amax, fabsf(s[i][j]));
-                }
-                store4(a.y + at + h, s[i]);
+            for (int j = 0; j < 8; ++j) {
+                s[j] = s[j] * rstd * w[j];
+                amax = fmaxf(amax, fabsf(s[j]));
             }
+            store8(a.y + at, threadIdx.x, s);
         }
         if (a.q == nullptr) continue;
         amax = block_reduce<true>(amax, sums[2]);
         const Quantum q = quantum_of(amax);
         if (threadIdx.x == 0) a.q_scale[row] = q.scale;
-#pragma unroll
-        for (int i = 0; i < kRingGroups; ++i) {
-            const int h = 4 * (threadIdx.x + i * T);
-            if (h < H) *reinterpret_cast<uint32_t*>(a.q + at + h) = q.round4(s[i]);
-        }
+        if (mine) *reinterpret_cast<uint2*>(a.q + at + h) = make_uint2(q.round4(s), q.round4(s + 4));
     }
 }
 
@@ -432,51 +448,43 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) block_norm_backward_ke
 
 // A thread reads its columns' values from the ring anew in each of the row's three parts: in
 // registers there is only room for what has no other place (the weights' sums and d).
-template <int SLOTS, typename S, int GATE, bool DS>
-__global__ void __launch_bounds__(kRingThreads) block_norm_backward_ring_kernel(const BlockNormBackwardArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];  // [SLOTS][dy row, x row, gate row, s row, ds row]
+template <typename S, int GATE, bool DS>
+__global__ void __launch_bounds__(kRingThreads) block_norm_backward_ring_kernel(const BlockNormBackwardArgs a,
+                                                                               const int slots) {
+    extern __shared__ __align__(16) uint8_t smem[];  // [slots][dy row, x row, gate row, s row, ds row]
     __shared__ float buf[2][2][32];
     pdl_wait();
     pdl_trigger();
-    const int T = blockDim.x, H = a.H;
+    const int H = a.H, W = ring_columns(H), first = threadIdx.x / 32 * 256, h = 8 * threadIdx.x;
+    const bool mine = h < H;
     constexpr int kNarrow = GATE == kFullGate ? 3 : 2;  // rows of two bytes an element
-    const uint32_t slot_bytes = static_cast<uint32_t>(H) * (2 * kNarrow + (DS ? 2 : 1) * sizeof(S));
+    const uint32_t slot_bytes = static_cast<uint32_t>(W) * (2 * kNarrow + (DS ? 2 : 1) * sizeof(S));
     const float over_h = 1.f / static_cast<float>(H);
     const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.N / gridDim.x;
     const int64_t end = (static_cast<int64_t>(blockIdx.x) + 1) * a.N / gridDim.x;
-    auto fetch = [&](int64_t row, uint32_t slot) {
+    auto fetch = [&](int64_t row, int slot) {
+        __syncwarp();  // all lanes have read what was there
         if (row < end) {
             uint16_t* dy = reinterpret_cast<uint16_t*>(smem + slot * slot_bytes);
-            S* s = reinterpret_cast<S*>(dy + kNarrow * H);
-#pragma unroll
-            for (int i = 0; i < kRingGroups; ++i) {
-                const int h = 4 * (threadIdx.x + i * T);
-                if (h < H) {
-                    cp_async_group(dy + h, a.dy + row * H + h);
-                    cp_async_group(s + h, static_cast<const S*>(a.s) + row * H + h);
-                    cp_async_group(dy + H + h, a.x + row * H + h);
-                    if constexpr (DS) cp_async_group(s + H + h, static_cast<const S*>(a.ds) + row * H + h);
-                    if constexpr (GATE == kFullGate)
-                        cp_async_group(dy + 2 * H + h, static_cast<const uint16_t*>(a.gate) + row * H + h);
-                }
-            }
+            S* s = reinterpret_cast<S*>(dy + kNarrow * W);
+            copy_columns(dy, a.dy + row * H, first, H);
+            copy_columns(s, static_cast<const S*>(a.s) + row * H, first, H);
+            copy_columns(dy + W, a.x + row * H, first, H);
+            if constexpr (DS) copy_columns(s + W, static_cast<const S*>(a.ds) + row * H, first, H);
+            if constexpr (GATE == kFullGate)
+                copy_columns(dy + 2 * W, static_cast<const uint16_t*>(a.gate) + row * H, first, H);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float w[kRingGroups][4], wp[kRingGroups][4], acc[kRingGroups][4], post_acc[kRingGroups][4];
-#pragma unroll
-    for (int i = 0; i < kRingGroups; ++i) {
-        const int h = 4 * (threadIdx.x + i * T);
-        if (h < H) {
-            load_weight4(a.weight, a.weight_f32, h, w[i]);
-            load_weight4(a.post_weight, a.post_f32, h, wp[i]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = post_acc[i][j] = 0.f;
+    float w[8], wp[8], acc[8], post_acc[8];
+    if (mine) {
+        load_weight8(a.weight, a.weight_f32, threadIdx.x, w);
+        load_weight8(a.post_weight, a.post_f32, threadIdx.x, wp);
     }
 #pragma unroll
-    for (int j = 0; j < SLOTS - 1; ++j) fetch(begin + j, j);
-    uint32_t slot = 0;  // the row's
+    for (int j = 0; j < 8; ++j) acc[j] = post_acc[j] = 0.f;
+    for (int j = 0; j < slots - 1; ++j) fetch(begin + j, j);
+    int slot = 0;  // the row's
     float next_rstd = 0.f, next_post = 0.f, next_gate = 1.f;
     auto scalars = [&](int64_t row) {
         if (row >= end) return;
@@ -485,69 +493,62 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_backward_ring_kernel(
         if constexpr (GATE == kTokenGate) next_gate = __ldg(static_cast<const float*>(a.gate) + row);
     };
     scalars(begin);
-    for (int64_t row = begin; row < end; ++row, slot = (slot + 1) % SLOTS) {
-        fetch(row + SLOTS - 1, (slot + SLOTS - 1) % SLOTS);
+    for (int64_t row = begin; row < end; ++row) {
+        fetch(row + slots - 1, slot == 0 ? slots - 1 : slot - 1);
         const float rstd = next_rstd, post = next_post, token_gate = next_gate;
         scalars(row + 1);
-        asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+        ring_wait(slots);
         const uint16_t* dy = reinterpret_cast<const uint16_t*>(smem + slot * slot_bytes);
-        const S* s = reinterpret_cast<const S*>(dy + kNarrow * H);
+        slot = slot + 1 == slots ? 0 : slot + 1;
+        const S* s = reinterpret_cast<const S*>(dy + kNarrow * W);
         const int64_t at = row * H;
         float(*sums)[32] = buf[row & 1];
         float dot = 0.f;
+        if (mine) {
+            float t[8], hat[8];
+            read8(dy, first, t);
+            read8(s, first, hat);
 #pragma unroll
-        for (int i = 0; i < kRingGroups; ++i) {
-            const int h = 4 * (threadIdx.x + i * T);
-            if (h < H) {
-                float t[4], hat[4];
-                load4(dy + h, t);
-                load4(s + h, hat);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    hat[j] *= rstd;
-                    acc[i][j] = fmaf(t[j], hat[j], acc[i][j]);
-                    dot = fmaf(t[j] * w[i][j], hat[j], dot);
-                }
+            for (int j = 0; j < 8; ++j) {
+                hat[j] *= rstd;
+                acc[j] = fmaf(t[j], hat[j], acc[j]);
+                dot = fmaf(t[j] * w[j], hat[j], dot);
             }
         }
         const float mean = block_reduce<false>(dot, sums[0]) * over_h;
-        float d[kRingGroups][4];
+        float d[8];
         dot = 0.f;
+        if (mine) {
+            float t[8], v[8], o[8];
+            read8(dy, first, t);
+            read8(s, first, v);
 #pragma unroll
-        for (int i = 0; i < kRingGroups; ++i) {
-            const int h = 4 * (threadIdx.x + i * T);
-            if (h < H) {
-                float t[4], v[4], o[4];
-                load4(dy + h, t);
-                load4(s + h, v);
+            for (int j = 0; j < 8; ++j) d[j] = 0.f;
+            if constexpr (DS) read8(s + W, first, d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
-                if constexpr (DS) load4(s + H + h, d[i]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    d[i][j] += rstd * (t[j] * w[i][j] - v[j] * rstd * mean);
-                    o[j] = a.alpha * d[i][j];
-                }
-                store4(static_cast<S*>(a.dres) + at + h, o);
-                load4(dy + H + h, v);
-                if constexpr (GATE == kFullGate) load4(dy + 2 * H + h, t);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[j] *= post;
-                    const float n = v[j] * wp[i][j];
-                    if constexpr (GATE == kFullGate) {
-                        o[j] = d[i][j] * n;
-                        d[i][j] *= t[j];
-                        dot = fmaf(d[i][j], n, dot);
-                    } else {
-                        dot = fmaf(d[i][j], n, dot);
-                        d[i][j] *= token_gate;
-                    }
-                    post_acc[i][j] = fmaf(d[i][j], v[j], post_acc[i][j]);
-                    d[i][j] *= wp[i][j];
-                }
-                if constexpr (GATE == kFullGate) store4(static_cast<uint16_t*>(a.dgate) + at + h, o);
+            for (int j = 0; j < 8; ++j) {
+                d[j] += rstd * (t[j] * w[j] - v[j] * rstd * mean);
+                o[j] = a.alpha * d[j];
             }
+            store8(static_cast<S*>(a.dres) + at, threadIdx.x, o);
+            read8(dy + W, first, v);
+            if constexpr (GATE == kFullGate) read8(dy + 2 * W, first, t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] *= post;
+                const float n = v[j] * wp[j];
+                if constexpr (GATE == kFullGate) {
+                    o[j] = d[j] * n;
+                    d[j] *= t[j];
+                    dot = fmaf(d[j], n, dot);
+                } else {
+                    dot = fmaf(d[j], n, dot);
+                    d[j] *= token_gate;
+                }
+                post_acc[j] = fmaf(d[j], v[j], post_acc[j]);
+                d[j] *= wp[j];
+            }
+            if constexpr (GATE == kFullGate) store8(static_cast<uint16_t*>(a.dgate) + at, threadIdx.x, o);
         }
         dot = block_reduce<false>(dot, sums[1]);
         if constexpr (GATE == kTokenGate) {
@@ -555,26 +556,18 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_backward_ring_kernel(
             dot *= token_gate;
         }
         const float post_mean = dot * over_h;
+        if (mine) {
+            float v[8];
+            read8(dy + W, first, v);
 #pragma unroll
-        for (int i = 0; i < kRingGroups; ++i) {
-            const int h = 4 * (threadIdx.x + i * T);
-            if (h < H) {
-                float v[4];
-                load4(dy + H + h, v);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d[i][j] = post * (d[i][j] - v[j] * post * post_mean);
-                store4(a.dx + at + h, d[i]);
-            }
+            for (int j = 0; j < 8; ++j) d[j] = post * (d[j] - v[j] * post * post_mean);
+            store8(a.dx + at, threadIdx.x, d);
         }
     }
     float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * H;
-#pragma unroll
-    for (int i = 0; i < kRingGroups; ++i) {
-        const int h = 4 * (threadIdx.x + i * T);
-        if (h < H) {
-            store4(out + h, acc[i]);
-            store4(out + H + h, post_acc[i]);
-        }
+    if (mine) {
+        store8(out, threadIdx.x, acc);
+        store8(out + H, threadIdx.x, post_acc);
     }
 }
 
@@ -639,49 +632,56 @@ int launch_backward(const moe::BlockNormBackwardArgs& a, bool f32, int gate, dim
                : launch_backward_gate<VPT, WARP, uint16_t>(a, gate, grid, block, smem, stream);
 }
 
-// Four slots of 8192 columns fit in up to six bytes a column; rings of two are for wider rows.
-constexpr bool may_need_two(int bytes) { return bytes > 6; }
+// The ring form of these kernels, with `bytes` a column of a row in a slot.  A row has two or three sums one
+// after the other, in which a block only waits: so an SM has as many blocks as its threads (64 registers
+// each) and two slots each allow, and slots as many as then fit.
+struct BlockRing {
+    int slots = 0, threads = 0, blocks = 0;  // slots = 0: not taken
+    size_t smem = 0;
+};
+BlockRing block_ring_for(int N, int H, int bytes) {
+    constexpr size_t kSmem = 220 * 1024;
+    const size_t slot = static_cast<size_t>(moe::ring_columns(H)) * bytes;
+    BlockRing r;
+    if (H <= 512 || H > 8 * moe::kRingThreads || 2 * slot > kSmem) return r;
+    const int threads = moe::ring_columns(H) / 8;
+    int per_sm = moe::kRingThreads / threads;
+    const int by_smem = static_cast<int>(kSmem / (2 * slot));
+    if (by_smem < per_sm) per_sm = by_smem;
+    if (per_sm > 6) per_sm = 6;
+    const int fit = static_cast<int>(kSmem / (per_sm * slot)), blocks = num_sms() * per_sm;
+    if (N < 4 * blocks) return r;
+    r.slots = fit >= 8 ? 8 : fit >= 4 ? 4 : fit;
+    r.threads = threads;
+    r.blocks = blocks;
+    r.smem = r.slots * slot;
+    return r;
+}
 
-template <int SLOTS, typename R>
-int launch_ring_gate(const Ring& r, const moe::BlockNormArgs& a, int gate, cudaStream_t stream) {
-    switch (gate) {
-        case moe::kNoGate: return launch_ring(moe::block_norm_ring_kernel<SLOTS, R, moe::kNoGate>, r, a, stream);
-        case moe::kTokenGate: return launch_ring(moe::block_norm_ring_kernel<SLOTS, R, moe::kTokenGate>, r, a, stream);
-        default: return launch_ring(moe::block_norm_ring_kernel<SLOTS, R, moe::kFullGate>, r, a, stream);
-    }
+template <typename Kernel, typename Args>
+int launch_block_ring(Kernel kernel, const BlockRing& r, const Args& a, cudaStream_t stream) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return launch(kernel, dim3(static_cast<unsigned>(r.blocks)), dim3(static_cast<unsigned>(r.threads)), r.smem, stream, a,
+                  r.slots);
 }
 
 template <typename R>
-int launch_forward_ring(const Ring& r, const moe::BlockNormArgs& a, int gate, cudaStream_t stream) {
-    if constexpr (may_need_two(sizeof(R) + 4))  // only with a gate an element
-        if (r.slots == 2) return launch_ring(moe::block_norm_ring_kernel<2, R, moe::kFullGate>, r, a, stream);
-    return r.slots == 8 ? launch_ring_gate<8, R>(r, a, gate, stream) : launch_ring_gate<4, R>(r, a, gate, stream);
-}
-
-template <int SLOTS, typename S, bool DS>
-int launch_backward_ring_gate(const Ring& r, const moe::BlockNormBackwardArgs& a, int gate, cudaStream_t stream) {
+int launch_forward_ring(const BlockRing& r, const moe::BlockNormArgs& a, int gate, cudaStream_t stream) {
     switch (gate) {
-        case moe::kNoGate:
-            if constexpr (SLOTS > 2 || may_need_two(4 + (DS ? 2 : 1) * sizeof(S)))
-                return launch_ring(moe::block_norm_backward_ring_kernel<SLOTS, S, moe::kNoGate, DS>, r, a, stream);
-            [[fallthrough]];
-        case moe::kTokenGate:
-            if constexpr (SLOTS > 2 || may_need_two(4 + (DS ? 2 : 1) * sizeof(S)))
-                return launch_ring(moe::block_norm_backward_ring_kernel<SLOTS, S, moe::kTokenGate, DS>, r, a, stream);
-            [[fallthrough]];
-        default: return launch_ring(moe::block_norm_backward_ring_kernel<SLOTS, S, moe::kFullGate, DS>, r, a, stream);
+        case moe::kNoGate: return launch_block_ring(moe::block_norm_ring_kernel<R, moe::kNoGate>, r, a, stream);
+        case moe::kTokenGate: return launch_block_ring(moe::block_norm_ring_kernel<R, moe::kTokenGate>, r, a, stream);
+        default: return launch_block_ring(moe::block_norm_ring_kernel<R, moe::kFullGate>, r, a, stream);
     }
 }
 
-template <typename S>
-int launch_backward_ring(const Ring& r, const moe::BlockNormBackwardArgs& a, int gate, cudaStream_t stream) {
-    if (a.ds != nullptr)
-        return r.slots == 8   ? launch_backward_ring_gate<8, S, true>(r, a, gate, stream)
-               : r.slots == 4 ? launch_backward_ring_gate<4, S, true>(r, a, gate, stream)
-                              : launch_backward_ring_gate<2, S, true>(r, a, gate, stream);
-    return r.slots == 8   ? launch_backward_ring_gate<8, S, false>(r, a, gate, stream)
-           : r.slots == 4 ? launch_backward_ring_gate<4, S, false>(r, a, gate, stream)
-                          : launch_backward_ring_gate<2, S, false>(r, a, gate, stream);
+template <typename S, bool DS>
+int launch_backward_ring(const BlockRing& r, const moe::BlockNormBackwardArgs& a, int gate, cudaStream_t stream) {
+    switch (gate) {
+        case moe::kNoGate: return launch_block_ring(moe::block_norm_backward_ring_kernel<S, moe::kNoGate, DS>, r, a, stream);
+        case moe::kTokenGate: return launch_block_ring(moe::block_norm_backward_ring_kernel<S, moe::kTokenGate, DS>, r, a, stream);
+        default: return launch_block_ring(moe::block_norm_backward_ring_kernel<S, moe::kFullGate, DS>, r, a, stream);
+    }
 }
 
 // Blocks of the backward kernel's other forms: four an SM, no more than there are rows.
@@ -730,9 +730,8 @@ extern "C" MOE_API int moe_block_norm(const uint16_t* x, const void* residual, i
                                   weight_dtype == MOE_DTYPE_F32, N, H, residual_scale, eps, down, mean, y,
                                   residual_out, post_rstd, rstd, q, q_scale};
     // (the ring has no second sum for squares that vanish: only with an eps that covers them)
-    const Ring ring = eps >= moe::kLeastEps
-                          ? ring_for(N, H, static_cast<size_t>(H) * (2 + (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0)))
-                          : Ring();
+    const BlockRing ring = eps >= moe::kLeastEps ? block_ring_for(N, H, 2 + (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0))
+                                                 : BlockRing();
     if (ring.slots > 0)
         return f32 ? launch_forward_ring<float>(ring, a, kind, stream) : launch_forward_ring<uint16_t>(ring, a, kind, stream);
     if (H <= 512) {
@@ -785,8 +784,7 @@ extern "C" MOE_API int moe_block_norm_backward(const uint16_t* dy, const uint16_
     }
     if (workspace_bytes < moe_block_norm_backward_workspace_size(N, H)) return MOE_ERR_CAPACITY;
     const bool f32 = s_dtype == MOE_DTYPE_F32;
-    const size_t slot = static_cast<size_t>(H) * (4 + (ds != nullptr ? 2 : 1) * (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0));
-    const Ring ring = ring_for(N, H, slot);
+    const BlockRing ring = block_ring_for(N, H, 4 + (ds != nullptr ? 2 : 1) * (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0));
     const int blocks = ring.slots > 0 ? ring.blocks : backward_blocks(N, H);
     float* partial = static_cast<float*>(workspace);
     const moe::BlockNormBackwardArgs a = {dy, x, s, ds, gate, post_weight, weight, post_weight_dtype == MOE_DTYPE_F32,
@@ -795,7 +793,12 @@ extern "C" MOE_API int moe_block_norm_backward(const uint16_t* dy, const uint16_
     const dim3 grid(static_cast<unsigned>(blocks));
     int rc;
     if (ring.slots > 0) {
-        rc = f32 ? launch_backward_ring<float>(ring, a, kind, stream) : launch_backward_ring<uint16_t>(ring, a, kind, stream);
+        if (ds != nullptr)
+            rc = f32 ? launch_backward_ring<float, true>(ring, a, kind, stream)
+                     : launch_backward_ring<uint16_t, true>(ring, a, kind, stream);
+        else
+            rc = f32 ? launch_backward_ring<float, false>(ring, a, kind, stream)
+                     : launch_backward_ring<uint16_t, false>(ring, a, kind, stream);
     } else if (H <= 512) {
         const dim3 block(128);
         const size_t smem = 8 * sizeof(float) * H;
