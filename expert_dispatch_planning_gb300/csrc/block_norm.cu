@@ -167,9 +167,6 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) block_norm_kernel(cons
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
-// The warp's columns first .. of one row, to its place in shared memory: of 256 elements, or up to H.  Of fp32
-// rows the 16-byte chunks of every second eight are swapped in pairs, so that a read of eight lanes,
-// each 32 bytes from the next, is in different banks.
 __device__ __forceinline__ void copy_columns(uint16_t* to, const uint16_t* row, int first, int H) {
     const int h = first + 8 * (threadIdx.x & 31);
     if (h < H) copy16(to + h, row + h);
@@ -177,41 +174,157 @@ __device__ __forceinline__ void copy_columns(uint16_t* to, const uint16_t* row, 
 __device__ __forceinline__ void copy_columns(float* to, const float* row, int first, int H) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int chunk = (threadIdx.x & 31) + 32 * i, h = first + 4 * chunk;
-        if (h < H) copy16(to + first + 4 * (chunk ^ (chunk >> 3 & 1)), row + h);
+        const int h = first + 128 * i + 4 * (threadIdx.x & 31);
+        if (h < H) copy16(to + h, row + h);
     }
 }
-// The lane's eight columns from there.
-__device__ __forceinline__ void read8(const uint16_t* from, int first, float (&f)[8]) {
-    unpack8(*reinterpret_cast<const uint4*>(from + first + 8 * (threadIdx.x & 31)), f);
-}
-__device__ __forceinline__ void read8(const float* from, int first, float (&f)[8]) {
-    const int chunk = 2 * (threadIdx.x & 31), swap = chunk >> 3 & 1;
-    const float4 a = *reinterpret_cast<const float4*>(from + first + 4 * (chunk ^ swap));
-    const float4 b = *reinterpret_cast<const float4*>(from + first + 4 * ((chunk + 1) ^ swap));
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
+
+// The lane's eight columns: one run, or where there are fp32 rows (SPLIT) two runs of four, 128 columns apart, so
+// that the lanes' 16 bytes of an fp32 row are side by side.
+template <bool SPLIT>
+struct Columns {
+    int at;         // the first run's
+    bool in0, in1;  // the runs are inside the row
+    __device__ __forceinline__ explicit Columns(int H) {
+        at = threadIdx.x / 32 * 256 + (SPLIT ? 4 : 8) * (threadIdx.x & 31);
+        in0 = at < H;
+        in1 = (SPLIT ? at + 128 : at) < H;
+    }
+    // Of a row in the ring, whose places behind its end hold zeros.
+    template <typename T>
+    __device__ __forceinline__ void read(const T* row, float (&f)[8]) const {
+        if constexpr (SPLIT) {
+            float v[4];
+            load4(row + at, v);
+            f[0] = v[0], f[1] = v[1], f[2] = v[2], f[3] = v[3];
+            load4(row + at + 128, v);
+            f[4] = v[0], f[5] = v[1], f[6] = v[2], f[7] = v[3];
+        } else {
+            unpack8(*reinterpret_cast<const uint4*>(row + at), f);
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void write(T* row, const float (&f)[8]) const {
+        if constexpr (SPLIT) {
+            const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
+            if (in0) store4(row + at, a);
+            if (in1) store4(row + at + 128, b);
+        } else {
+            if (in0) store8(row, at / 8, f);
+        }
+    }
+    __device__ __forceinline__ void write(uint8_t* row, const Quantum& q, const float (&f)[8]) const {
+        const uint32_t a = q.round4(f), b = q.round4(f + 4);
+        if constexpr (SPLIT) {
+            if (in0) *reinterpret_cast<uint32_t*>(row + at) = a;
+            if (in1) *reinterpret_cast<uint32_t*>(row + at + 128) = b;
+        } else {
+            if (in0) *reinterpret_cast<uint2*>(row + at) = make_uint2(a, b);
+        }
+    }
+    __device__ __forceinline__ void weights(const void* w, int f32, float (&f)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int h = at + j + (SPLIT && j >= 4 ? 124 : 0);
+            f[j] = !(j < 4 ? in0 : in1) ? 0.f
+                   : f32                ? static_cast<const float*>(w)[h]
+                                        : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(w)[h]) << 16);
+        }
+    }
+};
 // Until at most slots - 1 of the thread's groups of copies are under way, and the warp's have landed.
 __device__ __forceinline__ void ring_wait(int slots) {
     if (slots == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else if (slots == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (slots == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else asm volatile("cp.async.wait_group 7;" ::: "memory");
+    else asm volatile("cp.async.wait_group 2;" ::: "memory");
     __syncwarp();
+}
+// Zeros in the places behind the rows' end (and everywhere else), before the first copies: the columns of
+// rows of `bytes` a slot.
+__device__ __forceinline__ void ring_clear(uint8_t* smem, uint32_t bytes) {
+    for (uint32_t v = 16 * threadIdx.x; v < bytes; v += 16 * blockDim.x)
+        *reinterpret_cast<uint4*>(smem + v) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+}
+// Two elements at a time: the arithmetic of a pair is one instruction, and these kernels' rows of
+// two-byte elements are bound by instructions and barriers before memory.
+struct Pair {
+    uint64_t v;
+};
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float2 parts(Pair p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+    return f;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    Pair p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+    return p;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+    Pair p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return p;
+}
+__device__ __forceinline__ float sum_of(Pair p) {
+    const float2 f = parts(p);
+    return f.x + f.y;
+}
+__device__ __forceinline__ Pair both(float f) { return pair(f, f); }
+__device__ __forceinline__ void split(const float (&f)[8], Pair (&p)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = pair(f[2 * j], f[2 * j + 1]);
+}
+__device__ __forceinline__ void join(const Pair (&p)[4], float (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = parts(p[j]);
+        f[2 * j] = v.x, f[2 * j + 1] = v.y;
+    }
+}
+template <bool SPLIT, typename T>
+__device__ __forceinline__ void read(const Columns<SPLIT>& c, const T* row, Pair (&p)[4]) {
+    float f[8];
+    c.read(row, f);
+    split(f, p);
+}
+
+// The block's sum of one value and maximum of another, with one barrier.  buf: two of 32 floats, and as
+// block_reduce's one of two sets.
+__device__ __forceinline__ float2 sum_and_max(float v, float m, float (*buf)[32]) {
+    auto fold = [&] {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            v += __shfl_xor_sync(FULL_MASK, v, o);
+            m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
+        }
+    };
+    fold();
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) buf[0][threadIdx.x >> 5] = v, buf[1][threadIdx.x >> 5] = m;
+    __syncthreads();
+    const bool there = lane < static_cast<int>(blockDim.x >> 5);
+    v = there ? buf[0][lane] : 0.f;
+    m = there ? buf[1][lane] : 0.f;
+    fold();
+    return make_float2(v, m);
 }
 // A row's place holds its columns rounded up to whole warps'.
 __host__ __device__ __forceinline__ int ring_columns(int H) { return (H + 255) / 256 * 256; }
 
-// R: the residual's element type.  slots: 2, 3, 4 or 8.
+// R: the residual's element type.  slots: 2 or 3.
 template <typename R, int GATE>
 __global__ void __launch_bounds__(kRingThreads) block_norm_ring_kernel(const BlockNormArgs a, const int slots) {
     extern __shared__ __align__(16) uint8_t smem[];  // [slots][x row, gate row, residual row]
     __shared__ float buf[2][3][32];
     pdl_wait();
     pdl_trigger();
-    const int H = a.H, W = ring_columns(H), first = threadIdx.x / 32 * 256, h = 8 * threadIdx.x;
-    const bool mine = h < H;
+    const int H = a.H, W = ring_columns(H), first = threadIdx.x / 32 * 256;
+    const Columns<sizeof(R) == 4> mine(H);
     constexpr int kNarrow = GATE == kFullGate ? 2 : 1;  // rows of two bytes an element
     const uint32_t slot_bytes = static_cast<uint32_t>(W) * (2 * kNarrow + sizeof(R));
     const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.N / gridDim.x;
@@ -226,69 +339,67 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_ring_kernel(const Blo
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float wp[8], w[8];
-    if (mine) {
-        load_weight8(a.post_weight, a.post_f32, threadIdx.x, wp);
-        load_weight8(a.weight, a.weight_f32, threadIdx.x, w);
-    }
+    Pair wp[4], w[4];
+    float f[8];
+    mine.weights(a.post_weight, a.post_f32, f);
+    split(f, wp);
+    mine.weights(a.weight, a.weight_f32, f);
+    split(f, w);
+    if (H != W) ring_clear(smem, slots * slot_bytes);
     for (int j = 0; j < slots - 1; ++j) fetch(begin + j, j);
+    const Pair down = both(a.down), alpha = both(a.alpha);
     float next_gate = GATE == kTokenGate && begin < end ? __ldg(static_cast<const float*>(a.gate) + begin) : 1.f;
     int slot = 0;  // the row's
     for (int64_t row = begin; row < end; ++row) {
         fetch(row + slots - 1, slot == 0 ? slots - 1 : slot - 1);
-        const float token_gate = next_gate;
+        const Pair token_gate = both(next_gate);
         if (GATE == kTokenGate && row + 1 < end) next_gate = __ldg(static_cast<const float*>(a.gate) + row + 1);
         ring_wait(slots);
         const uint16_t* x = reinterpret_cast<const uint16_t*>(smem + slot * slot_bytes);
         slot = slot + 1 == slots ? 0 : slot + 1;
         const int64_t at = row * H;
-        float(*sums)[32] = buf[row & 1];
-        float s[8];
-        float ss = 0.f;
-        if (mine) {
-            read8(x, first, s);
+        Pair s[4], sum = both(0.f);
+        read(mine, x, s);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float t = s[j] * a.down;
-                ss = fmaf(t, t, ss);
-            }
+        for (int j = 0; j < 4; ++j) {
+            const Pair t = s[j] * down;
+            sum = fma(t, t, sum);
         }
-        ss = block_reduce<false>(ss, sums[0]);
-        const float post = rsqrtf(fmaf(ss, a.mean, a.eps));  // within 2^-22
-        if (threadIdx.x == 0) a.post_rstd[row] = post;
-        ss = 0.f;
-        if (mine) {
-            float q[8], g[8];
-            read8(reinterpret_cast<const R*>(x + kNarrow * W), first, q);
-            if constexpr (GATE == kFullGate) read8(x + W, first, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float n = s[j] * post * wp[j];
-                if constexpr (GATE == kTokenGate) n *= token_gate;
-                if constexpr (GATE == kFullGate) n *= g[j];
-                s[j] = fmaf(a.alpha, q[j], n);
-                const float t = s[j] * a.down;
-                ss = fmaf(t, t, ss);
-            }
-            store8(static_cast<R*>(a.residual_out) + at, threadIdx.x, s);
-        }
-        ss = block_reduce<false>(ss, sums[1]);
-        const float rstd = rsqrtf(fmaf(ss, a.mean, a.eps));
-        if (threadIdx.x == 0) a.rstd[row] = rstd;
+        const float post_root = rsqrtf(fmaf(block_reduce<false>(sum_of(sum), buf[row & 1][0]), a.mean, a.eps));  // within 2^-22
+        if (threadIdx.x == 0) a.post_rstd[row] = post_root;
+        const Pair post = both(post_root);
+        Pair q[4], g[4];
+        read(mine, reinterpret_cast<const R*>(x + kNarrow * W), q);
+        if constexpr (GATE == kFullGate) read(mine, x + W, g);
+        // The row's largest |v| comes with its sum: of s * w, scaled up so that what is below the normal numbers
+        // keeps its digits (a row whose s * w * 2^32 overflows has a weight above 2^24, or its squares do too).
         float amax = 0.f;
-        if (mine) {
+        sum = both(0.f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                s[j] = s[j] * rstd * w[j];
-                amax = fmaxf(amax, fabsf(s[j]));
-            }
-            store8(a.y + at, threadIdx.x, s);
+        for (int j = 0; j < 4; ++j) {
+            Pair n = s[j] * post * wp[j];
+            if constexpr (GATE == kTokenGate) n = n * token_gate;
+            if constexpr (GATE == kFullGate) n = n * g[j];
+            s[j] = fma(alpha, q[j], n);
+            const Pair t = s[j] * down;
+            sum = fma(t, t, sum);
+            const float2 u = parts(s[j] * (w[j] * both(0x1p32f)));
+            amax = fmaxf(amax, fmaxf(fabsf(u.x), fabsf(u.y)));
         }
+        join(s, f);
+        mine.write(static_cast<R*>(a.residual_out) + at, f);
+        const float2 joined = sum_and_max(sum_of(sum), amax, buf[row & 1] + 1);
+        const float root = rsqrtf(fmaf(joined.x, a.mean, a.eps));
+        if (threadIdx.x == 0) a.rstd[row] = root;
+        const Pair rstd = both(root);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = s[j] * rstd * w[j];
+        join(s, f);
+        mine.write(a.y + at, f);
         if (a.q == nullptr) continue;
-        amax = block_reduce<true>(amax, sums[2]);
-        const Quantum q = quantum_of(amax);
-        if (threadIdx.x == 0) a.q_scale[row] = q.scale;
-        if (mine) *reinterpret_cast<uint2*>(a.q + at + h) = make_uint2(q.round4(s), q.round4(s + 4));
+        const Quantum quantum = quantum_of(joined.y * root * 0x1p-32f);
+        if (threadIdx.x == 0) a.q_scale[row] = quantum.scale;
+        mine.write(a.q + at, quantum, f);
     }
 }
 
@@ -455,8 +566,8 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_backward_ring_kernel(
     __shared__ float buf[2][2][32];
     pdl_wait();
     pdl_trigger();
-    const int H = a.H, W = ring_columns(H), first = threadIdx.x / 32 * 256, h = 8 * threadIdx.x;
-    const bool mine = h < H;
+    const int H = a.H, W = ring_columns(H), first = threadIdx.x / 32 * 256;
+    const Columns<sizeof(S) == 4> mine(H);
     constexpr int kNarrow = GATE == kFullGate ? 3 : 2;  // rows of two bytes an element
     const uint32_t slot_bytes = static_cast<uint32_t>(W) * (2 * kNarrow + (DS ? 2 : 1) * sizeof(S));
     const float over_h = 1.f / static_cast<float>(H);
@@ -476,13 +587,15 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_backward_ring_kernel(
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float w[8], wp[8], acc[8], post_acc[8];
-    if (mine) {
-        load_weight8(a.weight, a.weight_f32, threadIdx.x, w);
-        load_weight8(a.post_weight, a.post_f32, threadIdx.x, wp);
-    }
+    Pair w[4], wp[4], acc[4], post_acc[4];
+    float o[8];
+    mine.weights(a.weight, a.weight_f32, o);
+    split(o, w);
+    mine.weights(a.post_weight, a.post_f32, o);
+    split(o, wp);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = post_acc[j] = 0.f;
+    for (int j = 0; j < 4; ++j) acc[j] = post_acc[j] = both(0.f);
+    if (H != W) ring_clear(smem, slots * slot_bytes);
     for (int j = 0; j < slots - 1; ++j) fetch(begin + j, j);
     int slot = 0;  // the row's
     float next_rstd = 0.f, next_post = 0.f, next_gate = 1.f;
@@ -495,7 +608,8 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_backward_ring_kernel(
     scalars(begin);
     for (int64_t row = begin; row < end; ++row) {
         fetch(row + slots - 1, slot == 0 ? slots - 1 : slot - 1);
-        const float rstd = next_rstd, post = next_post, token_gate = next_gate;
+        const Pair rstd = both(next_rstd), post = both(next_post);
+        const float token_gate = next_gate;
         scalars(row + 1);
         ring_wait(slots);
         const uint16_t* dy = reinterpret_cast<const uint16_t*>(smem + slot * slot_bytes);
@@ -503,72 +617,66 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_backward_ring_kernel(
         const S* s = reinterpret_cast<const S*>(dy + kNarrow * W);
         const int64_t at = row * H;
         float(*sums)[32] = buf[row & 1];
-        float dot = 0.f;
-        if (mine) {
-            float t[8], hat[8];
-            read8(dy, first, t);
-            read8(s, first, hat);
+        Pair t[4], v[4], d[4], sum = both(0.f);
+        read(mine, dy, t);
+        read(mine, s, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                hat[j] *= rstd;
-                acc[j] = fmaf(t[j], hat[j], acc[j]);
-                dot = fmaf(t[j] * w[j], hat[j], dot);
-            }
+        for (int j = 0; j < 4; ++j) {
+            v[j] = v[j] * rstd;
+            acc[j] = fma(t[j], v[j], acc[j]);
+            sum = fma(t[j] * w[j], v[j], sum);
         }
-        const float mean = block_reduce<false>(dot, sums[0]) * over_h;
-        float d[8];
-        dot = 0.f;
-        if (mine) {
-            float t[8], v[8], o[8];
-            read8(dy, first, t);
-            read8(s, first, v);
+        const Pair mean = both(-block_reduce<false>(sum_of(sum), sums[0]) * over_h);
+        read(mine, dy, t);
+        read(mine, s, v);
+        if constexpr (DS) read(mine, s + W, d);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = 0.f;
-            if constexpr (DS) read8(s + W, first, d);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                d[j] += rstd * (t[j] * w[j] - v[j] * rstd * mean);
-                o[j] = a.alpha * d[j];
-            }
-            store8(static_cast<S*>(a.dres) + at, threadIdx.x, o);
-            read8(dy + W, first, v);
-            if constexpr (GATE == kFullGate) read8(dy + 2 * W, first, t);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] *= post;
-                const float n = v[j] * wp[j];
-                if constexpr (GATE == kFullGate) {
-                    o[j] = d[j] * n;
-                    d[j] *= t[j];
-                    dot = fmaf(d[j], n, dot);
-                } else {
-                    dot = fmaf(d[j], n, dot);
-                    d[j] *= token_gate;
-                }
-                post_acc[j] = fmaf(d[j], v[j], post_acc[j]);
-                d[j] *= wp[j];
-            }
-            if constexpr (GATE == kFullGate) store8(static_cast<uint16_t*>(a.dgate) + at, threadIdx.x, o);
+        for (int j = 0; j < 4; ++j) {
+            const Pair u = fma(v[j] * rstd, mean, t[j] * w[j]);
+            if constexpr (DS) d[j] = fma(rstd, u, d[j]);
+            else d[j] = rstd * u;
+            v[j] = both(a.alpha) * d[j];
         }
-        dot = block_reduce<false>(dot, sums[1]);
+        join(v, o);
+        mine.write(static_cast<S*>(a.dres) + at, o);
+        read(mine, dy + W, v);
+        if constexpr (GATE == kFullGate) read(mine, dy + 2 * W, t);
+        sum = both(0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = v[j] * post;
+            const Pair n = v[j] * wp[j];
+            sum = fma(d[j], GATE == kFullGate ? n * t[j] : n, sum);
+            if constexpr (GATE == kFullGate) {
+                const Pair c = t[j];
+                t[j] = d[j] * n;
+                d[j] = d[j] * c;
+            }
+            if constexpr (GATE == kTokenGate) d[j] = d[j] * both(token_gate);
+            post_acc[j] = fma(d[j], v[j], post_acc[j]);
+            d[j] = d[j] * wp[j];
+        }
+        if constexpr (GATE == kFullGate) {
+            join(t, o);
+            mine.write(static_cast<uint16_t*>(a.dgate) + at, o);
+        }
+        float dot = block_reduce<false>(sum_of(sum), sums[1]);
         if constexpr (GATE == kTokenGate) {
             if (threadIdx.x == 0) static_cast<float*>(a.dgate)[row] = dot;
             dot *= token_gate;
         }
-        const float post_mean = dot * over_h;
-        if (mine) {
-            float v[8];
-            read8(dy + W, first, v);
+        const Pair post_mean = both(-dot * over_h);
+        read(mine, dy + W, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = post * (d[j] - v[j] * post * post_mean);
-            store8(a.dx + at, threadIdx.x, d);
-        }
+        for (int j = 0; j < 4; ++j) d[j] = post * fma(v[j] * post, post_mean, d[j]);
+        join(d, o);
+        mine.write(a.dx + at, o);
     }
     float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * H;
-    if (mine) {
-        store8(out, threadIdx.x, acc);
-        store8(out + H, threadIdx.x, post_acc);
-    }
+    join(acc, o);
+    mine.write(out, o);
+    join(post_acc, o);
+    mine.write(out + H, o);
 }
 
 // The weights' gradients from the blocks' partials: 32 columns a block; each
@@ -632,26 +740,30 @@ int launch_backward(const moe::BlockNormBackwardArgs& a, bool f32, int gate, dim
                : launch_backward_gate<VPT, WARP, uint16_t>(a, gate, grid, block, smem, stream);
 }
 
-// The ring form of these kernels, with `bytes` a column of a row in a slot.  A row has two or three sums one
-// after the other, in which a block only waits: so an SM has as many blocks as its threads (64 registers
-// each) and two slots each allow, and slots as many as then fit.
+// The ring form of these kernels, with `bytes` a column of a row in a slot.  A row has two sums one after the
+// other, in which a block only waits: so an SM has as many blocks as its threads (64 registers each) allow,
+// but not more than ask for `ahead` bytes at a time.  More than that in flight, by more blocks or more slots,
+// costs up to a fifth again (the forward kernel at 2048 fp32 columns: 94% of the copy rate with two blocks of
+// two slots, 81% with four slots, 87% with four blocks; at 4096 columns of bf16 90% and 82%).  A third slot is for
+// blocks that are alone on their SM and small.
 struct BlockRing {
     int slots = 0, threads = 0, blocks = 0;  // slots = 0: not taken
     size_t smem = 0;
 };
-BlockRing block_ring_for(int N, int H, int bytes) {
+constexpr int kMostBlocks = 8;  // of an SM
+constexpr size_t kForwardAhead = 36 * 1024, kBackwardAhead = 96 * 1024;
+BlockRing block_ring_for(int N, int H, int bytes, size_t ahead) {
     constexpr size_t kSmem = 220 * 1024;
     const size_t slot = static_cast<size_t>(moe::ring_columns(H)) * bytes;
     BlockRing r;
     if (H <= 512 || H > 8 * moe::kRingThreads || 2 * slot > kSmem) return r;
     const int threads = moe::ring_columns(H) / 8;
     int per_sm = moe::kRingThreads / threads;
-    const int by_smem = static_cast<int>(kSmem / (2 * slot));
-    if (by_smem < per_sm) per_sm = by_smem;
-    if (per_sm > 6) per_sm = 6;
-    const int fit = static_cast<int>(kSmem / (per_sm * slot)), blocks = num_sms() * per_sm;
+    if (per_sm > kMostBlocks) per_sm = kMostBlocks;
+    while (per_sm > 1 && (per_sm * slot > ahead || 2 * per_sm * slot > kSmem)) --per_sm;
+    const int blocks = num_sms() * per_sm;
     if (N < 4 * blocks) return r;
-    r.slots = fit >= 8 ? 8 : fit >= 4 ? 4 : fit;
+    r.slots = per_sm == 1 && 3 * slot <= kSmem && (slot <= kForwardAhead || threads <= moe::kRingThreads / 2) ? 3 : 2;
     r.threads = threads;
     r.blocks = blocks;
     r.smem = r.slots * slot;
@@ -730,10 +842,11 @@ extern "C" MOE_API int moe_block_norm(const uint16_t* x, const void* residual, i
                                   weight_dtype == MOE_DTYPE_F32, N, H, residual_scale, eps, down, mean, y,
                                   residual_out, post_rstd, rstd, q, q_scale};
     // (the ring has no second sum for squares that vanish: only with an eps that covers them)
-    const BlockRing ring = eps >= moe::kLeastEps ? block_ring_for(N, H, 2 + (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0))
-                                                 : BlockRing();
-    if (ring.slots > 0)
-        return f32 ? launch_forward_ring<float>(ring, a, kind, stream) : launch_forward_ring<uint16_t>(ring, a, kind, stream);
+    if (eps >= moe::kLeastEps) {
+        const BlockRing ring = block_ring_for(N, H, 2 + (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0), kForwardAhead);
+        if (ring.slots > 0)
+            return f32 ? launch_forward_ring<float>(ring, a, kind, stream) : launch_forward_ring<uint16_t>(ring, a, kind, stream);
+    }
     if (H <= 512) {
         const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(N) + 3) / 4)), block(128);
         return H <= 256 ? launch_forward<1, true>(a, f32, kind, grid, block, stream)
@@ -749,8 +862,8 @@ extern "C" MOE_API int moe_block_norm(const uint16_t* x, const void* residual, i
 
 extern "C" MOE_API size_t moe_block_norm_backward_workspace_size(int N, int H) {
     if (N < 0 || H < 8 || H % 8 != 0 || H > kMaxH) return 0;
-    int blocks = backward_blocks(N, H);  // the ring form may have more, of the narrowest type
-    if (N > blocks) blocks = N < 6 * num_sms() ? N : 6 * num_sms();
+    int blocks = backward_blocks(N, H);  // the ring form may have more
+    if (N > blocks) blocks = N < kMostBlocks * num_sms() ? N : kMostBlocks * num_sms();
     return static_cast<size_t>(blocks > 0 ? blocks : 1) * 2 * H * sizeof(float);
 }
 
@@ -784,7 +897,8 @@ extern "C" MOE_API int moe_block_norm_backward(const uint16_t* dy, const uint16_
     }
     if (workspace_bytes < moe_block_norm_backward_workspace_size(N, H)) return MOE_ERR_CAPACITY;
     const bool f32 = s_dtype == MOE_DTYPE_F32;
-    const BlockRing ring = block_ring_for(N, H, 4 + (ds != nullptr ? 2 : 1) * (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0));
+    const BlockRing ring = block_ring_for(N, H, 4 + (ds != nullptr ? 2 : 1) * (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0),
+                                          kBackwardAhead);
     const int blocks = ring.slots > 0 ? ring.blocks : backward_blocks(N, H);
     float* partial = static_cast<float*>(workspace);
     const moe::BlockNormBackwardArgs a = {dy, x, s, ds, gate, post_weight, weight, post_weight_dtype == MOE_DTYPE_F32,

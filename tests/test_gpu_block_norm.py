@@ -36,7 +36,8 @@ def rand(*shape, seed=0):
 
 # a row in one warp (up to 512), in a block with 1, 2 or 4 chunks a thread, the bounds between them, and many rows
 SIZES = [(1, 8), (3, 128), (7, 256), (5, 264), (129, 512), (2, 520), (1, 2048), (33, 2056), (4, 4096), (9, 7168),
-         (3, 8200), (2, 16384), (1, 32768), (1000, 136), (4001, 520), (1300, 1000), (3700, 1000), (2500, 4104), (1111, 7168), (700, 8192)]
+         (3, 8200), (2, 16384), (1, 32768), (1000, 136), (5003, 520), (1300, 1000), (4900, 1000), (2500, 2048), (1300, 4104),
+         (1400, 4096), (1111, 7168), (700, 8192)]
 KINDS = [(BF16, None, BF16, BF16), (F32, "token", F32, BF16), (BF16, "full", BF16, F32), (F32, "full", F32, F32),
          (F32, None, BF16, BF16), (BF16, "token", BF16, BF16)]
 
@@ -122,7 +123,7 @@ def test_in_place_and_given_outputs(m, res, N, H):
     assert torch.equal(q.view(torch.uint8), o.q.view(torch.uint8))
 
 
-@pytest.mark.parametrize("N", [12, 3000])
+@pytest.mark.parametrize("N", [12, 6000])
 @pytest.mark.parametrize("gate", [None, "token", "full"])
 def test_special_rows(m, N, gate):
     """Rows of zeros, of tiny and of huge values; NaN and infinities stay in their own rows; a closed gate."""
@@ -267,6 +268,20 @@ def test_backward_against_differences(m, gate):
         assert abs(float(diff - (grad * way).sum())) <= 1e-6 * float((grad * way).abs().sum())
 
 
+@pytest.mark.parametrize("res", [BF16, F32])
+@pytest.mark.parametrize("N", [40, 6000])
+def test_quantised_rows_of_every_size(m, N, res):
+    """The 8-bit output's scale and values of rows from the smallest numbers to large ones, few rows and many."""
+    H = 640
+    size = 10.0 ** torch.linspace(-42 if res == F32 else -39, 18, N, device="cuda")[:, None]
+    x, r = torch.zeros(N, H, dtype=BF16, device="cuda"), (rand(N, H) * size).to(res)
+    w = torch.full((H,), 0.5, device="cuda")
+    eps = 2.0 ** -80
+    o = m.block_norm(x, r, w, w, eps=eps, quantize=True)
+    e = forward64(x, r, w, w, None, alpha=1.0, eps=eps)
+    check_forward(o, e, res, H)
+
+
 def test_empty_batch(m):
     H = 256
     x, r, w = torch.empty(0, H, dtype=BF16, device="cuda"), torch.empty(0, H, device="cuda"), torch.ones(H, device="cuda")
@@ -276,7 +291,7 @@ def test_empty_batch(m):
     assert (g[3] == 0).all() and (g[4] == 0).all() and g[2].shape == (0,)
 
 
-@pytest.mark.parametrize("N,H", [(5, 512), (7, 1000), (1400, 1000), (1400, 7168)])
+@pytest.mark.parametrize("N,H", [(5, 512), (7, 1000), (2500, 1000), (1400, 7168)])
 def test_guard_zones(m, N, H):
     """Nothing is written outside the outputs."""
     x, r, wp, w, c = inputs(N, H, F32, "full", BF16, BF16)
