@@ -88,6 +88,46 @@ struct Chosen {
 __device__ __noinline__ int choose(uint8_t* smem, int N, int K, int E, const int32_t* topk_idx, const float* topk_w) {
     const Chosen c(smem, N, K, E);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pairs = N * K;
+    if (pairs <= 32) {  // one warp, a lane a pair; experts in the order of their first pairs (figures)
+        if (warp == 0) {
+            int e = -1 - lane;  // of no pair: unlike any other
+            float w = 0.f;
+            if (lane < pairs) {
+                const int i = topk_idx[lane];
+                w = topk_w[lane];
+                if (static_cast<unsigned>(i) < static_cast<unsigned>(E)) e = i;
+            }
+            const unsigned same = __match_any_sync(FULL_MASK, e), below = (1u << lane) - 1;
+            const int leader = __ffs(same) - 1;
+            const bool leads = e >= 0 && leader == lane;
+            const unsigned leaders = __ballot_sync(FULL_MASK, leads);
+            int before = leads ? __popc(same) : 0;  // pairs of this leader and those ahead of it
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(FULL_MASK, before, o);
+                if (lane >= o) before += t;
+            }
+            const int all = __shfl_sync(FULL_MASK, before, 31);
+            const int first = __shfl_sync(FULL_MASK, before, leader) - __popc(same);
+            if (leads) {
+                const int i = __popc(leaders & below);
+                c.expert[i] = e;
+                c.begin[i] = first;
+            }
+            if (e >= 0) {
+                const int p = first + __popc(same & below);
+                c.token[p] = static_cast<uint8_t>(lane / K);
+                c.pair[p] = static_cast<uint16_t>(lane);
+                c.weight[p] = w;
+            }
+            if (lane == 0) {
+                c.begin[__popc(leaders)] = all;
+                c.sums[0] = __popc(leaders);
+            }
+        }
+        __syncthreads();
+        return c.sums[0];
+    }
 #pragma unroll 1
     for (int e = tid; e < E; e += kLayerThreads) c.tokens[e] = 0;
     __syncthreads();
@@ -239,9 +279,15 @@ struct WeightRing {
         from = mine + g * kStepBytes + (t ^ (g & 1) << 2) * 16;
     }
     // The step at byte `k` of the rows; zeros behind a row's end (`bytes`) and for rows that are not there.
-    __device__ __forceinline__ void fetch(const WeightRows& w, int k, int bytes) {
+    // What is not read `again` is the first to leave L2, before tokens, h and the kernels' code
+    // (layer_batch 329 -> 321 us).
+    __device__ __forceinline__ void fetch(const WeightRows& w, int k, int bytes, bool again) {
         const int r = (threadIdx.x & 31) >> 3, mine = k + static_cast<int>(threadIdx.x & 7) * 16;
         const uint8_t* first = w.lane + k;
+        uint64_t once, kept;
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(kept));
+        const uint64_t policy = again ? kept : once;
         const uint32_t slot = to + fill;
         fill = fill == (DEPTH - 1) * kStep ? 0 : fill + kStep;
         __syncwarp();  // all lanes have read what was there
@@ -253,8 +299,9 @@ struct WeightRing {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const bool in = (HALVES ? 8 * m : 16 * m + 8 * half) + 4 * i + r < w.n && mine < bytes;
-                    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(slot + (4 * (2 * m + half) + 2 * i) * 256),
-                                 "l"(in ? eight + i * w.four : w.any), "r"(in ? 16 : 0)
+                    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2, %3;" ::"r"(
+                                     slot + (4 * (2 * m + half) + 2 * i) * 256),
+                                 "l"(in ? eight + i * w.four : w.any), "r"(in ? 16 : 0), "l"(policy)
                                  : "memory");
                 }
             }
@@ -492,7 +539,7 @@ __global__ void __launch_bounds__(kLayerThreads, 2) layer_rows_kernel(const Laye
                     w.set(DOWN ? static_cast<const void*>(a.w_down) : a.w_gate_up, first, row, weights.n);
                     weights.fresh = false;
                 }
-                ring.fetch(w, weights.step * kStepBytes, bytes);
+                ring.fetch(w, weights.step * kStepBytes, bytes, weights.pass + 1 < weights.passes);
                 weights.advance(c, units, warp, steps);
             }
             Ring::commit();
@@ -571,7 +618,7 @@ struct DownWalk {
     }
 };
 
-constexpr int kDownRows = 16 * kTiles;
+constexpr int kDownRows = 16 * kTiles, kDownBlocks = 4;  // of a cluster: rows, and blocks at most
 using DownRing = WeightRing<kTiles, false, 3>;
 
 // A part's products, weighted, are added to the warp's sums [rows][N].
@@ -596,12 +643,11 @@ __device__ __forceinline__ void down_add(const LayerArgs& a, const Chosen& c, fl
     __syncwarp();  // the next expert's tokens are other lanes'
 }
 
-__device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
+// Into the memory of the cluster's first block.
+__device__ __forceinline__ void store_first(float* p, float v) {
     uint32_t at;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(p)));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
 // A cluster has `rows` rows of the output, at most kDownRows; all warps of its blocks share the
@@ -610,12 +656,15 @@ __global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const Laye
     extern __shared__ __align__(128) uint8_t smem[];
     DownRing ring(smem);
     float* sums = reinterpret_cast<float*>(smem + kLayerWarps * DownRing::kWarpBytes);  // [warps][rows][N]
-    uint8_t* lists = reinterpret_cast<uint8_t*>(sums) + sizeof(float) * kLayerWarps * kDownRows * a.N;
+    float* parts = sums + kLayerWarps * kDownRows * a.N;  // [blocks of a cluster][rows][N], of the first
+    uint8_t* lists = reinterpret_cast<uint8_t*>(parts + kDownBlocks * kDownRows * a.N);
     const Chosen c(lists, a.N, a.K, a.E);
     const int tid = threadIdx.x, warp = tid >> 5;
     uint32_t rank, blocks;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(blocks));
+    // (waited for before the first write into another block's memory, which has to run by then)
+    if (blocks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 #pragma unroll 1
     for (int v = tid; v < kLayerWarps * kDownRows * a.N; v += kLayerThreads) sums[v] = 0.f;
     // topk_idx and the weights come from before the launch that this one may overlap
@@ -649,7 +698,7 @@ __global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const Laye
                 w.set(a.w_down, static_cast<int64_t>(c.expert[weights.expert]) * a.H + first_row, row, there);
                 weights.fresh = false;
             }
-            ring.fetch(w, weights.step * kStepBytes, bytes);
+            ring.fetch(w, weights.step * kStepBytes, bytes, false);
             weights.advance();
         }
         DownRing::commit();
@@ -684,23 +733,31 @@ __global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const Laye
         }
     }
     __syncthreads();
+    if (blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+#pragma unroll 1
     for (int v = tid; v < kDownRows * a.N; v += kLayerThreads) {
         float o = sums[v];
 #pragma unroll 1
         for (int w = 1; w < kLayerWarps; ++w) o += sums[w * kDownRows * a.N + v];
-        sums[v] = o;
+        store_first(parts + rank * kDownRows * a.N + v, o);
     }
-    // the blocks' sums are joined in their order, each block an equal part of them
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    for (int v = rank * kLayerThreads + tid; v < kDownRows * a.N; v += blocks * kLayerThreads) {
+    // the first block joins the blocks' sums, in their order; nobody reads the others' memory
+    if (blocks > 1) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        if (rank != 0) return;
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+#pragma unroll 1
+    for (int v = tid; v < kDownRows * a.N; v += kLayerThreads) {
         const int row = v % kDownRows, s = v / kDownRows;  // neighbouring threads write neighbouring elements
         if (row >= there) continue;
         float o = 0.f;
-        for (uint32_t r = 0; r < blocks; ++r) o += load_cluster(sums + row * a.N + s, r);
+#pragma unroll 1
+        for (uint32_t r = 0; r < blocks; ++r) o += parts[(r * kDownRows + row) * a.N + s];
         a.out[static_cast<int64_t>(s) * a.H + first_row + row] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
     }
-    // a block's sums stay until the others have read them
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace moe
@@ -723,7 +780,8 @@ int launch_rows(const LayerArgs& a, cudaStream_t stream) {
 }
 
 int launch_down(const LayerArgs& a, cudaStream_t stream) {
-    const size_t smem = moe::kLayerWarps * (moe::DownRing::kWarpBytes + sizeof(float) * moe::kDownRows * a.N) +
+    const size_t smem = moe::kLayerWarps * moe::DownRing::kWarpBytes +
+                        sizeof(float) * (moe::kLayerWarps + moe::kDownBlocks) * moe::kDownRows * a.N +
                         moe::Chosen::bytes(a.N, a.K, a.E);
     if (cudaFuncSetAttribute(moe::layer_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess)
         return MOE_ERR_CUDA;
@@ -734,7 +792,7 @@ int launch_down(const LayerArgs& a, cudaStream_t stream) {
     int rows = (a.H + slots - 1) / slots, blocks = 1;
     if (2 * rows <= moe::kDownRows) {
         rows = moe::kDownRows;
-        while (blocks < 4 && (a.H + rows - 1) / rows * blocks * 2 <= slots) blocks *= 2;
+        while (blocks < moe::kDownBlocks && (a.H + rows - 1) / rows * blocks * 2 <= slots) blocks *= 2;
     }
     if (rows > moe::kDownRows) rows = moe::kDownRows;
     const int groups = (a.H + rows - 1) / rows;
