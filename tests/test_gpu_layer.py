@@ -93,7 +93,9 @@ def check(m, a, K, **routing):
 
 SIZES = [(1, 1, 1, 8, 8), (1, 8, 2, 128, 72), (3, 4, 4, 24, 8), (2, 5, 3, 72, 200), (8, 16, 2, 264, 136), (9, 8, 8, 256, 64),
          (1, 128, 8, 2048, 768), (17, 60, 4, 1000, 712), (33, 128, 8, 512, 192), (64, 8, 2, 640, 328), (64, 3, 1, 128, 64),
-         (5, 1024, 32, 64, 16), (64, 1024, 32, 64, 24), (7, 4, 2, 4880, 40), (64, 6, 3, 4888, 72), (20, 33, 5, 96, 1032)]
+         (5, 1024, 32, 64, 16), (64, 1024, 32, 64, 24), (7, 4, 2, 4880, 40), (64, 6, 3, 4888, 72), (20, 33, 5, 96, 1032),
+         # many tiles a block; more tokens an expert than a pass takes
+         (8, 128, 8, 1024, 456), (24, 60, 4, 1032, 712), (33, 64, 4, 1032, 1048), (64, 48, 12, 1040, 1024)]
 
 
 @pytest.mark.parametrize("N,E,K,H,I", SIZES)
@@ -102,7 +104,7 @@ def test_bf16(m, N, E, K, H, I):  # noqa: E741
 
 
 @pytest.mark.parametrize("N,E,K,H,I", [(1, 2, 1, 16, 8), (3, 8, 2, 272, 72), (1, 128, 8, 2048, 768), (12, 16, 4, 1040, 200),
-                                       (31, 60, 6, 512, 136), (64, 8, 2, 256, 264), (6, 4, 3, 4880, 24)])
+                                       (31, 60, 6, 512, 136), (64, 8, 2, 256, 264), (6, 4, 3, 4880, 24), (16, 64, 6, 2064, 440)])
 def test_8bit(m, N, E, K, H, I):  # noqa: E741
     check(m, inputs(N, E, H, I, bits=8), K)
 
@@ -229,7 +231,7 @@ def test_refusals(m):
 
 def test_two_calls_at_once(m):
     """Calls on two streams, each with its own workspace."""
-    a, b = inputs(8, 32, 512, 200, seed=1), inputs(5, 64, 1024, 128, seed=2)
+    a, b = inputs(8, 32, 512, 200, seed=1), inputs(30, 64, 1024, 1040, seed=2)
     wa, wb = m.layer(K=4, **a), m.layer(K=6, **b)
     s, t = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -239,9 +241,10 @@ def test_two_calls_at_once(m):
         assert torch.equal(x, wa) and torch.equal(y, wb)
 
 
-def test_graph(m):
+@pytest.mark.parametrize("N,E,H,I", [(6, 16, 256, 136), (20, 64, 1024, 1024)])
+def test_graph(m, N, E, H, I):  # noqa: E741
     """Two captured layers in a row, the second on the first one's output; replayed with new inputs."""
-    a, b = inputs(6, 16, 256, 136, seed=1), inputs(6, 16, 256, 72, seed=2)
+    a, b = inputs(N, E, H, I, seed=1), inputs(N, 16, H, 72, seed=2)
     del b["x"]
 
     def both(stream=None):
@@ -253,7 +256,7 @@ def test_graph(m):
     with torch.cuda.graph(graph):
         y, z = both()
     for seed in (5, 6):
-        new = inputs(6, 16, 256, 136, seed=seed)
+        new = inputs(N, E, H, I, seed=seed)
         a["x"].copy_(new["x"])
         a["logits"].copy_(new["logits"])
         for _ in range(3):
