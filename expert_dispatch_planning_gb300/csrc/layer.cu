@@ -242,7 +242,7 @@ template <bool Q>
 __device__ __forceinline__ void product(float (&c)[4], const Fragment<Q>& lo, const Fragment<Q>& hi,
                                         const Fragment<Q>& b) {
 #pragma unroll
-    for (int i = 0; i < (Q ? 4 : 2); ++i) mma<Q>(c, lo.w[2 * i], hi.w[2 * i], lo.w[2 * i + 1], hi.w[2 * i + 1], b.w[2 * i], b.w[2 * i + 1]);
+    for (int i = 0; i < (Q ? 8 : 4); i += 2) mma<Q>(c, lo.w[i], hi.w[i], lo.w[i + 1], hi.w[i + 1], b.w[i], b.w[i + 1]);
 }
 
 // Not a read-only load: h comes from the launch before, which may still run as this one starts.
@@ -252,6 +252,7 @@ __device__ __forceinline__ uint4 load16(const uint8_t* p, bool inside) {
         asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
     return v;
 }
+
 // A warp's ring of weight steps in shared memory, filled by its own copies (cp.async): no
 // other warp waits for it, and it runs on over the ends of tiles and experts, so that memory
 // is kept busy while the warps join their sums.  A step is kStepBytes of each of the warp's MT
@@ -481,8 +482,8 @@ __device__ __forceinline__ void join(const LayerArgs& a, const Chosen& c, float4
             if (row >= walk.n) continue;
             float wg = 1.f, wu = 1.f;
             if constexpr (Q) {
-                wg = __ldg(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + ch);
-                wu = __ldg(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + a.I + ch);
+                wg = ld_stream_f32(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + ch);
+                wu = ld_stream_f32(a.w_scale + static_cast<int64_t>(e) * 2 * a.I + a.I + ch);
             }
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
@@ -490,7 +491,7 @@ __device__ __forceinline__ void join(const LayerArgs& a, const Chosen& c, float4
                 if (p >= cols) continue;
                 float gate = v == 0 ? s.x : s.y, up = v == 0 ? s.z : s.w;
                 if constexpr (Q) {
-                    const float xs = __ldg(a.x_scale + c.token[first + p]);
+                    const float xs = ld_stream_f32(a.x_scale + c.token[first + p]);
                     gate = gate * wg * xs;
                     up = up * wu * xs;
                 }
@@ -787,8 +788,8 @@ int launch_rows(const LayerArgs& a, cudaStream_t stream) {
     if (cudaFuncSetAttribute(moe::layer_rows_kernel<Q, DOWN, EIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
-    return launch(moe::layer_rows_kernel<Q, DOWN, EIGHTS>, dim3(static_cast<unsigned>(2 * num_sms())), dim3(moe::kLayerThreads), smem,
-                  stream, a);
+    const dim3 grid(static_cast<unsigned>(2 * num_sms())), block(moe::kLayerThreads);
+    return launch(moe::layer_rows_kernel<Q, DOWN, EIGHTS>, grid, block, smem, stream, a);
 }
 
 int launch_down(const LayerArgs& a, cudaStream_t stream) {
