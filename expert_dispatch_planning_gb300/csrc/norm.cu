@@ -235,6 +235,21 @@ __global__ void __launch_bounds__(WARP ? 128 : 256 * VPT) norm_backward_kernel(c
 }
 
 // ---------------------------------------------------------------- ring
+// A thread owns groups of four columns, t, t + T, ...: 8 bytes of a bf16 row,
+// 16 of an fp32 one, neighbouring threads side by side.
+__device__ __forceinline__ void cp_async_group(uint16_t* dst, const uint16_t* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_group(float* dst, const float* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void load_weight4(const void* w, int f32, int h, float (&f)[4]) {
+    if (f32) load4(static_cast<const float*>(w) + h, f);
+    else load4(static_cast<const uint16_t*>(w) + h, f);
+}
+
+constexpr int kRingGroups = 2;  // groups of four columns a thread at most: H <= 8192
+
 // R: the residual's element type (uint16_t also stands for none).
 template <int SLOTS, typename R, bool RES>
 __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs a) {
@@ -449,6 +464,42 @@ int launch_backward(const moe::NormBackwardArgs& a, bool f32, dim3 grid, dim3 bl
                     cudaStream_t stream) {
     if (f32) return moe_host::launch(moe::norm_backward_kernel<VPT, WARP, float>, grid, block, smem, stream, a);
     return moe_host::launch(moe::norm_backward_kernel<VPT, WARP, uint16_t>, grid, block, smem, stream, a);
+}
+
+// The ring form: `slot` bytes a row, two to eight slots, blocks as many as
+// their rings and threads fit an SM.  Taken when every block gets a few rows
+// (fewer would only wait for their own) and a row has enough columns to keep
+// its barrier cheap.  The forward kernel's is not taken with an eps (0, say) that does
+// not cover vanishing squares: the ring has no second sum, since a branch in
+// its loop costs up to a fifth (16384 x 1024: 16.6 us without, 19.6 us with it).
+struct Ring {
+    int slots = 0, threads = 0, blocks = 0;  // slots = 0: not taken
+    size_t smem = 0;
+};
+Ring ring_for(int N, int H, size_t slot) {
+    constexpr size_t kSmem = 220 * 1024;
+    Ring r;
+    if (H <= 512 || H > 4 * moe::kRingGroups * moe::kRingThreads || 2 * slot > kSmem) return r;
+    const int slots = 8 * slot <= kSmem / 2 ? 8 : 4 * slot <= kSmem ? 4 : 2;
+    const int per_thread = 4 * moe::kRingGroups;
+    const int threads = (H + 32 * per_thread - 1) / (32 * per_thread) * 32;
+    const int by_smem = static_cast<int>(kSmem / (slots * slot)), by_threads = 1536 / threads;
+    const int per_sm = by_smem < by_threads ? by_smem : by_threads;
+    const int blocks = num_sms() * (per_sm < 1 ? 1 : per_sm > 6 ? 6 : per_sm);
+    if (N < 4 * blocks) return r;
+    r.slots = slots;
+    r.threads = threads;
+    r.blocks = blocks;
+    r.smem = slots * slot;
+    return r;
+}
+
+template <typename Kernel, typename Args>
+int launch_ring(Kernel kernel, const Ring& r, const Args& a, cudaStream_t stream) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return launch(kernel, dim3(static_cast<unsigned>(r.blocks)), dim3(static_cast<unsigned>(r.threads)), r.smem, stream,
+                  a);
 }
 
 template <int SLOTS>

@@ -1,6 +1,6 @@
 // norm_parts.cuh -- what the kernels of norm.cu and block_norm.cu share: sums
-// and maxima over a row's threads, the 8-bit output's rounding, the ring of
-// rows in shared memory, and the host's choice of a launch.
+// and maxima over a row's threads, loads and stores of elements held in fp32,
+// the 8-bit output's rounding, and the host's choice of a launch.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -81,15 +81,7 @@ __device__ __forceinline__ Quantum quantum_of(float amax) {
     return q;
 }
 
-// ---------------------------------------------------------------- ring
-// A thread owns groups of four columns, t, t + T, ...: 8 bytes of a bf16 row,
-// 16 of an fp32 one, neighbouring threads side by side.
-__device__ __forceinline__ void cp_async_group(uint16_t* dst, const uint16_t* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_group(float* dst, const float* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
+// ---------------------------------------------------------------- four elements, the block's sums
 __device__ __forceinline__ void load4(const uint16_t* p, float (&f)[4]) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
@@ -104,10 +96,6 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
 }
 __device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-}
-__device__ __forceinline__ void load_weight4(const void* w, int f32, int h, float (&f)[4]) {
-    if (f32) load4(static_cast<const float*>(w) + h, f);
-    else load4(static_cast<const uint16_t*>(w) + h, f);
 }
 
 // The block's sum or maximum with one barrier: `buf` holds two sets of 32
@@ -131,7 +119,6 @@ __device__ __forceinline__ float block_reduce(float v, float* buf) {
 }
 
 constexpr int kRingThreads = 1024;
-constexpr int kRingGroups = 2;  // groups of four columns a thread at most: H <= 8192
 
 }  // namespace moe
 
@@ -147,34 +134,6 @@ inline bool float_type(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32
 inline int norm_vpt(int H) { return H <= 2048 ? 1 : H <= 8192 ? 2 : 4; }
 inline int norm_threads(int H) { return (H / 8 + 32 * norm_vpt(H) - 1) / (32 * norm_vpt(H)) * 32; }
 
-// The ring form: `slot` bytes a row, two to eight slots, blocks as many as
-// their rings and threads fit an SM.  Taken when every block gets a few rows
-// (fewer would only wait for their own) and a row has enough columns to keep
-// its barrier cheap.  The forward kernel's is not taken with an eps (0, say) that does
-// not cover vanishing squares: the ring has no second sum, since a branch in
-// its loop costs up to a fifth (16384 x 1024: 16.6 us without, 19.6 us with it).
-struct Ring {
-    int slots = 0, threads = 0, blocks = 0;  // slots = 0: not taken
-    size_t smem = 0;
-};
-inline Ring ring_for(int N, int H, size_t slot) {
-    constexpr size_t kSmem = 220 * 1024;
-    Ring r;
-    if (H <= 512 || H > 4 * moe::kRingGroups * moe::kRingThreads || 2 * slot > kSmem) return r;
-    const int slots = 8 * slot <= kSmem / 2 ? 8 : 4 * slot <= kSmem ? 4 : 2;
-    const int per_thread = 4 * moe::kRingGroups;
-    const int threads = (H + 32 * per_thread - 1) / (32 * per_thread) * 32;
-    const int by_smem = static_cast<int>(kSmem / (slots * slot)), by_threads = 1536 / threads;
-    const int per_sm = by_smem < by_threads ? by_smem : by_threads;
-    const int blocks = num_sms() * (per_sm < 1 ? 1 : per_sm > 6 ? 6 : per_sm);
-    if (N < 4 * blocks) return r;
-    r.slots = slots;
-    r.threads = threads;
-    r.blocks = blocks;
-    r.smem = slots * slot;
-    return r;
-}
-
 // Squares are summed scaled down by a power of two near 1/sqrt(H), so that a
 // row overflows only where a mean square does; `mean` is 1/(H down^2).
 inline void square_scale(int H, float* down, float* mean) {
@@ -182,14 +141,6 @@ inline void square_scale(int H, float* down, float* mean) {
     while ((int64_t(1) << (2 * k)) < H) ++k;
     *down = std::ldexp(1.f, -k);
     *mean = static_cast<float>(static_cast<double>(int64_t(1) << (2 * k)) / H);
-}
-
-template <typename Kernel, typename Args>
-int launch_ring(Kernel kernel, const Ring& r, const Args& a, cudaStream_t stream) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    return launch(kernel, dim3(static_cast<unsigned>(r.blocks)), dim3(static_cast<unsigned>(r.threads)), r.smem, stream,
-                  a);
 }
 
 }  // namespace moe_host
