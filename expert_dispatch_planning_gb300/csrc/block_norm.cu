@@ -861,7 +861,6 @@ extern "C" MOE_API int moe_block_norm(const uint16_t* x, const void* residual, i
     const moe::BlockNormArgs a = {x, residual, gate, post_weight, weight, post_weight_dtype == MOE_DTYPE_F32,
                                   weight_dtype == MOE_DTYPE_F32, N, H, residual_scale, eps, down, mean, y,
                                   residual_out, post_rstd, rstd, q, q_scale};
-    // (the ring has no second sum for squares that vanish: only with an eps that covers them)
     const int rows = H > 2048 ? 4 : H >= 1024 && !f32 ? 16 : 0;
     // (the ring has no second sum for squares that vanish: only with an eps that covers them)
     if (eps >= moe::kLeastEps && rows > 0) {
