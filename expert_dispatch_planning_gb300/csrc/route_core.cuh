@@ -76,12 +76,15 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 
 // e^(a - b) for a <= b, with the rounding error of the subtraction carried
 // to first order (TwoSum), so only the exponential's own error remains.
+// Where the difference is infinite (a is -infinity, or the two are too far
+// apart for fp32) TwoSum's terms are NaN: below -104 e is 0, and so is the
+// result.  Two infinities of one sign have no difference: NaN.
 __device__ __forceinline__ float exp_diff(float a, float b) {
     const float s = __fsub_rn(a, b);
     const float bb = __fsub_rn(s, a);
     const float err = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(-b, bb));
     const float e = exp_nonpos(s);
-    return __fmaf_rn(e, err, e);
+    return s < -104.0f ? 0.0f : __fmaf_rn(e, err, e);
 }
 
 // Float-float accumulation (hi + lo, |lo| <= ulp(hi)/2) of non-negative

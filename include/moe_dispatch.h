@@ -100,7 +100,12 @@ MOE_API const char* moe_status_string(int code);
  * 0 <= N (N = 0 launches nothing), 1 <= E <= 1024, E % 4 == 0 for the
  * vector path (any E works).
  * NaN logits are outside the contract (their position in the order is
- * unspecified).
+ * unspecified).  An expert may be masked by a logit of -infinity: its score
+ * is 0, so that it adds nothing to a sum and its weight is 0.  Softmax chooses
+ * it after every open expert, lowest index first; sigmoid's key is then the
+ * bias alone.  Where the sum that divides is zero (softmax: every logit
+ * -infinity; sigmoid with renormalize: every chosen one) the row's weights are
+ * 0/0, NaN; so are those of a softmax row with a logit of +infinity.
  *
  * From 16384 tokens on, with E = 32*G (G = 4, 8 or 16) and K <= 8, sigmoid
  * scores with n_group 1 or G and K <= G, and renormalised softmax scores
