@@ -23,8 +23,8 @@
 // spills registers: right, but not tuned), and for many rows a ring of rows in
 // shared memory.
 // Measured (GB300, copy rate 6.80 TB/s): forward with a gate a token and the 8-bit
-// output at 8192 x 7168, 93 us, 5.7 TB/s (a block a row: 124 us); with fp32 sums and a gate
-// an element at 16384 x 4096, 142 us, 6.6 TB/s; backward at 16384 x 4096 with
+// output at 8192 x 7168, 95 us, 5.6 TB/s (a block a row: 124 us); with fp32 sums and a gate
+// an element at 16384 x 4096, 144 us, 6.5 TB/s; backward at 16384 x 4096 with
 // fp32 sums 200 us, 6.0 TB/s (a block a row: 234), at 8192 x 7168 with a gate an element
 // 158 us, 5.9 TB/s (282).
 #include "norm_parts.cuh"
@@ -332,6 +332,13 @@ __device__ __forceinline__ float2 sum_and_max(float v, float m, float (*buf)[32]
     return make_float2(v, m);
 }
 
+// The least product s * w * 2^32 of a row whose largest |v| is taken from it: it is a normal number with room to
+// spare.  Where the largest is below, or infinite (a weight of 2^96, or both large), the row's threads, which hold the
+// same value, take the maximum of |v| itself; of ordinary rows only those of zeros.  (The way out costs 8192 x 7168
+// 2.5%, 94.8 us against 92.5: other registers and order, not the test.  The power of two by the block's weights, or a
+// loop of its own for large ones, cost 6%.)
+constexpr float kLeastProduct = 0x1p-58f;
+
 // A row's place holds its columns rounded up to whole warps'.
 __host__ __device__ __forceinline__ int ring_columns(int H) { return (H + 255) / 256 * 256; }
 
@@ -390,8 +397,7 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_ring_kernel(const Blo
         Pair q[4], g[4];
         read(mine, reinterpret_cast<const R*>(x + kNarrow * W), q);
         if constexpr (GATE == kFullGate) read(mine, x + W, g);
-        // The row's largest |v| comes with its sum: of s * w, scaled up so that what is below the normal numbers
-        // keeps its digits (a row whose s * w * 2^32 overflows has a weight above 2^24, or its squares do too).
+        // The row's largest |v| comes with its sum, as that of s * w * 2^32 (kLeastProduct).
         float amax = 0.f;
         sum = both(0.f);
 #pragma unroll
@@ -416,7 +422,14 @@ __global__ void __launch_bounds__(kRingThreads) block_norm_ring_kernel(const Blo
         join(s, f);
         mine.write(a.y + at, f);
         if (a.q == nullptr) continue;
-        const Quantum quantum = quantum_of(joined.y * root * 0x1p-32f);
+        amax = joined.y * 0x1p-32f * root;
+        if (!(joined.y >= kLeastProduct && joined.y < INFINITY)) {
+            amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
+            amax = row_reduce<false, true>(amax, buf[row & 1][0]);
+        }
+        const Quantum quantum = quantum_of(amax);
         if (threadIdx.x == 0) a.q_scale[row] = quantum.scale;
         mine.write(a.q + at, quantum, f);
     }
