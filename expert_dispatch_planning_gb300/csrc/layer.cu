@@ -781,6 +781,14 @@ namespace {
 using namespace moe_host;
 using moe::LayerArgs;
 
+// Blocks of these kernels that the GPU holds at once: two an SM by their threads and registers, one where the lists of
+// many experts and pairs leave no room for two.  Grids have no more, as the rest would run after them, in a second wave
+// (64 tokens, 8 of 384 experts of 2048 x 512: 357 us with two an SM, 345 with one; 8 tokens, 8 of 512: 80 and 75).
+int resident_blocks(size_t smem) {
+    constexpr size_t kOfAnSm = 228 * 1024, kOfTheSystem = 1024;  // of every block
+    return num_sms() * (2 * (smem + kOfTheSystem) <= kOfAnSm ? 2 : 1);
+}
+
 template <bool Q, bool DOWN, int EIGHTS>
 int launch_rows(const LayerArgs& a, cudaStream_t stream) {
     const size_t smem = moe::kLayerWarps * (moe::TileRing<DOWN>::kWarpBytes + sizeof(float4) * moe::kTiles * 32) +
@@ -788,7 +796,7 @@ int launch_rows(const LayerArgs& a, cudaStream_t stream) {
     if (cudaFuncSetAttribute(moe::layer_rows_kernel<Q, DOWN, EIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
-    const dim3 grid(static_cast<unsigned>(2 * num_sms())), block(moe::kLayerThreads);
+    const dim3 grid(static_cast<unsigned>(resident_blocks(smem))), block(moe::kLayerThreads);
     return launch(moe::layer_rows_kernel<Q, DOWN, EIGHTS>, grid, block, smem, stream, a);
 }
 
@@ -798,10 +806,10 @@ int launch_down(const LayerArgs& a, cudaStream_t stream) {
                         moe::Chosen::bytes(a.N, a.K, a.E);
     if (cudaFuncSetAttribute(moe::layer_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess)
         return MOE_ERR_CUDA;
-    // Two blocks an SM, all resident: with so many rows that blocks alone fill the GPU, equal parts
-    // of them; with fewer, as many blocks to a cluster as fit (a GPC's SMs are not all filled by clusters,
-    // and one left for a second wave costs more than SMs with one block).
-    const int slots = 2 * num_sms();
+    // With so many rows that blocks alone fill the GPU, equal parts of them (above kDownRows a block there are more
+    // blocks than the GPU holds); with fewer, as many blocks to a cluster as fit (a GPC's SMs are not all filled by
+    // clusters, and one left for a second wave costs more than SMs with one block).
+    const int slots = resident_blocks(smem);
     int rows = (a.H + slots - 1) / slots, blocks = 1;
     if (2 * rows <= moe::kDownRows) {
         rows = moe::kDownRows;
