@@ -779,12 +779,12 @@ int launch_backward(const moe::BlockNormBackwardArgs& a, bool f32, int gate, dim
 // two slots, 81% with four slots, 87% with four blocks; at 4096 columns of bf16 90% and 82%).  A third slot is for
 // blocks that are alone on their SM and small.
 struct BlockRing {
-    int slots = 0, threads = 0, blocks = 0;  // slots = 0: not taken
+    int slots = 0, threads = 0, blocks = 0;  // slots = 0: there is none
     size_t smem = 0;
 };
 constexpr int kMostBlocks = 8;  // of an SM
 constexpr size_t kForwardAhead = 36 * 1024, kBackwardAhead = 96 * 1024;
-BlockRing block_ring_for(int N, int H, int bytes, size_t ahead, int rows) {
+BlockRing block_ring_for(int H, int bytes, size_t ahead, int sms) {
     constexpr size_t kSmem = 220 * 1024;
     const size_t slot = static_cast<size_t>(moe::ring_columns(H)) * bytes;
     BlockRing r;
@@ -793,11 +793,9 @@ BlockRing block_ring_for(int N, int H, int bytes, size_t ahead, int rows) {
     int per_sm = moe::kRingThreads / threads;
     if (per_sm > kMostBlocks) per_sm = kMostBlocks;
     while (per_sm > 1 && (per_sm * slot > ahead || 2 * per_sm * slot > kSmem)) --per_sm;
-    const int blocks = num_sms() * per_sm;
-    if (N / rows < blocks) return r;
     r.slots = per_sm == 1 && 3 * slot <= kSmem && (slot <= kForwardAhead || threads <= moe::kRingThreads / 2) ? 3 : 2;
     r.threads = threads;
-    r.blocks = blocks;
+    r.blocks = sms * per_sm;
     r.smem = r.slots * slot;
     return r;
 }
@@ -829,11 +827,31 @@ int launch_backward_ring(const BlockRing& r, const moe::BlockNormBackwardArgs& a
     }
 }
 
+bool ring_taken(const BlockRing& r, int N, int rows) { return r.slots > 0 && N / rows >= r.blocks; }
+
+// The gradient's ring, by the bytes of a column of its rows, and the rows a block from which it is taken.
+BlockRing backward_ring(int H, int bytes, int sms) { return block_ring_for(H, bytes, kBackwardAhead, sms); }
+int backward_ring_rows(int H) { return H >= 2048 ? 1 : 4; }
+
 // Blocks of the backward kernel's other forms: four an SM, no more than there are rows.
-int backward_blocks(int N, int H) {
+int backward_blocks(int N, int H, int sms) {
     const int64_t units = H <= 512 ? (static_cast<int64_t>(N) + 3) / 4 : N;
-    const int64_t cap = static_cast<int64_t>(num_sms()) * 4;
+    const int64_t cap = static_cast<int64_t>(sms) * 4;
     return static_cast<int>(units < cap ? units : cap);
+}
+
+// For the most blocks of any call with these rows or fewer: a caller's workspace for its largest batch serves all.
+size_t backward_workspace(int N, int H, int sms) {
+    const int rows = backward_ring_rows(H);
+    int blocks = 1;
+    for (int bytes = 6; bytes <= 14; bytes += 2) {  // dy, x; sums of 2 or 4 bytes, twice with ds; a gate an element
+        const BlockRing ring = backward_ring(H, bytes, sms);
+        const bool taken = ring_taken(ring, N, rows);
+        const int others = backward_blocks(taken ? ring.blocks * rows - 1 : N, H, sms);
+        if (others > blocks) blocks = others;
+        if (taken && ring.blocks > blocks) blocks = ring.blocks;
+    }
+    return static_cast<size_t>(blocks) * 2 * H * sizeof(float);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -877,8 +895,9 @@ extern "C" MOE_API int moe_block_norm(const uint16_t* x, const void* residual, i
     const int rows = H > 2048 ? 4 : H >= 1024 && !f32 ? 16 : 0;
     // (the ring has no second sum for squares that vanish: only with an eps that covers them)
     if (eps >= moe::kLeastEps && rows > 0) {
-        const BlockRing ring = block_ring_for(N, H, 2 + (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0), kForwardAhead, rows);
-        if (ring.slots > 0)
+        const BlockRing ring = block_ring_for(H, 2 + (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0), kForwardAhead,
+                                              num_sms());
+        if (ring_taken(ring, N, rows))
             return f32 ? launch_forward_ring<float>(ring, a, kind, stream) : launch_forward_ring<uint16_t>(ring, a, kind, stream);
     }
     if (H <= 512) {
@@ -896,9 +915,7 @@ extern "C" MOE_API int moe_block_norm(const uint16_t* x, const void* residual, i
 
 extern "C" MOE_API size_t moe_block_norm_backward_workspace_size(int N, int H) {
     if (N < 0 || H < 8 || H % 8 != 0 || H > kMaxH) return 0;
-    int blocks = backward_blocks(N, H);  // the ring form may have more
-    if (N > blocks) blocks = N < kMostBlocks * num_sms() ? N : kMostBlocks * num_sms();
-    return static_cast<size_t>(blocks > 0 ? blocks : 1) * 2 * H * sizeof(float);
+    return backward_workspace(N, H, num_sms());
 }
 
 extern "C" MOE_API int moe_block_norm_backward(const uint16_t* dy, const uint16_t* x, const void* s, int s_dtype,
@@ -929,18 +946,20 @@ extern "C" MOE_API int moe_block_norm_backward(const uint16_t* dy, const uint16_
             return MOE_ERR_CUDA;
         return MOE_OK;
     }
-    if (workspace_bytes < moe_block_norm_backward_workspace_size(N, H)) return MOE_ERR_CAPACITY;
+    const int sms = num_sms();
+    if (workspace_bytes < backward_workspace(N, H, sms)) return MOE_ERR_CAPACITY;
     const bool f32 = s_dtype == MOE_DTYPE_F32;
-    const BlockRing ring = block_ring_for(N, H, 4 + (ds != nullptr ? 2 : 1) * (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0),
-                                          kBackwardAhead, H >= 2048 ? 1 : 4);
-    const int blocks = ring.slots > 0 ? ring.blocks : backward_blocks(N, H);
+    const BlockRing ring =
+        backward_ring(H, 4 + (ds != nullptr ? 2 : 1) * (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0), sms);
+    const bool taken = ring_taken(ring, N, backward_ring_rows(H));
+    const int blocks = taken ? ring.blocks : backward_blocks(N, H, sms);
     float* partial = static_cast<float*>(workspace);
     const moe::BlockNormBackwardArgs a = {dy, x, s, ds, gate, post_weight, weight, post_weight_dtype == MOE_DTYPE_F32,
                                           weight_dtype == MOE_DTYPE_F32, post_rstd, rstd, N, H, residual_scale, dx, dres,
                                           dgate, partial};
     const dim3 grid(static_cast<unsigned>(blocks));
     int rc;
-    if (ring.slots > 0) {
+    if (taken) {
         if (ds != nullptr)
             rc = f32 ? launch_backward_ring<float, true>(ring, a, kind, stream)
                      : launch_backward_ring<uint16_t, true>(ring, a, kind, stream);

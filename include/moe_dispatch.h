@@ -510,7 +510,8 @@ MOE_API int moe_block_norm(const uint16_t* x, const void* residual, int residual
  *   dpost_weight, (device) float32[H] out.  Summed in a fixed order.
  *   dweight
  *   workspace    (device) moe_block_norm_backward_workspace_size(N, H) bytes,
- *                16-byte aligned, no initialisation.
+ *                16-byte aligned, no initialisation.  What serves N rows
+ *                serves fewer.
  * Two launches.  N = 0 zeroes the weights' gradients.
  */
 MOE_API size_t moe_block_norm_backward_workspace_size(int N, int H);
