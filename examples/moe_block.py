@@ -5,8 +5,9 @@
 norm -> router -> plan -> permute -> experts -> combine, then the gradients of all
 of it: the combine's, the experts', the permute's (the combine with weights of
 one), the router's (a few torch operations on [tokens, K] values) and the norm's.
-Plain gradient steps on random data bring the loss down.  The decoding step is the
-norm and one call for the whole layer, with 8-bit rows and gate/up weights.
+Plain gradient steps on random data bring the loss down.  The decoding step, with
+8-bit rows and gate/up weights, is the norm and one call for the whole layer; more
+than moe.LAYER_MAX_TOKENS tokens go by the plan.
 """
 import argparse
 import os
@@ -72,9 +73,17 @@ class Block:
         return dx, dstream
 
     def decode(self, x, stream, w8, w8_scale):
-        """The forward pass of a few tokens with 8-bit rows and gate/up weights (w8 e4m3[E,2,I,H], w8_scale float32[E,2,I])."""
+        """The forward pass with 8-bit rows and gate/up weights (w8 e4m3[E,2,I,H], w8_scale float32[E,2,I])."""
         n = moe.residual_norm(x, self.norm, residual=stream, quantize=True)
-        return moe.layer(n.q, n.y.float() @ self.router.T, w8, self.w_down16, K, x_scale=n.q_scale, w_scale=w8_scale)
+        logits = n.y.float() @ self.router.T
+        if x.shape[0] <= moe.LAYER_MAX_TOKENS:
+            return moe.layer(n.q, logits, w8, self.w_down16, K, x_scale=n.q_scale, w_scale=w8_scale)
+        idx, w, plan = moe.route_plan(logits, K, R, ALIGN)
+        # two 8-bit values are one 16-bit element to the permute; the scales follow by the plan's indexes
+        qp = moe.permute(n.q.view(BF16), plan).view(torch.float8_e4m3fn)
+        scale = n.q_scale[(plan.src_of_slot.clamp(min=0) // K).long()].contiguous()
+        yp = moe.expert_ffn(qp, w8, self.w_down16, plan, x_scale=scale, w_scale=w8_scale)
+        return moe.combine(yp, w, plan)
 
 
 def quantize_channels(w):
