@@ -502,7 +502,8 @@ def layer(x: torch.Tensor, logits: torch.Tensor, w_gate_up: torch.Tensor, w_down
     Routing as in route_topk; x, weights and scales as in expert_ffn (bf16, or
     8-bit rows and gate/up weights with x_scale float32[N] and w_scale
     float32[E,2,I]).  topk_idx int32[N,K] and topk_w float32[N,K], if given,
-    get the router's choice.
+    get the router's choice.  Past about twelve tokens an expert on average
+    (N * K / E) route_plan, permute, expert_ffn and combine are faster.
     """
     r = _lib.binding().layer(x, logits, w_gate_up, w_down, K, SCORING[scoring], bool(renormalize), bias, n_group, topk_group,
                              routed_scaling, x_scale, w_scale, out, topk_idx, topk_w, _handle(stream))

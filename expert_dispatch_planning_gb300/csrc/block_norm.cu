@@ -21,7 +21,8 @@
 // Memory bound: every element is read once and written once.  Forms as in
 // norm.cu: a warp a row (H <= 512), a block a row (past 8192 columns the gradient
 // spills registers: right, but not tuned), and for many rows a ring of rows in
-// shared memory.
+// shared memory (which rows, and both sides' figures: forward_ring_rows,
+// backward_ring_rows).
 // Measured (GB300, copy rate 6.80 TB/s): forward with a gate a token and the 8-bit
 // output at 8192 x 7168, 95 us, 5.6 TB/s (a block a row: 124 us); with fp32 sums and a gate
 // an element at 16384 x 4096, 144 us, 6.5 TB/s; backward at 16384 x 4096 with
@@ -775,8 +776,10 @@ int launch_backward(const moe::BlockNormBackwardArgs& a, bool f32, int gate, dim
 // The ring form of these kernels, with `bytes` a column of a row in a slot.  A row has two sums one after the
 // other, in which a block only waits: so an SM has as many blocks as its threads (64 registers each) allow,
 // but not more than ask for `ahead` bytes at a time.  More than that in flight, by more blocks or more slots,
-// costs up to a fifth again (the forward kernel at 2048 fp32 columns: 94% of the copy rate with two blocks of
-// two slots, 81% with four slots, 87% with four blocks; at 4096 columns of bf16 90% and 82%).  A third slot is for
+// costs up to a sixth again, and less does too.  Share of the copy rate with half of `ahead`, this, and twice this:
+// forward, bf16 sums and a gate a token, 32000 x 2048 69, 87, 87%; 16384 x 4096 68, 85, 85%; fp32 sums and a gate an
+// element, 16384 x 4096 95, 95, 86%; gradient with bf16 sums 16384 x 4096 51, 90, 90%, with a gate an element
+// 8192 x 7168 90, 90, 78%; with fp32 sums 32000 x 2048 71, 95, 95%, 16384 x 4096 94, 88, 88%.  A third slot is for
 // blocks that are alone on their SM and small.
 struct BlockRing {
     int slots = 0, threads = 0, blocks = 0;  // slots = 0: there is none
@@ -829,8 +832,21 @@ int launch_backward_ring(const BlockRing& r, const moe::BlockNormBackwardArgs& a
 
 bool ring_taken(const BlockRing& r, int N, int rows) { return r.slots > 0 && N / rows >= r.blocks; }
 
+// Rows a block from which the forward kernel takes the ring; 0: never.  Wide rows after a few (block a row, ring, us:
+// 7168 bf16 620 rows 10.6, 10.9, 2600 rows 39.9, 32.5, with a gate an element 63.1, 35.6; 4096 bf16 1300 rows 10.9, 11.6,
+// 5000 rows 37.8, 32.8; 4096 fp32 with a gate an element 14.8, 15.6 and 53.7, 47.0), bf16 rows of 1024 to 2048 columns
+// later (1024: 10000 rows 15.3, 17.8, 40000 rows 58.6, 56.4; 2048: 5000 rows 15.9, 18.4, 32000 rows 95.5, 88.9), fp32 rows
+// up to there and narrower ones never (2048 fp32 32000 rows 137, 145; 640 bf16 65536 rows 70, 86).  Where the rule is off:
+// bf16 rows of 1024 to 2048 columns with a gate an element (32000 x 2048 110, 118) and fp32 rows of 2056 to 4096 without
+// one (20000 x 2056 83, 107; 16384 x 4096 123, 134).
+int forward_ring_rows(int H, bool f32) { return H > 2048 ? 4 : H >= 1024 && !f32 ? 16 : 0; }
+
 // The gradient's ring, by the bytes of a column of its rows, and the rows a block from which it is taken.
 BlockRing backward_ring(int H, int bytes, int sms) { return block_ring_for(H, bytes, kBackwardAhead, sms); }
+// Wide rows take it as soon as every block has one (block a row, ring, us: 7168 bf16 160 rows 15.4, 12.6, 8192 rows
+// 219, 121; 2048 bf16 1300 rows 16.9, 14.3, 32000 rows 207, 132); narrow ones after four (1000 bf16 1300 rows 11.9, 13.7,
+// 5000 rows 22.5, 21.5, 65536 rows 211, 140, fp32 with a gate a token 24.3, 25.8 and 230, 188; 640 bf16 65536 rows 177,
+// 118).
 int backward_ring_rows(int H) { return H >= 2048 ? 1 : 4; }
 
 // Blocks of the backward kernel's other forms: four an SM, no more than there are rows.
@@ -892,7 +908,7 @@ extern "C" MOE_API int moe_block_norm(const uint16_t* x, const void* residual, i
     const moe::BlockNormArgs a = {x, residual, gate, post_weight, weight, post_weight_dtype == MOE_DTYPE_F32,
                                   weight_dtype == MOE_DTYPE_F32, N, H, residual_scale, eps, down, mean, y,
                                   residual_out, post_rstd, rstd, q, q_scale};
-    const int rows = H > 2048 ? 4 : H >= 1024 && !f32 ? 16 : 0;
+    const int rows = forward_ring_rows(H, f32);
     // (the ring has no second sum for squares that vanish: only with an eps that covers them)
     if (eps >= moe::kLeastEps && rows > 0) {
         const BlockRing ring = block_ring_for(H, 2 + (f32 ? 4 : 2) + (kind == moe::kFullGate ? 2 : 0), kForwardAhead,

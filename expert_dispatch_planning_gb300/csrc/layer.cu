@@ -9,11 +9,13 @@
 // from memory once, through rings in shared memory that each warp fills and
 // reads by itself, and everything else hides behind them.
 //
-// Measured (GB300, copy rate 6.80 TB/s): 61 tokens, 64 experts of 4096 x 1280,
-// 321 us, 6.3 TB/s (the same streams without any products: 330, before weights
-// were the first to leave L2); three tokens, 24 experts of 7168 x 1024 in 8 bits, 111 us,
-// 6.2 TB/s.  One token, 8 experts of 2048 x 768: 23 us of which the weights
-// take 11; the rest is the launches' starts and ends, one after the other.
+// Measured (GB300, copy rate 6.80 TB/s; from run to run): 61 tokens, 64 experts of
+// 4096 x 1280, 321 to 328 us, 6.1 to 6.3 TB/s; three tokens, 24 experts of 7168 x 1024
+// in 8 bits, 109 to 115 us, 6.0 to 6.3 TB/s.  One token, 8 experts of 2048 x 768: 23 us
+// of which the weights take 11; the rest is the launches' starts and ends, one after the
+// other.  Narrow experts are further off: k is dealt to a block's warps anew for each
+// tile, so that with fewer than eight steps of 128 bytes some load nothing (17 tokens, 60
+// experts of 1000 x 712: 1.6 times the weights' time; 64 tokens, 64 of 2048 x 96: 4.3).
 //
 // Launches: the router's, gate/up, down; for more than eight tokens the down product's
 // parts are summed by a fourth.  Each block finds the chosen experts and their tokens by
@@ -37,7 +39,7 @@ namespace moe {
 constexpr int kLayerThreads = 256;
 constexpr int kLayerWarps = kLayerThreads / 32;
 // At most, in layer_down_kernel, whose sums are [warps][rows][N].  (By tiles of rows and a sum, as for more tokens, the
-// layer takes 28.9 us for one token and 95.7 for eight, of 128 experts of 2048 x 768; so 23.5 and 86.7.)
+// layer takes 29.3 us for one token and 95 for eight, of 128 experts of 2048 x 768; so 23.7 and 85.5.)
 constexpr int kDownTokens = 8;
 
 struct LayerArgs {
@@ -293,7 +295,7 @@ struct WeightRing {
     }
     // The step at byte `k` of the rows; zeros behind a row's end (`bytes`) and for rows that are not there.
     // What is not read `again` is the first to leave L2, before tokens, h and the kernels' code
-    // (layer_batch 329 -> 321 us).
+    // (61 tokens, 64 experts of 4096 x 1280: 327 us, 338 without; the 8-bit case of the header 108 to 113, 117 to 121).
     __device__ __forceinline__ void fetch(const WeightRows& w, int k, int bytes, bool again) {
         const int r = (threadIdx.x & 31) >> 3, mine = k + static_cast<int>(threadIdx.x & 7) * 16;
         const uint8_t* first = w.lane + k;
@@ -664,7 +666,8 @@ __device__ __forceinline__ void store_first(float* p, float v) {
 }
 
 // A cluster has `rows` rows of the output, at most kDownRows; all warps of its blocks share the
-// chosen experts' k.
+// chosen experts' k.  (Where a token's sum is cut so depends on how many experts all tokens chose: its
+// last bits may change with the others.  layer_rows_kernel's do not.)
 __global__ void __launch_bounds__(kLayerThreads, 2) layer_down_kernel(const LayerArgs a, int rows) {
     extern __shared__ __align__(128) uint8_t smem[];
     DownRing ring(smem);

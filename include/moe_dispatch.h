@@ -621,6 +621,11 @@ MOE_API int moe_combine_backward(const uint16_t* dout, const uint16_t* y, const 
  * combine serve those).  H % 8 == 0 (H % 16 == 0 with e4m3), I % 8 == 0, H and I < 2^20;
  * 16-byte aligned arrays.  Three launches, four for more than eight tokens; N = 0
  * launches nothing.
+ * The same inputs give the same bits.  With more than eight tokens a token's output
+ * does not depend on the other tokens; with up to eight its last bits may, by how
+ * many experts they choose.  Up to about twelve tokens an expert on average
+ * (N * K / E) this is the faster way; with more, experts of more than 16 tokens take
+ * a second pass over their weights, and the plan's calls are.
  */
 #define MOE_LAYER_MAX_TOKENS 64
 MOE_API size_t moe_layer_workspace_size(int N, int K, int H, int I);

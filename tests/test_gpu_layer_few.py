@@ -102,6 +102,24 @@ def test_gates_of_every_size(m):
     assert_within(got, want, fp32 + 2 * U * (want.abs() + fp32), "out")
 
 
+@pytest.mark.parametrize("N", [9, 16, 33, 64])
+@pytest.mark.parametrize("bits", [16, 8])
+def test_more_than_eight_tokens_are_independent(m, N, bits):
+    """A token's output has the same bits whatever the other tokens hold and choose."""
+    E, K, H, I = 24, 3, 272, 136  # noqa: E741
+    a, b = inputs(N, E, H, I, bits=bits, seed=1), inputs(N, E, H, I, bits=bits, seed=2)
+    a["w_gate_up"], a["w_down"] = b["w_gate_up"], b["w_down"]
+    keep = N // 2
+    b["logits"][keep] = a["logits"][keep]
+    b["x"].view(torch.uint8)[keep] = a["x"].view(torch.uint8)[keep]
+    if bits == 8:
+        a["w_scale"] = b["w_scale"]
+        b["x_scale"][keep] = a["x_scale"][keep]
+    b["logits"][:keep, 5] += 30     # an expert with many tokens
+    x, y = m.layer(K=K, **a), m.layer(K=K, **b)
+    assert torch.equal(x[keep], y[keep]) and not torch.equal(x, y)
+
+
 def guarded(nbytes, around=4096):
     """(buffer, address of `nbytes` in it); the rest holds 0xA5."""
     t = torch.full((nbytes + 2 * around,), 0xA5, dtype=torch.uint8, device="cuda")
